@@ -14,6 +14,9 @@ import os
 
 import torch  # loads the HIP runtime the library must share with torch
 
+from . import encoder
+from .encoder import GradSet, clip_grads, embed, embed_grad, layer_norm, layer_norm_grad
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # ERSJ_LIBRARY selects another build of the same library (for example the
 # host-sanitized one that exact_range_similarity_amd.build makes on request)
@@ -150,6 +153,7 @@ def lib():
               "ersj_batch_info",
               "ersj_get_stats"):
         getattr(L, f).restype = ctypes.c_int
+    encoder.declare(L)
     _lib = L
     return L
 

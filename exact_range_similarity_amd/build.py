@@ -20,7 +20,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 SOURCES = ["k_index.hip", "k_refine.hip", "k_refine_mfma.hip", "k_refine_m16.hip", "k_refine_g16.hip", "k_expand.hip", "k_knn.hip", "k_scratch.hip",
-           "ersj_api.cpp"]
+           "k_embed.hip", "k_norm.hip", "k_clip.hip", "ersj_api.cpp", "ersj_encoder.cpp"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-I", INCLUDE, "-I", CSRC,
           "-Wall", "-Wno-unused-result", "-Wno-unused-command-line-argument"]
@@ -76,13 +76,15 @@ def build_sanitized(verbose: bool = False) -> str:
     objs = [os.path.join(OBJ, os.path.splitext(s)[0] + ".o") for s in SOURCES if s.endswith(".hip")]
     if not all(os.path.exists(o) for o in objs):
         build(verbose)
-    api = os.path.join(OBJ, "ersj_api_san.o")
-    cmd = [HIPCC, *COMMON, *SAN_FLAGS, "-c", os.path.join(CSRC, "ersj_api.cpp"), "-o", api]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+    for src in (s for s in SOURCES if s.endswith(".cpp")):
+        out = os.path.join(OBJ, os.path.splitext(src)[0] + "_san.o")
+        cmd = [HIPCC, *COMMON, *SAN_FLAGS, "-c", os.path.join(CSRC, src), "-o", out]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+        objs.append(out)
     cmd = [HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", "-shared-libsan", "-Xarch_host",
-           "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined", *objs, api, "-o", SAN_LIB]
+           "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined", *objs, "-o", SAN_LIB]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)

@@ -277,6 +277,16 @@ size_t pool_cached(int dev)
     return pool_of(dev).cached;
 }
 
+}  // namespace
+
+namespace ersj {
+int set_error(int code, const char *msg) { return fail(code, "%s", msg); }
+hipError_t device_block_get(int dev, size_t bytes, void **out) { return pool_get(dev, pool_round(bytes), out); }
+void device_block_put(int dev, void *p, size_t bytes) { pool_put(dev, p, pool_round(bytes)); }
+}  // namespace ersj
+
+namespace {
+
 template <typename T>
 int dalloc(ersj_index *h, T **p, size_t count, const char *what)
 {

@@ -1,0 +1,270 @@
+// C ABI of the encoder operators (see include/ersj_encoder.h): argument
+// validation, and the chunk table of a set of gradients.
+#include "ersj_encoder.h"
+#include "encoder_internal.h"
+
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <new>
+#include <vector>
+
+using namespace ersj;
+
+static_assert(ERSJ_F32 == kF32 && ERSJ_F16 == kF16 && ERSJ_BF16 == kBF16, "element types");
+static_assert(kGradParts * sizeof(double) == ERSJ_GRADS_WORK, "working memory of ersj_grads_clip");
+
+struct ersj_grads {
+    int device = 0;
+    GradChunk *chunks = nullptr;  // device
+    uint32_t n_chunks = 0;
+    size_t bytes = 0;
+};
+
+namespace {
+
+int refuse(const char *fmt, ...)
+{
+    char buf[256];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return set_error(ERSJ_ERR_INVALID_ARG, buf);
+}
+
+int done(hipError_t e, const char *what)
+{
+    if (e == hipSuccess) return ERSJ_OK;
+    (void)hipGetLastError();
+    char buf[256];
+    snprintf(buf, sizeof buf, "%s: %s", what, hipGetErrorString(e));
+    return set_error(e == hipErrorOutOfMemory ? ERSJ_ERR_OOM : ERSJ_ERR_HIP, buf);
+}
+
+bool is_type(int32_t t) { return t == ERSJ_F32 || t == ERSJ_F16 || t == ERSJ_BF16; }
+
+bool aligned(const void *p, size_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
+
+constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1;
+
+int check_rows(int64_t n, int32_t dim)
+{
+    if (n < 0 || n > kMaxRows) return refuse("n = %lld: must be in [0, 2^31)", (long long)n);
+    if (dim < 1 || dim > ERSJ_ENCODER_MAX_DIM)
+        return refuse("dim = %d: must be in [1, %d]", dim, ERSJ_ENCODER_MAX_DIM);
+    return ERSJ_OK;
+}
+
+int check_tensor(const void *p, int32_t type, int64_t ld, int32_t dim, bool used, const char *what)
+{
+    if (!is_type(type)) return refuse("%s: unknown element type %d", what, type);
+    if (ld < dim) return refuse("%s: row spacing %lld is below dim = %d", what, (long long)ld, dim);
+    if (ld > (int64_t)1 << 40) return refuse("%s: row spacing %lld is out of range", what, (long long)ld);
+    if (used && !p) return refuse("%s is NULL", what);
+    if (!aligned(p, elem_size(type))) return refuse("%s is not aligned to its element size", what);
+    return ERSJ_OK;
+}
+
+int check_ids(const void *ids, int32_t type, int64_t n, int64_t rows)
+{
+    if (type != ERSJ_I32 && type != ERSJ_I64) return refuse("ids: unknown id type %d", type);
+    if (n > 0 && !ids) return refuse("ids is NULL");
+    if (!aligned(ids, type == ERSJ_I64 ? 8 : 4)) return refuse("ids is not aligned to its element size");
+    if (rows < 1 || rows >= kMaxRows) return refuse("rows = %lld: must be in [1, 2^31 - 1)", (long long)rows);
+    return ERSJ_OK;
+}
+
+int check_work(const void *work, uint64_t have, uint64_t need, size_t align)
+{
+    if (have < need)
+        return refuse("working memory of %llu bytes, %llu are needed", (unsigned long long)have,
+                      (unsigned long long)need);
+    if (need && !work) return refuse("d_work is NULL");
+    if (!aligned(work, align)) return refuse("d_work is not aligned to %zu bytes", align);
+    return ERSJ_OK;
+}
+
+#define TRY(expr)                       \
+    do {                                \
+        int r__ = (expr);               \
+        if (r__ != ERSJ_OK) return r__; \
+    } while (0)
+
+}  // namespace
+
+extern "C" {
+
+int ersj_embed(const void *d_table, int32_t table_type, int64_t rows, int32_t dim, int64_t ld_table,
+               const void *d_ids, int32_t id_type, int64_t n, float scale, int64_t padding_id, void *d_out,
+               int32_t out_type, int64_t ld_out, void *stream)
+{
+    TRY(check_rows(n, dim));
+    TRY(check_tensor(d_table, table_type, ld_table, dim, true, "table"));
+    TRY(check_ids(d_ids, id_type, n, rows));
+    TRY(check_tensor(d_out, out_type, ld_out, dim, n > 0, "out"));
+    if (table_type != ERSJ_F32 && out_type != table_type)
+        return refuse("out: a table of 16 bits gives rows of its own type");
+    if (padding_id < -1) return refuse("padding_id = %lld: must be an id or -1", (long long)padding_id);
+    const EmbedArgs a{d_table, table_type, rows, ld_table, dim, d_ids, id_type, n, scale, padding_id, d_out, out_type,
+                      ld_out};
+    return done(launch_embed(a, (hipStream_t)stream), "embed kernel");
+}
+
+uint64_t ersj_embed_grad_work(int64_t n, int64_t rows, int32_t dim)
+{
+    if (n < 0 || n > kMaxRows || rows < 1 || rows >= kMaxRows || dim < 1 || dim > ERSJ_ENCODER_MAX_DIM) return 0;
+    return embed_grad_work(n, rows, dim);
+}
+
+int ersj_embed_grad(const void *d_grad, int32_t grad_type, int64_t ld_grad, const void *d_ids, int32_t id_type,
+                    int64_t n, float scale, int64_t padding_id, void *d_out, int32_t out_type, int64_t rows,
+                    int32_t dim, int64_t ld_out, int32_t accumulate, void *d_work, uint64_t d_work_bytes,
+                    void *stream)
+{
+    TRY(check_rows(n, dim));
+    TRY(check_tensor(d_grad, grad_type, ld_grad, dim, n > 0, "grad"));
+    TRY(check_ids(d_ids, id_type, n, rows));
+    TRY(check_tensor(d_out, out_type, ld_out, dim, true, "out"));
+    if (out_type != ERSJ_F32 && out_type != grad_type)
+        return refuse("out: must have the type of grad or 32 bits");
+    if (padding_id < -1) return refuse("padding_id = %lld: must be an id or -1", (long long)padding_id);
+    TRY(check_work(d_work, d_work_bytes, embed_grad_work(n, rows, dim), 256));
+    const EmbedGradArgs a{d_grad, grad_type, ld_grad, d_ids, id_type, n, scale, padding_id, d_out, out_type, rows,
+                          dim, ld_out, accumulate, d_work};
+    return done(launch_embed_grad(a, (hipStream_t)stream), "embed gradient kernels");
+}
+
+int ersj_layer_norm(const void *d_x, int32_t type, int64_t n, int32_t dim, int64_t ld_x, const void *d_weight,
+                    const void *d_bias, int32_t param_type, float eps, void *d_y, int64_t ld_y, float *d_mean,
+                    float *d_rstd, void *stream)
+{
+    TRY(check_rows(n, dim));
+    TRY(check_tensor(d_x, type, ld_x, dim, n > 0, "x"));
+    TRY(check_tensor(d_y, type, ld_y, dim, n > 0, "y"));
+    TRY(check_tensor(d_weight, param_type, dim, dim, false, "weight"));
+    TRY(check_tensor(d_bias, param_type, dim, dim, false, "bias"));
+    if (param_type != ERSJ_F32 && param_type != type)
+        return refuse("weight and bias must have the type of x or 32 bits");
+    if (!(eps >= 0.f) || std::isinf(eps)) return refuse("eps = %g: must be finite and not negative", (double)eps);
+    if (d_y == d_x && ld_y != ld_x) return refuse("y: in place, its row spacing must be that of x");
+    if (!aligned(d_mean, 4) || !aligned(d_rstd, 4)) return refuse("mean and rstd must be aligned to 4 bytes");
+    const NormArgs a{d_x, type, n, dim, ld_x, d_weight, d_bias, param_type, eps, d_y, ld_y, d_mean, d_rstd};
+    return done(launch_layer_norm(a, (hipStream_t)stream), "layer norm kernel");
+}
+
+uint64_t ersj_layer_norm_grad_work(int64_t n, int32_t dim)
+{
+    if (n < 0 || n > kMaxRows || dim < 1 || dim > ERSJ_ENCODER_MAX_DIM) return 0;
+    return layer_norm_grad_work(n, dim);
+}
+
+int ersj_layer_norm_grad(const void *d_grad_y, int64_t ld_grad_y, const void *d_x, int64_t ld_x, int32_t type,
+                         int64_t n, int32_t dim, const float *d_mean, const float *d_rstd, const void *d_weight,
+                         int32_t param_type, void *d_grad_x, int64_t ld_grad_x, void *d_grad_weight,
+                         void *d_grad_bias, void *d_work, uint64_t d_work_bytes, void *stream)
+{
+    TRY(check_rows(n, dim));
+    TRY(check_tensor(d_grad_y, type, ld_grad_y, dim, n > 0, "grad_y"));
+    TRY(check_tensor(d_x, type, ld_x, dim, n > 0, "x"));
+    TRY(check_tensor(d_grad_x, type, ld_grad_x, dim, false, "grad_x"));
+    TRY(check_tensor(d_weight, param_type, dim, dim, false, "weight"));
+    TRY(check_tensor(d_grad_weight, param_type, dim, dim, false, "grad_weight"));
+    TRY(check_tensor(d_grad_bias, param_type, dim, dim, false, "grad_bias"));
+    if (param_type != ERSJ_F32 && param_type != type)
+        return refuse("weight and its gradients must have the type of x or 32 bits");
+    if (n > 0 && (!d_mean || !d_rstd)) return refuse("mean or rstd is NULL");
+    if (!aligned(d_mean, 4) || !aligned(d_rstd, 4)) return refuse("mean and rstd must be aligned to 4 bytes");
+    if ((d_grad_x == d_grad_y && ld_grad_x != ld_grad_y && d_grad_x) ||
+        (d_grad_x == d_x && ld_grad_x != ld_x && d_grad_x))
+        return refuse("grad_x: in place, its row spacing must be that of the tensor it replaces");
+    if (d_grad_weight || d_grad_bias) TRY(check_work(d_work, d_work_bytes, layer_norm_grad_work(n, dim), 256));
+    const NormGradArgs a{d_grad_y, ld_grad_y, d_x, ld_x, type, n, dim, d_mean, d_rstd, d_weight, param_type,
+                         d_grad_x, ld_grad_x, d_grad_weight, d_grad_bias, d_work};
+    return done(launch_layer_norm_grad(a, (hipStream_t)stream), "layer norm gradient kernels");
+}
+
+int ersj_grads_create(int32_t count, const void *const *d_grad, void *const *d_out, const int64_t *size,
+                      const int32_t *type, void *stream, ersj_grads **out)
+{
+    if (!out) return refuse("out is NULL");
+    *out = nullptr;
+    if (count < 1 || count > 65536) return refuse("count = %d: must be in [1, 65536]", count);
+    if (!d_grad || !size || !type) return refuse("d_grad, size or type is NULL");
+    uint64_t total = 0;
+    for (int32_t i = 0; i < count; ++i) {
+        if (!is_type(type[i])) return refuse("tensor %d: unknown element type %d", i, type[i]);
+        if (size[i] < 0 || size[i] > (int64_t)1 << 40)
+            return refuse("tensor %d: size %lld is out of range", i, (long long)size[i]);
+        if (size[i] == 0) continue;
+        if (!d_grad[i] || (d_out && !d_out[i])) return refuse("tensor %d is NULL", i);
+        if (!aligned(d_grad[i], elem_size(type[i])) || (d_out && !aligned(d_out[i], elem_size(type[i]))))
+            return refuse("tensor %d is not aligned to its element size", i);
+        const uint64_t step = kGradChunkBytes / elem_size(type[i]);
+        total += ((uint64_t)size[i] + step - 1) / step;
+    }
+    // half a terabyte, more than the memory of any one device
+    if (total > ((uint64_t)1 << 24)) return refuse("the tensors hold too many elements");
+    try {
+        std::vector<GradChunk> table;
+        table.reserve(total);
+        for (int32_t i = 0; i < count; ++i) {
+            const size_t es = elem_size(type[i]);
+            const int64_t step = kGradChunkBytes / es;
+            for (int64_t k = 0; k < size[i]; k += step) {
+                GradChunk c{};
+                c.in = (const char *)d_grad[i] + k * es;
+                c.out = d_out ? (char *)d_out[i] + k * es : (char *)const_cast<void *>(d_grad[i]) + k * es;
+                c.count = (uint32_t)(size[i] - k < step ? size[i] - k : step);
+                c.type = type[i];
+                table.push_back(c);
+            }
+        }
+        ersj_grads *h = new ersj_grads;
+        h->n_chunks = (uint32_t)total;
+        h->bytes = total * sizeof(GradChunk);
+        int r = ERSJ_OK;
+        if (total) {
+            r = done(hipGetDevice(&h->device), "hipGetDevice");
+            if (r == ERSJ_OK) {
+                void *p = nullptr;
+                r = done(device_block_get(h->device, h->bytes, &p), "table of a set of gradients");
+                h->chunks = (GradChunk *)p;
+            }
+            if (r == ERSJ_OK)
+                r = done(hipMemcpyAsync(h->chunks, table.data(), h->bytes, hipMemcpyHostToDevice,
+                                        (hipStream_t)stream), "copy");
+            if (r == ERSJ_OK) r = done(hipStreamSynchronize((hipStream_t)stream), "copy");
+        }
+        if (r != ERSJ_OK) {
+            ersj_grads_free(h);
+            return r;
+        }
+        *out = h;
+        return ERSJ_OK;
+    } catch (const std::bad_alloc &) {
+        return set_error(ERSJ_ERR_OOM, "host memory for the table of a set of gradients");
+    }
+}
+
+int ersj_grads_clip(const ersj_grads *h, float max_norm, float *d_norm, void *d_work, uint64_t d_work_bytes,
+                    void *stream)
+{
+    if (!h) return refuse("handle is NULL");
+    if (!(max_norm >= 0.f)) return refuse("max_norm = %g: must not be negative", (double)max_norm);
+    if (!aligned(d_norm, 4)) return refuse("d_norm is not aligned to 4 bytes");
+    TRY(check_work(d_work, d_work_bytes, ERSJ_GRADS_WORK, 8));
+    return done(launch_grads_clip(h->chunks, h->n_chunks, max_norm, d_norm, d_work, (hipStream_t)stream),
+                "gradient clipping kernels");
+}
+
+void ersj_grads_free(ersj_grads *h)
+{
+    if (!h) return;
+    if (h->chunks) device_block_put(h->device, h->chunks, h->bytes);
+    delete h;
+}
+
+}  // extern "C"
