@@ -6,6 +6,7 @@ namespace ersj {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
 
 template <typename I>
 __device__ __forceinline__ int64_t id_at(const void *ids, int64_t t)
@@ -32,17 +33,23 @@ __global__ __launch_bounds__(kThreads) void k_embed(EmbedArgs a)
 // ---- sort of the tokens by id -------------------------------------------
 //
 // Stable least-significant-digit radix sort of (key, t), key = id or `rows`
-// for tokens that add nothing.  A workgroup counts the digits of its kSortRun
-// consecutive entries; the scatter kernel derives its own offsets from the
-// table of all counts.
+// for tokens that add nothing.  A workgroup takes a run of consecutive
+// entries: one kernel counts the run's digits, the next ranks and moves its
+// entries.  With few runs the second kernel derives its own offsets from the
+// counts of all runs; with more, a scan kernel lies between.  Tokens that fit
+// one workgroup are sorted by it in one kernel, through LDS.
 
-constexpr int kSortRun = 4096;
-constexpr int kSortItems = kSortRun / kThreads;
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kMaxDigitBits = 9;
-constexpr int kWaves = kThreads / 64;
+constexpr int kMaxDigits = 1 << kMaxDigitBits;
+constexpr int kScanRuns = 64;       // more runs than this are scanned by a kernel of their own
+constexpr int kLocalItems = 4;      // entries per thread of the one-workgroup sort
+constexpr int kLocalMax = kSortThreads * kLocalItems;
 
 struct SortPlan {
     int passes, bits;
+    int items;  // per thread
     int64_t runs;
 };
 
@@ -53,7 +60,9 @@ SortPlan sort_plan(int64_t n, int64_t rows)
     SortPlan p;
     p.passes = (kb + kMaxDigitBits - 1) / kMaxDigitBits;
     p.bits = (kb + p.passes - 1) / p.passes;
-    p.runs = (n + kSortRun - 1) / kSortRun;
+    p.items = n <= (int64_t)1 << 18 ? 4 : 8;
+    const int64_t run = (int64_t)p.items * kSortThreads;
+    p.runs = (n + run - 1) / run;
     return p;
 }
 
@@ -73,94 +82,224 @@ __device__ __forceinline__ uint32_t sort_key(const SortSource &s, uint32_t i)
 }
 
 template <typename I>
-__global__ __launch_bounds__(kThreads) void k_sort_count(SortSource s, int shift, int bits, uint32_t *counts)
+__global__ __launch_bounds__(kSortThreads) void k_sort_count(SortSource s, int shift, int bits, uint32_t run,
+                                                             uint32_t *counts)
 {
-    __shared__ uint32_t cnt[1 << kMaxDigitBits];
+    __shared__ uint32_t cnt[kMaxDigits];
     const int nd = 1 << bits;
-    for (int k = threadIdx.x; k < nd; k += kThreads) cnt[k] = 0;
+    if ((int)threadIdx.x < nd) cnt[threadIdx.x] = 0;
     __syncthreads();
-    const uint32_t i0 = blockIdx.x * kSortRun;
-    for (uint32_t i = i0 + threadIdx.x; i < i0 + kSortRun && i < s.n; i += kThreads)
+    const uint64_t i0 = (uint64_t)blockIdx.x * run;
+    const uint32_t i1 = (uint32_t)(i0 + run < s.n ? i0 + run : s.n);
+    for (uint32_t i = (uint32_t)i0 + threadIdx.x; i < i1; i += kSortThreads)
         atomicAdd(&cnt[(sort_key<I>(s, i) >> shift) & (nd - 1)], 1u);
     __syncthreads();
-    for (int k = threadIdx.x; k < nd; k += kThreads) counts[(size_t)blockIdx.x * nd + k] = cnt[k];
+    if ((int)threadIdx.x < nd) counts[(size_t)blockIdx.x * nd + threadIdx.x] = cnt[threadIdx.x];
 }
 
-template <typename I>
-__global__ __launch_bounds__(kThreads) void k_sort_scatter(SortSource s, int shift, int bits, uint32_t *counts,
-                                                           uint32_t *keys_out, uint32_t *pos_out)
+// Each digit's counts over the runs become their exclusive prefix; the total
+// goes to row `runs`.  One wave per digit.
+__global__ __launch_bounds__(kThreads) void k_sort_scan(uint32_t *counts, uint32_t runs, int bits)
 {
-    __shared__ uint32_t base[1 << kMaxDigitBits];
-    __shared__ uint32_t cnt[kWaves][1 << kMaxDigitBits];
-    __shared__ uint32_t wsum[kWaves];
-    const int nd = 1 << bits, tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-    for (int k = tid; k < kWaves * nd; k += kThreads) cnt[k / nd][k % nd] = 0;
-
-    // offsets: all smaller digits, then the same digit in earlier runs
+    const int lane = threadIdx.x & 63;
+    const uint32_t nd = 1u << bits, k = blockIdx.x * kWaves + (threadIdx.x >> 6);
+    if (k >= nd) return;
     uint32_t carry = 0;
-    for (int k0 = 0; k0 < nd; k0 += kThreads) {
-        const int k = k0 + tid;
-        uint32_t total = 0, before = 0;
-        if (k < nd) {
-            for (uint32_t g = 0; g < gridDim.x; ++g) {
-                const uint32_t c = counts[(size_t)g * nd + k];
-                total += c;
-                if (g < blockIdx.x) before += c;
-            }
-        }
-        uint32_t inc = total;
+    for (uint32_t g0 = 0; g0 < runs; g0 += 64) {
+        const uint32_t g = g0 + lane;
+        const uint32_t c = g < runs ? counts[(size_t)g * nd + k] : 0;
+        uint32_t inc = c;
         for (int o = 1; o < 64; o <<= 1) {
             const uint32_t v = __shfl_up(inc, o, 64);
             if (lane >= o) inc += v;
         }
-        if (lane == 63) wsum[w] = inc;
-        __syncthreads();
-        uint32_t below = carry;
-        for (int j = 0; j < kWaves; ++j) {
-            if (j < w) below += wsum[j];
-            carry += wsum[j];
+        if (g < runs) counts[(size_t)g * nd + k] = carry + inc - c;
+        carry += __shfl(inc, 63, 64);
+    }
+    if (lane == 0) counts[(size_t)runs * nd + k] = carry;
+}
+
+// Exclusive prefix over the first kMaxDigits threads' values, in those threads.
+__device__ __forceinline__ uint32_t digit_prefix(uint32_t v, uint32_t *wsum)
+{
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    uint32_t inc = v;
+    for (int o = 1; o < 64; o <<= 1) {
+        const uint32_t u = __shfl_up(inc, o, 64);
+        if (lane >= o) inc += u;
+    }
+    __syncthreads();
+    if (lane == 63 && w < kMaxDigits / 64) wsum[w] = inc;
+    __syncthreads();
+    for (int j = 0; j < kMaxDigits / 64; ++j)
+        if (j < w) inc += wsum[j];
+    return inc - v;
+}
+
+// Rank of each of the thread's ITEMS entries among the wave's entries with
+// the same digit, in order (entry r of a lane comes before entry r + 1 of any
+// lane); cnt, the wave's own counters, ends as its digit counts.
+template <int ITEMS>
+__device__ __forceinline__ void wave_ranks(const uint32_t (&dg)[ITEMS], const bool (&ok)[ITEMS], int bits,
+                                           uint32_t *cnt, uint32_t (&rank)[ITEMS])
+{
+    const int lane = threadIdx.x & 63;
+    const uint64_t below = ((uint64_t)1 << lane) - 1;
+#pragma unroll
+    for (int r = 0; r < ITEMS; ++r) {
+        uint64_t same = __ballot(ok[r]);
+        for (int b = 0; b < bits; ++b) {
+            const uint64_t m = __ballot((dg[r] >> b) & 1);
+            same &= (dg[r] >> b) & 1 ? m : ~m;
         }
-        if (k < nd) base[k] = below + inc - total + before;
-        __syncthreads();
+        // the lanes of a digit read its counter together; the first then writes it
+        const uint32_t old = ok[r] ? ((volatile uint32_t *)cnt)[dg[r]] : 0;
+        if (ok[r] && (same & below) == 0) ((volatile uint32_t *)cnt)[dg[r]] = old + (uint32_t)__popcll(same);
+        __builtin_amdgcn_wave_barrier();
+        rank[r] = old + (uint32_t)__popcll(same & below);
+    }
+}
+
+template <typename I, int ITEMS>
+__global__ __launch_bounds__(kSortThreads) void k_sort_scatter(SortSource s, int shift, int bits,
+                                                               const uint32_t *counts, bool scanned,
+                                                               uint32_t *keys_out, uint32_t *pos_out)
+{
+    __shared__ uint32_t cnt[kSortWaves][kMaxDigits];
+    __shared__ uint32_t halves[2][kSortThreads];
+    __shared__ uint32_t wsum[kMaxDigits / 64];
+    const uint32_t nd = 1u << bits, tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const uint32_t run = kSortThreads * ITEMS;
+    for (uint32_t k = tid; k < kSortWaves * kMaxDigits; k += kSortThreads) (&cnt[0][0])[k] = 0;
+
+    // a wave's entries are consecutive
+    uint32_t key[ITEMS], at[ITEMS], dg[ITEMS], rank[ITEMS];
+    bool ok[ITEMS];
+    const uint64_t i0 = (uint64_t)blockIdx.x * run + w * (64 * ITEMS) + lane;
+#pragma unroll
+    for (int r = 0; r < ITEMS; ++r) {
+        const uint64_t i = i0 + r * 64;
+        ok[r] = i < s.n;
+        key[r] = ok[r] ? sort_key<I>(s, (uint32_t)i) : 0;
+        at[r] = ok[r] && s.pos ? s.pos[i] : (uint32_t)i;
+        dg[r] = (key[r] >> shift) & (nd - 1);
     }
 
-    // ranks within the wave's stretch of the run, in order
-    uint32_t key[kSortItems], rank[kSortItems];
-    const uint32_t i0 = blockIdx.x * kSortRun + w * (kSortRun / kWaves) + lane;
-#pragma unroll
-    for (int r = 0; r < kSortItems; ++r) {
-        const uint32_t i = i0 + r * 64;
-        const bool ok = i < s.n;
-        key[r] = ok ? sort_key<I>(s, i) : 0;
-        const uint32_t dg = (key[r] >> shift) & (nd - 1);
-        uint64_t same = __ballot(ok);
-        for (int b = 0; b < bits; ++b) {
-            const uint64_t m = __ballot((dg >> b) & 1);
-            same &= (dg >> b) & 1 ? m : ~m;
+    // offsets: all smaller digits, then the same digit in earlier runs
+    uint32_t total = 0, before = 0;
+    if (scanned) {
+        if (tid < nd) {
+            before = counts[(size_t)blockIdx.x * nd + tid];
+            total = counts[(size_t)gridDim.x * nd + tid];
         }
-        uint32_t old = 0;
-        const int leader = ok ? __ffsll((unsigned long long)same) - 1 : lane;
-        if (ok && lane == leader) old = atomicAdd(&cnt[w][dg], (uint32_t)__popcll(same));
-        old = __shfl(old, leader, 64);
-        rank[r] = old + __popcll(same & (((uint64_t)1 << lane) - 1));
+    } else {
+        // kSortThreads / nd threads share a digit's runs
+        const uint32_t k = tid & (nd - 1), part = tid >> bits, parts = kSortThreads >> bits;
+#pragma unroll 8
+        for (uint32_t g = part; g < gridDim.x; g += parts) {
+            const uint32_t c = counts[(size_t)g * nd + k];
+            total += c;
+            before += g < blockIdx.x ? c : 0;
+        }
+        halves[0][tid] = total;
+        halves[1][tid] = before;
+        __syncthreads();
+        if (tid < nd) {
+            for (uint32_t j = 1; j < parts; ++j) {
+                total += halves[0][j * nd + tid];
+                before += halves[1][j * nd + tid];
+            }
+        } else
+            total = 0;
+    }
+    uint32_t base = digit_prefix(total, wsum) + before;  // its barriers also publish the cleared counters
+
+    wave_ranks<ITEMS>(dg, ok, bits, cnt[w], rank);
+    __syncthreads();
+    if (tid < nd) {
+#pragma unroll
+        for (int j = 0; j < kSortWaves; ++j) {
+            const uint32_t c = cnt[j][tid];
+            cnt[j][tid] = base;
+            base += c;
+        }
     }
     __syncthreads();
-    for (int k = tid; k < nd; k += kThreads) {
-        uint32_t at = base[k];
-        for (int j = 0; j < kWaves; ++j) {
-            const uint32_t c = cnt[j][k];
-            cnt[j][k] = at;
-            at += c;
+#pragma unroll
+    for (int r = 0; r < ITEMS; ++r) {
+        if (ok[r]) {
+            const uint32_t to = cnt[w][dg[r]] + rank[r];
+            keys_out[to] = key[r];
+            pos_out[to] = at[r];
         }
     }
-    __syncthreads();
+}
+
+// The whole sort of up to kLocalMax tokens by one workgroup.
+template <typename I>
+__global__ __launch_bounds__(kSortThreads) void k_sort_local(SortSource s, int passes, int bits, uint32_t *keys_out,
+                                                             uint32_t *pos_out)
+{
+    __shared__ uint32_t cnt[kSortWaves][kMaxDigits];
+    __shared__ uint32_t keys[kLocalMax], pos[kLocalMax];
+    __shared__ uint32_t wsum[kMaxDigits / 64];
+    constexpr int ITEMS = kLocalItems;
+    const uint32_t nd = 1u << bits, tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    uint32_t key[ITEMS], at[ITEMS], dg[ITEMS], rank[ITEMS];
+    bool ok[ITEMS];
+    // the same stretch for every wave, as short as the tokens allow
+    const uint32_t per = (s.n + kSortThreads - 1) / kSortThreads;
+    const uint32_t i0 = w * 64 * per + lane;
 #pragma unroll
-    for (int r = 0; r < kSortItems; ++r) {
+    for (int r = 0; r < ITEMS; ++r) {
         const uint32_t i = i0 + r * 64;
-        if (i < s.n) {
-            const uint32_t at = cnt[w][(key[r] >> shift) & (nd - 1)] + rank[r];
-            keys_out[at] = key[r];
-            pos_out[at] = s.pos ? s.pos[i] : i;
+        ok[r] = r < (int)per && i < s.n;
+        key[r] = ok[r] ? sort_key<I>(s, i) : 0;
+        at[r] = i;
+    }
+    for (int p = 0; p < passes; ++p) {
+        for (uint32_t k = tid; k < kSortWaves * kMaxDigits; k += kSortThreads) (&cnt[0][0])[k] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < ITEMS; ++r) dg[r] = (key[r] >> (p * bits)) & (nd - 1);
+        wave_ranks<ITEMS>(dg, ok, bits, cnt[w], rank);
+        __syncthreads();
+        uint32_t total = 0;
+        if (tid < nd) {
+#pragma unroll
+            for (int j = 0; j < kSortWaves; ++j) {
+                const uint32_t c = cnt[j][tid];
+                cnt[j][tid] = total;
+                total += c;
+            }
+        }
+        const uint32_t base = digit_prefix(total, wsum);
+        if (tid < nd) {
+#pragma unroll
+            for (int j = 0; j < kSortWaves; ++j) cnt[j][tid] += base;
+        }
+        __syncthreads();
+        const bool last = p == passes - 1;
+#pragma unroll
+        for (int r = 0; r < ITEMS; ++r) {
+            if (!ok[r]) continue;
+            const uint32_t to = cnt[w][dg[r]] + rank[r];
+            if (last) {
+                keys_out[to] = key[r];
+                pos_out[to] = at[r];
+            } else {
+                keys[to] = key[r];
+                pos[to] = at[r];
+            }
+        }
+        if (last) break;
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < ITEMS; ++r) {
+            if (ok[r]) {
+                key[r] = keys[i0 + r * 64];
+                at[r] = pos[i0 + r * 64];
+            }
         }
     }
 }
@@ -184,7 +323,13 @@ __global__ __launch_bounds__(kThreads) void k_sort_scatter(SortSource s, int shi
 constexpr int kSnap = 32;
 constexpr int kShareMin = 32;
 constexpr int kMaxShares = 8192;  // waves of the sum kernel: 8 per SIMD
-enum { kFirstCut = 1, kLastCut = 2, kInside = 4 };
+enum { kFirstCut = 1, kInside = 2 };
+
+// What a share leaves to the join: whether it ends a row begun before it
+// (row), and whether it lies inside one row.
+struct Note {
+    uint32_t row, flags;
+};
 
 struct SumPlan {
     int cols;        // columns of one wave: 64 lanes of 16 bytes of the 16-bit types
@@ -258,7 +403,7 @@ __device__ __forceinline__ Cut find_cut(const uint32_t *keys, uint32_t n, uint32
 template <typename T, typename O, int LEN, int NV>
 __global__ __launch_bounds__(kThreads) void k_embed_grad_sum(EmbedGradArgs a, const uint32_t *keys,
                                                              const uint32_t *pos, int64_t share, uint32_t shares,
-                                                             float *part, uint8_t *flags)
+                                                             float *part, Note *notes)
 {
     typedef T tvec __attribute__((ext_vector_type(LEN)));
     typedef O ovec __attribute__((ext_vector_type(LEN)));
@@ -278,6 +423,7 @@ __global__ __launch_bounds__(kThreads) void k_embed_grad_sum(EmbedGradArgs a, co
     if (at > total) at = total;
     const Cut cut = find_cut(keys, n, rows, at);
     uint32_t i = __builtin_amdgcn_readlane(cut.i, 0), v = __builtin_amdgcn_readlane(cut.v, 0);
+    const uint32_t v0 = v;
     const uint32_t i1 = __builtin_amdgcn_readlane(cut.i, 32);
     uint32_t v1 = __builtin_amdgcn_readlane(cut.v, 32);
     const bool begun = __builtin_amdgcn_readlane((int)cut.inside, 0);
@@ -371,68 +517,93 @@ __global__ __launch_bounds__(kThreads) void k_embed_grad_sum(EmbedGradArgs a, co
 #pragma unroll
         for (int k = 0; k < NV; ++k)
             if (on[k]) ((fslot *)(part + ((uint64_t)w * 2 + 1) * a.dim + cols[k]))->v = acc[k];
-        flag |= kLastCut | (first ? kInside : 0);
+        flag |= first ? kInside : 0;
     }
-    if (lane == 0 && blockIdx.y == 0) flags[w] = (uint8_t)flag;
+    if (lane == 0 && blockIdx.y == 0) notes[w] = Note{v0, flag};
 }
 
-// Rows cut over several shares.  A workgroup goes through its share of the
-// flags; for each row that ends there it finds the share where the row was
-// begun, and its waves add equal stretches of the parts between, which are
-// then added in order.
+// Rows cut over several shares.  A workgroup looks at its share of the
+// notes; for each row that ends there it finds the share where the row was
+// begun, groups of threads that cover a block of columns add equal stretches
+// of the parts between, and the groups' sums are then added in order.
 constexpr int kJoinThreads = 512;
 constexpr int kJoinBlocks = 512;
-static_assert(kMaxShares / kJoinBlocks <= 64, "a join block's flags fit one wave");
+static_assert(kMaxShares / kJoinBlocks <= 64, "a join block's notes fit one wave");
 
 template <typename O>
-__global__ __launch_bounds__(kJoinThreads) void k_embed_grad_join(EmbedGradArgs a, const uint32_t *keys,
-                                                                  int64_t share, uint32_t shares, const float *part,
-                                                                  const uint8_t *flags)
+__global__ __launch_bounds__(kJoinThreads) void k_embed_grad_join(EmbedGradArgs a, uint32_t shares,
+                                                                  const float *part, const Note *notes)
 {
-    constexpr int kJoinWaves = kJoinThreads / 64;
-    __shared__ float sums[kJoinWaves][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __shared__ float4 sums[kJoinThreads];
+    typedef float fvec __attribute__((ext_vector_type(4)));
+    struct __attribute__((packed, aligned(4))) fslot { fvec v; };
+    const int lane = threadIdx.x & 63;
     const uint32_t per = (shares + gridDim.x - 1) / gridDim.x;
     const uint32_t w0 = blockIdx.x * per, w1 = w0 + per < shares ? w0 + per : shares;
-    // a block has at most kMaxShares / kJoinBlocks shares, one to a lane
-    const uint32_t mine = w0 + lane < w1 ? flags[w0 + lane] : 0;
-    for (uint64_t todo = __ballot((mine & kFirstCut) != 0); todo; todo &= todo - 1) {  // the same for all waves
-        const uint32_t w = w0 + (__ffsll((unsigned long long)todo) - 1);
+    const Note mine = w0 + lane < w1 ? notes[w0 + lane] : Note{0, 0};
+    // lanes that cover a row of parts four columns at a time
+    int wide = 1;
+    while (wide < kJoinThreads && wide * 4 < a.dim) wide <<= 1;
+    const int groups = kJoinThreads / wide, group = threadIdx.x / wide, col = (threadIdx.x & (wide - 1)) * 4;
+    for (uint64_t todo = __ballot((mine.flags & kFirstCut) != 0); todo; todo &= todo - 1) {  // the same for all waves
+        const int which = __ffsll((unsigned long long)todo) - 1;
+        const uint32_t w = w0 + which;
+        const int64_t v = (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)mine.row, which);
         // the share where the row was begun: the first before w that is not all inside it
         uint32_t b = w;
         for (bool more = true; more;) {
             const int64_t q = (int64_t)b - 1 - lane;
-            const uint64_t m = __ballot(q < 0 || !(flags[q] & kInside));
+            const uint64_t m = __ballot(q < 0 || !(notes[q < 0 ? 0 : q].flags & kInside));
             if (m) {
                 b = b - 1 - (__ffsll((unsigned long long)m) - 1);
                 more = false;
             } else
                 b -= 64;
         }
-        const int64_t at = (int64_t)w * share;
-        const Cut cut = find_cut(keys, (uint32_t)a.n, (uint32_t)a.rows, at);
-        const uint32_t v = __builtin_amdgcn_readfirstlane(cut.v);
         const uint32_t count = w - b + 1;  // parts: the last rows of b .. w - 1, the first row of w
-        const uint32_t each = (count + kJoinWaves - 1) / kJoinWaves;
-        const uint32_t p0 = wave * each, p1 = p0 + each < count ? p0 + each : count;
-        for (int c0 = 0; c0 < a.dim; c0 += 64) {
-            const int c = c0 + lane;
-            float s = 0.f;
-            if (c < a.dim) {
+        const uint32_t each = (count + groups - 1) / groups;
+        const uint32_t p0 = group * each, p1 = p0 + each < count ? p0 + each : count;
+        for (int c0 = 0; c0 < a.dim; c0 += wide * 4) {
+            const int c = c0 + col;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c + 4 <= a.dim) {
 #pragma unroll 8
-                for (uint32_t p = p0; p < p1; ++p)
-                    s += part[((uint64_t)(b + p) * 2 + (b + p < w ? 1 : 0)) * a.dim + c];
+                for (uint32_t p = p0; p < p1; ++p) {
+                    const fvec x = ((const fslot *)(part + ((uint64_t)(b + p) * 2 + (b + p < w ? 1 : 0)) * a.dim + c))->v;
+                    s.x += x.x;
+                    s.y += x.y;
+                    s.z += x.z;
+                    s.w += x.w;
+                }
+            } else {
+                for (uint32_t p = p0; p < p1; ++p) {
+                    const float *x = part + ((uint64_t)(b + p) * 2 + (b + p < w ? 1 : 0)) * a.dim + c;
+                    if (c < a.dim) s.x += x[0];
+                    if (c + 1 < a.dim) s.y += x[1];
+                    if (c + 2 < a.dim) s.z += x[2];
+                }
             }
             __syncthreads();
-            sums[wave][lane] = s;
+            sums[threadIdx.x] = s;
             __syncthreads();
-            if (wave == 0 && c < a.dim) {
-                s = 0.f;
-                for (int k = 0; k < kJoinWaves; ++k) s += sums[k][lane];
-                s *= a.scale;
-                O *out = (O *)a.out + (int64_t)v * a.ld_out + c;
-                if (a.accumulate) s += (float)*out;
-                *out = (O)s;
+            if (group == 0) {
+                for (int k = 1; k < groups; ++k) {
+                    const float4 x = sums[k * wide + threadIdx.x];
+                    s.x += x.x;
+                    s.y += x.y;
+                    s.z += x.z;
+                    s.w += x.w;
+                }
+                const float r[4] = {s.x, s.y, s.z, s.w};
+                O *out = (O *)a.out + v * a.ld_out + c;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (c + k < a.dim) {
+                        float t = r[k] * a.scale;
+                        if (a.accumulate) t += (float)out[k];
+                        out[k] = (O)t;
+                    }
+                }
             }
         }
     }
@@ -452,12 +623,41 @@ hipError_t launch_embed(const EmbedArgs &a, hipStream_t s)
     return hipGetLastError();
 }
 
+static uint64_t count_bytes(const SortPlan &p) { return up256(((uint64_t)4 << p.bits) * (uint64_t)(p.runs + 1)); }
+
 uint64_t embed_grad_work(int64_t n, int64_t rows, int dim)
 {
-    const SortPlan p = sort_plan(n, rows);
     const SumPlan q = sum_plan(n, rows, dim);
-    return 4 * up256(4 * (uint64_t)n) + up256(((uint64_t)4 << p.bits) * (uint64_t)p.runs) +
-           up256((uint64_t)q.shares) + (uint64_t)q.shares * 2 * 4 * (uint64_t)dim;
+    return 4 * up256(4 * (uint64_t)n) + count_bytes(sort_plan(n, rows)) + up256(q.shares * sizeof(Note)) +
+           (uint64_t)q.shares * 2 * 4 * (uint64_t)dim;
+}
+
+template <typename I>
+static void launch_sort(const SortPlan &p, SortSource &src, uint32_t *const (&buf)[4], uint32_t *counts, hipStream_t s)
+{
+    const dim3 block(kSortThreads);
+    if (src.n <= (uint32_t)kLocalMax) {
+        k_sort_local<I><<<dim3(1), block, 0, s>>>(src, p.passes, p.bits, buf[0], buf[1]);
+        src.keys = buf[0];
+        src.pos = buf[1];
+        return;
+    }
+    const dim3 grid((unsigned)p.runs);
+    const bool scan = p.runs > kScanRuns;
+    for (int k = 0; k < p.passes; ++k) {
+        uint32_t *ko = buf[2 * (k & 1)], *po = buf[2 * (k & 1) + 1];
+        const int shift = k * p.bits;
+        k_sort_count<I><<<grid, block, 0, s>>>(src, shift, p.bits, (uint32_t)(p.items * kSortThreads), counts);
+        if (scan)
+            k_sort_scan<<<dim3(((1u << p.bits) + kWaves - 1) / kWaves), dim3(kThreads), 0, s>>>(
+                counts, (uint32_t)p.runs, p.bits);
+        if (p.items == 4)
+            k_sort_scatter<I, 4><<<grid, block, 0, s>>>(src, shift, p.bits, counts, scan, ko, po);
+        else
+            k_sort_scatter<I, 8><<<grid, block, 0, s>>>(src, shift, p.bits, counts, scan, ko, po);
+        src.keys = ko;
+        src.pos = po;
+    }
 }
 
 hipError_t launch_embed_grad(const EmbedGradArgs &a, hipStream_t s)
@@ -467,35 +667,25 @@ hipError_t launch_embed_grad(const EmbedGradArgs &a, hipStream_t s)
     uint32_t *buf[4];
     for (int k = 0; k < 4; ++k, at += up256(4 * (uint64_t)a.n)) buf[k] = (uint32_t *)at;
     uint32_t *counts = (uint32_t *)at;
-    at += up256(((uint64_t)4 << p.bits) * (uint64_t)p.runs);
+    at += count_bytes(p);
     SortSource src{a.ids, nullptr, nullptr, a.padding_id, a.rows, (uint32_t)a.n};
-    int side = 0;
-    for (int k = 0; k < p.passes && a.n; ++k, side ^= 1) {
-        const dim3 grid((unsigned)p.runs), block(kThreads);
-        uint32_t *ko = buf[2 * side], *po = buf[2 * side + 1];
-        if (a.id_type) {
-            k_sort_count<int64_t><<<grid, block, 0, s>>>(src, k * p.bits, p.bits, counts);
-            k_sort_scatter<int64_t><<<grid, block, 0, s>>>(src, k * p.bits, p.bits, counts, ko, po);
-        } else {
-            k_sort_count<int32_t><<<grid, block, 0, s>>>(src, k * p.bits, p.bits, counts);
-            k_sort_scatter<int32_t><<<grid, block, 0, s>>>(src, k * p.bits, p.bits, counts, ko, po);
-        }
-        src.keys = ko;
-        src.pos = po;
+    if (a.n) {
+        if (a.id_type) launch_sort<int64_t>(p, src, buf, counts, s);
+        else launch_sort<int32_t>(p, src, buf, counts, s);
     }
     const SumPlan q = sum_plan(a.n, a.rows, a.dim);
-    uint8_t *flags = (uint8_t *)at;
-    float *part = (float *)(at + up256((uint64_t)q.shares));
+    Note *notes = (Note *)at;
+    float *part = (float *)(at + up256(q.shares * sizeof(Note)));
     const int len = a.grad_type == kF32 ? 4 : 8;
     const dim3 grid((unsigned)((q.shares + kWaves - 1) / kWaves), q.col_blocks), block(kThreads);
 #define SUM(T, O)                                                                                                  \
     do {                                                                                                           \
         if (a.dim < len)                                                                                           \
             k_embed_grad_sum<T, O, 1, 1><<<grid, block, 0, s>>>(a, src.keys, src.pos, q.share, (uint32_t)q.shares, \
-                                                                part, flags);                                      \
+                                                                part, notes);                                      \
         else                                                                                                       \
             k_embed_grad_sum<T, O, 16 / sizeof(T), sizeof(T) / 2><<<grid, block, 0, s>>>(                          \
-                a, src.keys, src.pos, q.share, (uint32_t)q.shares, part, flags);                                   \
+                a, src.keys, src.pos, q.share, (uint32_t)q.shares, part, notes);                                   \
     } while (0)
     switch (a.grad_type * 4 + a.out_type) {
     case kF32 * 4 + kF32: SUM(float, float); break;
@@ -505,9 +695,9 @@ hipError_t launch_embed_grad(const EmbedGradArgs &a, hipStream_t s)
     default: SUM(bf16_t, bf16_t); break;
     }
 #undef SUM
-    if (a.n > kSnap)
+    if (a.n > kSnap)  // else no row is long enough to be cut
         ERSJ_ELEM_SWITCH(a.out_type, O, k_embed_grad_join<O><<<dim3(kJoinBlocks), dim3(kJoinThreads), 0, s>>>(
-                                            a, src.keys, q.share, (uint32_t)q.shares, part, flags))
+                                            a, (uint32_t)q.shares, part, notes))
     return hipGetLastError();
 }
 
