@@ -320,8 +320,8 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_local(SortSource s, int p
 // begun before, its last row if that is not finished), and k_embed_grad_join
 // adds them up in order.
 
-constexpr int kSnap = 32;
-constexpr int kShareMin = 32;
+constexpr int kSnap = 8;
+constexpr int kShareMin = 16;
 constexpr int kMaxShares = 8192;  // waves of the sum kernel: 8 per SIMD
 enum { kFirstCut = 1, kInside = 2 };
 
@@ -388,7 +388,7 @@ __device__ __forceinline__ Cut find_cut(const uint32_t *keys, uint32_t n, uint32
     const bool same = begun && j < n && keys[j] == r.v;
     const uint32_t m = (uint32_t)(__ballot(same) >> half);
     if (begun) {
-        if (m == 0xffffffffu) r.inside = true;
+        if (__popc(m) >= kSnap) r.inside = true;
         else {
             r.i += __popc(m);
             r.v += 1;
@@ -411,7 +411,7 @@ __global__ __launch_bounds__(kThreads) void k_embed_grad_sum(EmbedGradArgs a, co
     struct __attribute__((packed, aligned(sizeof(T)))) tslot { tvec v; };
     struct __attribute__((packed, aligned(sizeof(O)))) oslot { ovec v; };
     struct __attribute__((packed, aligned(4))) fslot { fvec v; };
-    constexpr int kAhead = 8 / NV;  // rows in flight
+    constexpr int kAhead = 4 / NV;  // tokens of one set of loads; two sets are in flight
 
     const int lane = threadIdx.x & 63;
     const uint32_t w = __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + (threadIdx.x >> 6));
@@ -435,14 +435,14 @@ __global__ __launch_bounds__(kThreads) void k_embed_grad_sum(EmbedGradArgs a, co
     const int vecs = (a.dim + LEN - 1) / LEN;
     const int c0 = (int)((int64_t)blockIdx.y * vecs / gridDim.y) * LEN;
     const int block_cols = (int)((int64_t)(blockIdx.y + 1) * vecs / gridDim.y) * LEN - c0;
-    int cols[NV];
-    bool on[NV];
+    uint32_t cols[NV];
+    bool on[NV];  // lanes beyond the columns load and add the last vector, and write nothing
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        int c = (k * 64 + lane) * LEN;
+        const int c = (k * 64 + lane) * LEN;
         on[k] = c < block_cols;
-        c += c0;
-        cols[k] = c + LEN > a.dim ? a.dim - LEN : c;
+        const int last = c0 + block_cols < a.dim ? c0 + block_cols - LEN : a.dim - LEN;
+        cols[k] = (uint32_t)(c0 + c < last ? c0 + c : last);
     }
 
     fvec acc[NV];
@@ -478,39 +478,46 @@ __global__ __launch_bounds__(kThreads) void k_embed_grad_sum(EmbedGradArgs a, co
     };
 
     while (i < i1) {
-        // up to 64 tokens' keys and places, one to a lane
-        const uint32_t m = i1 - i < 64 ? i1 - i : 64;
-        const uint32_t kk = keys[i + (lane < (int)m ? lane : 0)];
-        const uint32_t pp = pos[i + (lane < (int)m ? lane : 0)];
-        if (__builtin_amdgcn_readlane(kk, 0) >= rows) { i = i1; break; }
-        for (uint32_t t = 0; t < m; t += kAhead) {
-            tvec x[kAhead][NV];
+        // up to 64 tokens, one to a lane: key and place of the row of grad in bytes
+        uint32_t m = i1 - i < 64 ? i1 - i : 64;
+        const uint32_t mine = i + (lane < (int)m ? lane : 0);
+        const uint32_t kk = keys[mine];
+        const uint64_t place = (uint64_t)pos[mine] * (uint64_t)a.ld_grad * sizeof(T);
+        const uint32_t place_lo = (uint32_t)place, place_hi = (uint32_t)(place >> 32);
+        // tokens that add nothing come last
+        const uint32_t real = (uint32_t)__popcll(__ballot(lane < (int)m && kk < rows));
+        i = real < m ? i1 : i + m;
+        m = real;
+        if (m == 0) break;
+        auto load = [&](uint32_t t, tvec (&x)[kAhead][NV]) {
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 const uint32_t tu = t + u < m ? t + u : m - 1;
-                // tokens that add nothing (key `rows`) are not read
-                const uint32_t p = __builtin_amdgcn_readlane(kk, tu) < rows ? __builtin_amdgcn_readlane(pp, tu)
-                                                                              : __builtin_amdgcn_readlane(pp, 0);
-                const T *row = (const T *)a.grad + (int64_t)p * a.ld_grad;
+                const char *row = (const char *)a.grad + (((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)place_hi, tu) << 32) |
+                                                          (uint32_t)__builtin_amdgcn_readlane((int)place_lo, tu));
 #pragma unroll
-                for (int k = 0; k < NV; ++k)
-                    if (on[k]) x[u][k] = ((const tslot *)(row + cols[k]))->v;
+                for (int k = 0; k < NV; ++k) x[u][k] = ((const tslot *)(row + cols[k] * (uint32_t)sizeof(T)))->v;
             }
+        };
+        auto add = [&](uint32_t t, const tvec (&x)[kAhead][NV]) {
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                if (t + u < m) {
-                    const uint32_t key = __builtin_amdgcn_readlane(kk, t + u);
-                    if (key < rows) {
-                        while (v < key) finish();
+                if (t + u >= m) continue;
+                const uint32_t key = (uint32_t)__builtin_amdgcn_readlane((int)kk, t + u);
+                while (v != key) finish();
 #pragma unroll
-                        for (int k = 0; k < NV; ++k)
-                            if (on[k]) acc[k] += __builtin_convertvector(x[u][k], fvec);
-                        any = true;
-                    }
-                }
+                for (int k = 0; k < NV; ++k) acc[k] += __builtin_convertvector(x[u][k], fvec);
+                any = true;
             }
+        };
+        tvec x[kAhead][NV], y[kAhead][NV];
+        load(0, x);
+        for (uint32_t t = 0; t < m; t += 2 * kAhead) {
+            if (t + kAhead < m) load(t + kAhead, y);
+            add(t, x);
+            if (t + 2 * kAhead < m) load(t + 2 * kAhead, x);
+            add(t + kAhead, y);
         }
-        i += m;
     }
     while (v < v1) finish();
     if (open) {
@@ -522,35 +529,60 @@ __global__ __launch_bounds__(kThreads) void k_embed_grad_sum(EmbedGradArgs a, co
     if (lane == 0 && blockIdx.y == 0) notes[w] = Note{v0, flag};
 }
 
-// Rows cut over several shares.  A workgroup looks at its share of the
-// notes; for each row that ends there it finds the share where the row was
-// begun, groups of threads that cover a block of columns add equal stretches
-// of the parts between, and the groups' sums are then added in order.
+// Rows cut over several shares: the last rows of shares b .. w - 1 and the
+// first row of share w are parts of one row of the table.  A wave looks at one
+// share w; where a row that was begun before ends there, it finds b and adds
+// the parts in order.  More than kJoinAlone parts are added by the whole
+// workgroup, each wave an equal stretch of them, and then the waves' sums in
+// order.
 constexpr int kJoinThreads = 512;
-constexpr int kJoinBlocks = 512;
-static_assert(kMaxShares / kJoinBlocks <= 64, "a join block's notes fit one wave");
+constexpr int kJoinWaves = kJoinThreads / 64;
+constexpr uint32_t kJoinAlone = 16;
 
 template <typename O>
 __global__ __launch_bounds__(kJoinThreads) void k_embed_grad_join(EmbedGradArgs a, uint32_t shares,
                                                                   const float *part, const Note *notes)
 {
-    __shared__ float4 sums[kJoinThreads];
     typedef float fvec __attribute__((ext_vector_type(4)));
     struct __attribute__((packed, aligned(4))) fslot { fvec v; };
-    const int lane = threadIdx.x & 63;
-    const uint32_t per = (shares + gridDim.x - 1) / gridDim.x;
-    const uint32_t w0 = blockIdx.x * per, w1 = w0 + per < shares ? w0 + per : shares;
-    const Note mine = w0 + lane < w1 ? notes[w0 + lane] : Note{0, 0};
-    // lanes that cover a row of parts four columns at a time
-    int wide = 1;
-    while (wide < kJoinThreads && wide * 4 < a.dim) wide <<= 1;
-    const int groups = kJoinThreads / wide, group = threadIdx.x / wide, col = (threadIdx.x & (wide - 1)) * 4;
-    for (uint64_t todo = __ballot((mine.flags & kFirstCut) != 0); todo; todo &= todo - 1) {  // the same for all waves
-        const int which = __ffsll((unsigned long long)todo) - 1;
-        const uint32_t w = w0 + which;
-        const int64_t v = (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)mine.row, which);
-        // the share where the row was begun: the first before w that is not all inside it
-        uint32_t b = w;
+    __shared__ fvec sums[kJoinWaves][64];
+    __shared__ uint32_t first[kJoinWaves], row[kJoinWaves], count[kJoinWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint32_t w = blockIdx.x * kJoinWaves + wave;
+
+    // sum of parts p0 .. p1 - 1 of the row begun in share b and ended in share e, four columns from c
+    auto sum = [&](uint32_t b, uint32_t e, uint32_t p0, uint32_t p1, int c) {
+        fvec s = (fvec)0.f;
+        if (c + 4 <= a.dim) {
+#pragma unroll 8
+            for (uint32_t p = p0; p < p1; ++p)
+                s += ((const fslot *)(part + ((uint64_t)(b + p) * 2 + (b + p < e ? 1 : 0)) * a.dim + c))->v;
+        } else {
+            for (uint32_t p = p0; p < p1; ++p) {
+                const float *x = part + ((uint64_t)(b + p) * 2 + (b + p < e ? 1 : 0)) * a.dim + c;
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    if (c + k < a.dim) s[k] += x[k];
+            }
+        }
+        return s;
+    };
+    auto write = [&](uint32_t v, fvec s, int c) {
+        O *out = (O *)a.out + (int64_t)v * a.ld_out + c;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (c + k < a.dim) {
+                float t = s[k] * a.scale;
+                if (a.accumulate) t += (float)out[k];
+                out[k] = (O)t;
+            }
+        }
+    };
+
+    uint32_t parts = 0, b = w;
+    const Note note = w < shares ? notes[w] : Note{0, 0};
+    if (note.flags & kFirstCut) {
+        // b: the first share before w that is not all inside the row
         for (bool more = true; more;) {
             const int64_t q = (int64_t)b - 1 - lane;
             const uint64_t m = __ballot(q < 0 || !(notes[q < 0 ? 0 : q].flags & kInside));
@@ -560,50 +592,31 @@ __global__ __launch_bounds__(kJoinThreads) void k_embed_grad_join(EmbedGradArgs 
             } else
                 b -= 64;
         }
-        const uint32_t count = w - b + 1;  // parts: the last rows of b .. w - 1, the first row of w
-        const uint32_t each = (count + groups - 1) / groups;
-        const uint32_t p0 = group * each, p1 = p0 + each < count ? p0 + each : count;
-        for (int c0 = 0; c0 < a.dim; c0 += wide * 4) {
-            const int c = c0 + col;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (c + 4 <= a.dim) {
-#pragma unroll 8
-                for (uint32_t p = p0; p < p1; ++p) {
-                    const fvec x = ((const fslot *)(part + ((uint64_t)(b + p) * 2 + (b + p < w ? 1 : 0)) * a.dim + c))->v;
-                    s.x += x.x;
-                    s.y += x.y;
-                    s.z += x.z;
-                    s.w += x.w;
-                }
-            } else {
-                for (uint32_t p = p0; p < p1; ++p) {
-                    const float *x = part + ((uint64_t)(b + p) * 2 + (b + p < w ? 1 : 0)) * a.dim + c;
-                    if (c < a.dim) s.x += x[0];
-                    if (c + 1 < a.dim) s.y += x[1];
-                    if (c + 2 < a.dim) s.z += x[2];
-                }
-            }
+        parts = w - b + 1;
+        if (parts <= kJoinAlone)
+            for (int c = lane * 4; c < a.dim; c += 256) write(note.row, sum(b, w, 0, parts, c), c);
+    }
+    if (lane == 0) {
+        first[wave] = b;
+        row[wave] = note.row;
+        count[wave] = parts > kJoinAlone ? parts : 0;
+    }
+    __syncthreads();
+    for (int j = 0; j < kJoinWaves; ++j) {
+        const uint32_t n = count[j];
+        if (n == 0) continue;
+        const uint32_t e = blockIdx.x * kJoinWaves + j, each = (n + kJoinWaves - 1) / kJoinWaves;
+        const uint32_t p0 = wave * each < n ? wave * each : n, p1 = p0 + each < n ? p0 + each : n;
+        for (int c0 = 0; c0 < a.dim; c0 += 256) {
+            const int c = c0 + lane * 4;
             __syncthreads();
-            sums[threadIdx.x] = s;
+            if (c < a.dim) sums[wave][lane] = sum(first[j], e, p0, p1, c);
             __syncthreads();
-            if (group == 0) {
-                for (int k = 1; k < groups; ++k) {
-                    const float4 x = sums[k * wide + threadIdx.x];
-                    s.x += x.x;
-                    s.y += x.y;
-                    s.z += x.z;
-                    s.w += x.w;
-                }
-                const float r[4] = {s.x, s.y, s.z, s.w};
-                O *out = (O *)a.out + v * a.ld_out + c;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (c + k < a.dim) {
-                        float t = r[k] * a.scale;
-                        if (a.accumulate) t += (float)out[k];
-                        out[k] = (O)t;
-                    }
-                }
+            // the waves take turns in adding up the blocks of columns
+            if (wave == ((c0 >> 8) & (kJoinWaves - 1)) && c < a.dim) {
+                fvec s = sums[0][lane];
+                for (int k = 1; k < kJoinWaves; ++k) s += sums[k][lane];
+                write(row[j], s, c);
             }
         }
     }
@@ -696,8 +709,9 @@ hipError_t launch_embed_grad(const EmbedGradArgs &a, hipStream_t s)
     }
 #undef SUM
     if (a.n > kSnap)  // else no row is long enough to be cut
-        ERSJ_ELEM_SWITCH(a.out_type, O, k_embed_grad_join<O><<<dim3(kJoinBlocks), dim3(kJoinThreads), 0, s>>>(
-                                            a, (uint32_t)q.shares, part, notes))
+        ERSJ_ELEM_SWITCH(a.out_type, O,
+            k_embed_grad_join<O><<<dim3((unsigned)((q.shares + kJoinWaves - 1) / kJoinWaves)), dim3(kJoinThreads), 0,
+                                   s>>>(a, (uint32_t)q.shares, part, notes))
     return hipGetLastError();
 }
 
