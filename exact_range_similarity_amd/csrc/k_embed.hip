@@ -60,7 +60,7 @@ SortPlan sort_plan(int64_t n, int64_t rows)
     SortPlan p;
     p.passes = (kb + kMaxDigitBits - 1) / kMaxDigitBits;
     p.bits = (kb + p.passes - 1) / p.passes;
-    p.items = n <= (int64_t)1 << 18 ? 4 : 8;
+    p.items = n <= (int64_t)kScanRuns * 2 * kSortThreads ? 2 : 4;
     const int64_t run = (int64_t)p.items * kSortThreads;
     p.runs = (n + run - 1) / run;
     return p;
@@ -533,9 +533,9 @@ __global__ __launch_bounds__(kThreads) void k_embed_grad_sum(EmbedGradArgs a, co
 // first row of share w are parts of one row of the table.  A wave looks at one
 // share w; where a row that was begun before ends there, it finds b and adds
 // the parts in order.  More than kJoinAlone parts are added by the whole
-// workgroup, each wave an equal stretch of them, and then the waves' sums in
-// order.
-constexpr int kJoinThreads = 512;
+// workgroup: its waves form groups that cover a block of columns, each group
+// adds an equal stretch of the parts, and the groups' sums are added in order.
+constexpr int kJoinThreads = 1024;
 constexpr int kJoinWaves = kJoinThreads / 64;
 constexpr uint32_t kJoinAlone = 16;
 
@@ -550,13 +550,22 @@ __global__ __launch_bounds__(kJoinThreads) void k_embed_grad_join(EmbedGradArgs 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t w = blockIdx.x * kJoinWaves + wave;
 
-    // sum of parts p0 .. p1 - 1 of the row begun in share b and ended in share e, four columns from c
+    // sum of parts p0 .. p1 - 1 of the row begun in share b and ended in share e, four columns from c;
+    // the loads of eight parts are in flight together, the last ones repeated where there are fewer
     auto sum = [&](uint32_t b, uint32_t e, uint32_t p0, uint32_t p1, int c) {
         fvec s = (fvec)0.f;
         if (c + 4 <= a.dim) {
-#pragma unroll 8
-            for (uint32_t p = p0; p < p1; ++p)
-                s += ((const fslot *)(part + ((uint64_t)(b + p) * 2 + (b + p < e ? 1 : 0)) * a.dim + c))->v;
+            for (uint32_t p = p0; p < p1; p += 8) {
+                fvec x[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const uint32_t q = b + (p + u < p1 ? p + u : p1 - 1);
+                    x[u] = ((const fslot *)(part + ((uint64_t)q * 2 + (q < e ? 1 : 0)) * a.dim + c))->v;
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (p + u < p1) s += x[u];
+            }
         } else {
             for (uint32_t p = p0; p < p1; ++p) {
                 const float *x = part + ((uint64_t)(b + p) * 2 + (b + p < e ? 1 : 0)) * a.dim + c;
@@ -582,15 +591,23 @@ __global__ __launch_bounds__(kJoinThreads) void k_embed_grad_join(EmbedGradArgs 
     uint32_t parts = 0, b = w;
     const Note note = w < shares ? notes[w] : Note{0, 0};
     if (note.flags & kFirstCut) {
-        // b: the first share before w that is not all inside the row
+        // b: the first share before w that is not all inside the row, found 256 shares at a time
         for (bool more = true; more;) {
-            const int64_t q = (int64_t)b - 1 - lane;
-            const uint64_t m = __ballot(q < 0 || !(notes[q < 0 ? 0 : q].flags & kInside));
-            if (m) {
-                b = b - 1 - (__ffsll((unsigned long long)m) - 1);
-                more = false;
-            } else
-                b -= 64;
+            uint64_t m[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t q = (int64_t)b - 1 - 64 * k - lane;
+                m[k] = __ballot(q < 0 || !(notes[q < 0 ? 0 : q].flags & kInside));
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (!more) continue;
+                if (m[k]) {
+                    b = b - 1 - (__ffsll((unsigned long long)m[k]) - 1);
+                    more = false;
+                } else
+                    b -= 64;
+            }
         }
         parts = w - b + 1;
         if (parts <= kJoinAlone)
@@ -602,20 +619,22 @@ __global__ __launch_bounds__(kJoinThreads) void k_embed_grad_join(EmbedGradArgs 
         count[wave] = parts > kJoinAlone ? parts : 0;
     }
     __syncthreads();
+    const int blocks = (a.dim + 255) / 256;  // blocks of columns, one per wave of a group
+    const int across = blocks < kJoinWaves ? blocks : kJoinWaves;
+    const int groups = kJoinWaves / across, group = wave / across, block = wave - group * across;
     for (int j = 0; j < kJoinWaves; ++j) {
         const uint32_t n = count[j];
         if (n == 0) continue;
-        const uint32_t e = blockIdx.x * kJoinWaves + j, each = (n + kJoinWaves - 1) / kJoinWaves;
-        const uint32_t p0 = wave * each < n ? wave * each : n, p1 = p0 + each < n ? p0 + each : n;
-        for (int c0 = 0; c0 < a.dim; c0 += 256) {
-            const int c = c0 + lane * 4;
+        const uint32_t e = blockIdx.x * kJoinWaves + j, each = (n + groups - 1) / groups;
+        const uint32_t p0 = group * each < n ? group * each : n, p1 = p0 + each < n ? p0 + each : n;
+        for (int c0 = 0; c0 < blocks; c0 += across) {
+            const int c = (c0 + block) * 256 + lane * 4;
             __syncthreads();
-            if (c < a.dim) sums[wave][lane] = sum(first[j], e, p0, p1, c);
+            if (group < groups && c < a.dim) sums[wave][lane] = sum(first[j], e, p0, p1, c);
             __syncthreads();
-            // the waves take turns in adding up the blocks of columns
-            if (wave == ((c0 >> 8) & (kJoinWaves - 1)) && c < a.dim) {
-                fvec s = sums[0][lane];
-                for (int k = 1; k < kJoinWaves; ++k) s += sums[k][lane];
+            if (group == 0 && c < a.dim) {
+                fvec s = sums[wave][lane];
+                for (int k = 1; k < groups; ++k) s += sums[k * across + wave][lane];
                 write(row[j], s, c);
             }
         }
@@ -664,10 +683,10 @@ static void launch_sort(const SortPlan &p, SortSource &src, uint32_t *const (&bu
         if (scan)
             k_sort_scan<<<dim3(((1u << p.bits) + kWaves - 1) / kWaves), dim3(kThreads), 0, s>>>(
                 counts, (uint32_t)p.runs, p.bits);
-        if (p.items == 4)
-            k_sort_scatter<I, 4><<<grid, block, 0, s>>>(src, shift, p.bits, counts, scan, ko, po);
+        if (p.items == 2)
+            k_sort_scatter<I, 2><<<grid, block, 0, s>>>(src, shift, p.bits, counts, scan, ko, po);
         else
-            k_sort_scatter<I, 8><<<grid, block, 0, s>>>(src, shift, p.bits, counts, scan, ko, po);
+            k_sort_scatter<I, 4><<<grid, block, 0, s>>>(src, shift, p.bits, counts, scan, ko, po);
         src.keys = ko;
         src.pos = po;
     }
