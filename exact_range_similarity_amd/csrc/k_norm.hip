@@ -48,6 +48,26 @@ __device__ __forceinline__ float lanes_sum(float v)
     return v;
 }
 
+// Sum over the teams of a wave, lane by lane (over the lanes that differ by a
+// multiple of L), in every lane.
+template <int L>
+__device__ __forceinline__ float teams_sum(float v)
+{
+    if constexpr (L <= 8) v += dpp<0x128>(v);  // rotations within 16 lanes, by 8, 4, 2, 1
+    if constexpr (L <= 4) v += dpp<0x124>(v);
+    if constexpr (L <= 2) v += dpp<0x122>(v);
+    if constexpr (L <= 1) v += dpp<0x121>(v);
+    if constexpr (L <= 16) {
+        const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+    }
+    if constexpr (L <= 32) {
+        const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+    }
+    return v;
+}
+
 // Sums of K values over a team of L lanes.  A team of a workgroup goes through
 // `red`, one slot of which is free of readers when the next sum writes it
 // (two slots used in turn, one barrier a sum).
@@ -208,7 +228,7 @@ __global__ __launch_bounds__(1024) void k_norm_long(NormArgs a)
 }
 
 // The gradient.  dw and db are sums over rows: each team keeps its own in
-// registers, a workgroup's teams are added in order at the end, and
+// registers, a workgroup's teams are added in a fixed order at the end, and
 // k_norm_grad_join adds the workgroups' sums, part [workgroup][2][dim].
 template <typename T, typename P, int LEN, int L, int NV>
 __global__ __launch_bounds__(L > kThreads ? L : kThreads) void k_norm_grad(NormGradArgs a, float *part)
@@ -220,7 +240,7 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void k_norm_grad(NormG
     typedef Slot<T, LEN> X;
     typedef Slot<P, LEN> W;
     __shared__ float red[2][L > 64 ? L / 64 : 1][2];
-    __shared__ float sums[L > 64 ? 1 : 2 * L * NV * LEN];
+    __shared__ __align__(16) float sums[L > 64 ? 1 : kBlock / 64][L > 64 ? 1 : 2 * L * NV * LEN];
     int slot = 0;
     const Columns<LEN, L, NV> at(a.dim);
     const P *pw = (const P *)a.weight;
@@ -297,46 +317,44 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void k_norm_grad(NormG
     }
     if (!part) return;
     float *out = part + (uint64_t)blockIdx.x * 2 * a.dim;
+    typedef Slot<float, LEN> S;
+    // a lane's own columns of vector k to p[column] (p in LDS or not)
+    auto put = [&](float *p, int k, fvec v) {
+        if (k < NV - 1 || at.skip == 0) S::store(p + at.col[k], v);
+        else {
+#pragma unroll
+            for (int j = 0; j < LEN; ++j)
+                if (j >= at.skip) p[at.col[k] + j] = v[j];
+        }
+    };
     if constexpr (L > 64) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            put(out, k, dw[k]);
+            put(out + a.dim, k, db[k]);
+        }
+    } else {
+        // the teams of a wave by lane exchanges, then the waves in order
+        float *own = sums[threadIdx.x >> 6];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
 #pragma unroll
             for (int j = 0; j < LEN; ++j) {
-                if (k < NV - 1 || j >= at.skip) {
-                    out[at.col[k] + j] = dw[k][j];
-                    out[a.dim + at.col[k] + j] = db[k][j];
-                }
+                dw[k][j] = teams_sum<L>(dw[k][j]);
+                db[k][j] = teams_sum<L>(db[k][j]);
+            }
+            if ((threadIdx.x & 63) < L) {
+                put(own, k, dw[k]);
+                put(own + L * NV * LEN, k, db[k]);
             }
         }
-    } else {
-        // the teams in order, at [vector][element][lane] so that lanes lie side by side
-        const int lane = threadIdx.x & (L - 1);
-        for (int t = 0; t < kTeams; ++t) {
-            if ((int)threadIdx.x / L == t) {
+        __syncthreads();
+        for (int c = threadIdx.x; c < 2 * a.dim; c += kBlock) {
+            const int i = c < a.dim ? c : c - a.dim + L * NV * LEN;
+            float s = sums[0][i];
 #pragma unroll
-                for (int k = 0; k < NV; ++k) {
-#pragma unroll
-                    for (int j = 0; j < LEN; ++j) {
-                        float *p = sums + (k * LEN + j) * L + lane;
-                        p[0] = t ? p[0] + dw[k][j] : dw[k][j];
-                        p[L * NV * LEN] = t ? p[L * NV * LEN] + db[k][j] : db[k][j];
-                    }
-                }
-            }
-            __syncthreads();
-        }
-        if ((int)threadIdx.x < L) {
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-#pragma unroll
-                for (int j = 0; j < LEN; ++j) {
-                    if (k < NV - 1 || j >= at.skip) {
-                        const float *p = sums + (k * LEN + j) * L + lane;
-                        out[at.col[k] + j] = p[0];
-                        out[a.dim + at.col[k] + j] = p[L * NV * LEN];
-                    }
-                }
-            }
+            for (int t = 1; t < kBlock / 64; ++t) s += sums[t][i];
+            out[c] = s;
         }
     }
 }
@@ -444,7 +462,7 @@ Shape shape_of(int type, int dim, int most)
 int teams_of(const Shape &s) { return s.lanes > kThreads ? 1 : kThreads / s.lanes; }
 
 constexpr int kNormBlocks = 2048;  // 8 workgroups of 256 threads to each CU
-constexpr int kGradBlocks = 768;   // 3 to each CU: the registers allow no more
+constexpr int kGradBlocks = 512;   // 2 to each CU, what the registers allow
 
 unsigned blocks_of(int64_t n, const Shape &s, int most)
 {
