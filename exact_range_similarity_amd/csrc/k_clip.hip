@@ -9,11 +9,11 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
+constexpr int kVecs = (int)(kGradChunkBytes / 16) / kThreads;  // 16-byte vectors of a thread in a whole chunk
 
 __device__ __forceinline__ double block_sum(double v, double *red)
 {
     for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o, 64);
-    __syncthreads();
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
     double t = 0.;
@@ -21,15 +21,48 @@ __device__ __forceinline__ double block_sum(double v, double *red)
     return t;
 }
 
+// A chunk's vectors: thread t takes vectors t, t + kThreads, ...; the elements
+// after the last whole vector go to the first threads one by one.
+template <typename T>
+struct Chunk {
+    typedef Vec<T> V;
+    typename V::type v[kVecs];
+
+    __device__ __forceinline__ void load(const T *p, uint32_t n)
+    {
+        const uint32_t vecs = n / V::kLen;
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) {
+            const uint32_t i = threadIdx.x + k * kThreads;
+            if (i < vecs) v[k] = V::load(p + i * V::kLen);
+        }
+    }
+};
+
 template <typename T>
 __device__ __forceinline__ double chunk_squares(const T *p, uint32_t n)
 {
-    double s = 0.;
-    for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-        const double v = (double)(float)p[i];
-        s += v * v;
+    typedef Vec<T> V;
+    Chunk<T> c;
+    c.load(p, n);
+    const uint32_t vecs = n / V::kLen;
+    double s[2] = {0., 0.};
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+        if (threadIdx.x + k * kThreads < vecs) {
+#pragma unroll
+            for (int j = 0; j < V::kLen; ++j) {
+                const double x = (double)(float)c.v[k][j];
+                s[j & 1] += x * x;
+            }
+        }
     }
-    return s;
+    const uint32_t i = vecs * V::kLen + threadIdx.x;
+    if (i < n) {
+        const double x = (double)(float)p[i];
+        s[0] += x * x;
+    }
+    return s[0] + s[1];
 }
 
 __global__ __launch_bounds__(kThreads) void k_grad_squares(const GradChunk *chunks, uint32_t n, double *part)
@@ -47,7 +80,20 @@ __global__ __launch_bounds__(kThreads) void k_grad_squares(const GradChunk *chun
 template <typename T>
 __device__ __forceinline__ void chunk_scale(const T *in, T *out, uint32_t n, float f)
 {
-    for (uint32_t i = threadIdx.x; i < n; i += kThreads) out[i] = (T)(f * (float)in[i]);
+    typedef Vec<T> V;
+    typedef float fvec __attribute__((ext_vector_type(16 / sizeof(T))));
+    Chunk<T> c;
+    c.load(in, n);
+    const uint32_t vecs = n / V::kLen;
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+        const uint32_t i = threadIdx.x + k * kThreads;
+        if (i < vecs)
+            V::store(out + i * V::kLen,
+                     __builtin_convertvector(__builtin_convertvector(c.v[k], fvec) * f, typename V::type));
+    }
+    const uint32_t i = vecs * V::kLen + threadIdx.x;
+    if (i < n) out[i] = (T)(f * (float)in[i]);
 }
 
 __global__ __launch_bounds__(kThreads) void k_grad_scale(const GradChunk *chunks, uint32_t n, const double *part,
@@ -55,13 +101,18 @@ __global__ __launch_bounds__(kThreads) void k_grad_scale(const GradChunk *chunks
 {
     __shared__ double red[kWaves];
     double s = 0.;
-    for (int k = threadIdx.x; k < parts; k += kThreads) s += part[k];
+#pragma unroll
+    for (int k = 0; k < kGradParts / kThreads; ++k) {
+        const int i = threadIdx.x + k * kThreads;
+        s += i < parts ? part[i] : 0.;
+    }
     const double norm = sqrt(block_sum(s, red));
     if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
     const double bound = norm + 1e-6;
     const float f = (double)max_norm >= bound ? 1.f : (float)((double)max_norm / bound);
+    // from the end: what the other kernel read last is the likeliest to be in a cache
     for (uint32_t k = blockIdx.x; k < n; k += gridDim.x) {
-        const GradChunk c = chunks[k];
+        const GradChunk c = chunks[n - 1 - k];
         if (f == 1.f && c.in == c.out) continue;
         ERSJ_ELEM_SWITCH(c.type, T, chunk_scale((const T *)c.in, (T *)c.out, c.count, f))
     }
