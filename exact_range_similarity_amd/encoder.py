@@ -26,6 +26,7 @@ ENCODER_SYMBOLS = ("ersj_embed", "ersj_embed_grad", "ersj_embed_grad_work", "ers
 
 def declare(L):
     """Argument types of the entry points on the loaded library."""
+    global _lib
     vp, i32, i64, u64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float
     L.ersj_embed.argtypes = [vp, i32, i64, i32, i64, vp, i32, i64, f32, i64, vp, i32, i64, vp]
     L.ersj_embed_grad.argtypes = [vp, i32, i64, vp, i32, i64, f32, i64, vp, i32, i64, i32, i64, i32, vp, u64, vp]
@@ -39,57 +40,52 @@ def declare(L):
     L.ersj_grads_clip.argtypes = [vp, f32, vp, vp, u64, vp]
     L.ersj_grads_free.argtypes = [vp]
     L.ersj_grads_free.restype = None
+    _lib = L
 
 
-def _core():
-    import exact_range_similarity_amd as ersj
-    return ersj
+_lib = None  # the loaded library, set by declare
+# the current stream's handle without a Stream object, where torch offers it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _library():
+    if _lib is None:
+        from . import lib
+        lib()
+    return _lib
 
 
 def _check(rc):
     if rc:
-        _core()._check(rc)
+        from . import _check
+        _check(rc)
 
 
-class _Place:
-    """The device and stream of a call.  Inside, torch allocates on that
-    stream; tensors of another stream are kept until its work is done."""
-    __slots__ = ("raw", "side", "_ctx")
+def _elsewhere(device, stream):
+    """Whether a call for tensors on ``device`` has to change the current device
+    or stream first (``_run_elsewhere`` does)."""
+    if device.type != "cuda":
+        raise TypeError("the tensors must live on the GPU")
+    return stream is not None or device.index != torch.cuda.current_device()
 
-    def __init__(self, device, stream):
-        if device.type != "cuda":
-            raise TypeError("the tensors must live on the GPU")
-        self.side = None
+
+def _run_elsewhere(device, stream, tensors, call):
+    """``call()`` with the device and the stream current, so that torch
+    allocates there; the tensors are kept until the stream's work is done."""
+    with torch.cuda.device(device):
         if stream is None:
-            if device.index != torch.cuda.current_device():
-                self._ctx = torch.cuda.device(device)
-            else:
-                self._ctx = None
-            self.raw = torch.cuda.current_stream(device).cuda_stream
-        else:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            elif stream.device != device:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-            self._ctx = torch.cuda.stream(stream)
-            self.raw = stream.cuda_stream
-            self.side = stream
-
-    def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
-        return False
-
-    def keep(self, *tensors):
-        if self.side is not None:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.side)
+            return call()
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        elif stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        with torch.cuda.stream(stream):
+            result = call()
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+        return result
 
 
 def _type(t, what):
@@ -126,13 +122,12 @@ def _rows(t, what, dim=None):
     return n, ld
 
 
-def _same_device(device, **tensors):
-    for what, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{what} is on {t.device}, expected {device}")
+def _on(device, t, what):
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, expected {device}")
 
 
-def _param(t, what, dim, row_type):
+def _param(t, what, dim, row_type, device):
     """Type code of a weight or bias vector."""
     code = _type(t, what)
     if t.dim() != 1 or t.shape[0] != dim:
@@ -141,6 +136,7 @@ def _param(t, what, dim, row_type):
         raise ValueError(f"{what} must be contiguous")
     if code and code != row_type:
         raise TypeError(f"{what} must have the rows' type or float32")
+    _on(device, t, what)
     return code
 
 
@@ -160,14 +156,12 @@ def _padding(padding_idx):
     return int(padding_idx)
 
 
-def _output(out, what, shape, dtype, device):
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(out, torch.Tensor) or out.dtype != dtype or tuple(out.shape) != tuple(shape):
+def _given(out, what, shape, dtype, device):
+    """Row spacing of an output that the caller gave."""
+    if not isinstance(out, torch.Tensor) or out.dtype != dtype or out.shape != shape:
         raise ValueError(f"{what} must be a {dtype} tensor of shape {list(shape)}")
-    if out.device != device:
-        raise ValueError(f"{what} is on {out.device}, expected {device}")
-    return out
+    _on(device, out, what)
+    return _rows(out, what)[1]
 
 
 def embed(weight, ids, scale=1.0, padding_idx=None, dtype=None, out=None, stream=None):
@@ -186,22 +180,25 @@ def embed(weight, ids, scale=1.0, padding_idx=None, dtype=None, out=None, stream
 
 def _embed(weight, ids, scale, padding_idx, dtype, out, stream):
     wt = _type(weight, "weight")
+    device = weight.device
+    if _elsewhere(device, stream):
+        return _run_elsewhere(device, stream, (weight, ids, out),
+                              lambda: _embed(weight, ids, scale, padding_idx, dtype, out, None))
     if weight.dim() != 2:
         raise ValueError("weight must have two dimensions")
     rows, dim = weight.shape
-    device = weight.device
     dtype = weight.dtype if dtype is None else dtype
     if dtype not in _TYPES:
         raise TypeError("dtype must be float32, float16 or bfloat16")
-    with _Place(device, stream) as at:
-        ids = _ids(ids, device)
-        ldw = _rows(weight, "weight")[1]
-        out = _output(out, "out", ids.shape + (dim,), dtype, device)
-        ldo = _rows(out, "out")[1]
-        _check(_core().lib().ersj_embed(weight.data_ptr(), wt, rows, dim, ldw, ids.data_ptr(), _ID_TYPES[ids.dtype],
-                                        ids.numel(), scale, _padding(padding_idx), out.data_ptr(), _TYPES[dtype],
-                                        ldo, at.raw))
-        at.keep(weight, ids, out)
+    ids = _ids(ids, device)
+    shape = ids.shape + (dim,)
+    if out is None:
+        out, ldo = torch.empty(shape, dtype=dtype, device=device), dim
+    else:
+        ldo = _given(out, "out", shape, dtype, device)
+    _check(_library().ersj_embed(weight.data_ptr(), wt, rows, dim, _rows(weight, "weight")[1], ids.data_ptr(),
+                                 _ID_TYPES[ids.dtype], ids.numel(), scale, _padding(padding_idx), out.data_ptr(),
+                                 _TYPES[dtype], ldo, _raw_stream(device.index)))
     return out
 
 
@@ -211,25 +208,28 @@ def embed_grad(grad, ids, rows, scale=1.0, padding_idx=None, dtype=None, out=Non
     default) or float32.  With ``accumulate`` it is added to ``out``."""
     gt = _type(grad, "grad")
     device = grad.device
+    if _elsewhere(device, stream):
+        return _run_elsewhere(device, stream, (grad, ids, out),
+                              lambda: embed_grad(grad, ids, rows, scale, padding_idx, dtype, out, accumulate))
     dtype = dtype or (grad.dtype if out is None else out.dtype)
     if dtype not in _TYPES:
         raise TypeError("dtype must be float32, float16 or bfloat16")
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    with _Place(device, stream) as at:
-        ids = _ids(ids, device)
-        if grad.shape[:-1] != ids.shape:
-            raise ValueError(f"grad has the leading shape {list(grad.shape[:-1])}, ids {list(ids.shape)}")
-        n, dim = ids.numel(), grad.shape[-1]
-        ldg = _rows(grad, "grad")[1]
-        out = _output(out, "out", (rows, dim), dtype, device)
-        ldo = _rows(out, "out")[1]
-        L = _core().lib()
-        work = torch.empty(L.ersj_embed_grad_work(n, rows, dim), dtype=torch.uint8, device=device)
-        _check(L.ersj_embed_grad(grad.data_ptr(), gt, ldg, ids.data_ptr(), _ID_TYPES[ids.dtype], n, scale,
-                                 _padding(padding_idx), out.data_ptr(), _TYPES[dtype], rows, dim, ldo,
-                                 1 if accumulate else 0, work.data_ptr(), work.numel(), at.raw))
-        at.keep(grad, ids, out)
+    ids = _ids(ids, device)
+    if grad.shape[:-1] != ids.shape:
+        raise ValueError(f"grad has the leading shape {list(grad.shape[:-1])}, ids {list(ids.shape)}")
+    n, dim = ids.numel(), grad.shape[-1]
+    L = _library()
+    need = L.ersj_embed_grad_work(n, rows, dim)
+    work = torch.empty(need, dtype=torch.uint8, device=device)
+    if out is None:
+        out, ldo = torch.empty((rows, dim), dtype=dtype, device=device), dim
+    else:
+        ldo = _given(out, "out", (rows, dim), dtype, device)
+    _check(L.ersj_embed_grad(grad.data_ptr(), gt, _rows(grad, "grad")[1], ids.data_ptr(), _ID_TYPES[ids.dtype], n,
+                             scale, _padding(padding_idx), out.data_ptr(), _TYPES[dtype], rows, dim, ldo,
+                             1 if accumulate else 0, work.data_ptr(), need, _raw_stream(device.index)))
     return out
 
 
@@ -263,27 +263,29 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
 def _layer_norm(x, weight, bias, eps, out, stream):
     xt = _type(x, "x")
     device = x.device
-    with _Place(device, stream) as at:
-        n, ldx = _rows(x, "x")
-        dim = x.shape[-1]
-        pt = 0
-        if weight is not None:
-            pt = _param(weight, "weight", dim, xt)
-        if bias is not None:
-            bt = _param(bias, "bias", dim, xt)
-            if weight is not None and bt != pt:
-                raise TypeError("weight and bias must have one type")
-            pt = bt
-        _same_device(device, weight=weight, bias=bias)
-        out = _output(out, "out", x.shape, x.dtype, device)
-        ldy = _rows(out, "out")[1]
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
-        _check(_core().lib().ersj_layer_norm(x.data_ptr(), xt, n, dim, ldx,
-                                             None if weight is None else weight.data_ptr(),
-                                             None if bias is None else bias.data_ptr(), pt, eps, out.data_ptr(), ldy,
-                                             mean.data_ptr(), rstd.data_ptr(), at.raw))
-        at.keep(x, weight, bias, out)
+    if _elsewhere(device, stream):
+        return _run_elsewhere(device, stream, (x, weight, bias, out),
+                              lambda: _layer_norm(x, weight, bias, eps, out, None))
+    n, ldx = _rows(x, "x")
+    shape = x.shape
+    dim = shape[-1]
+    pt, w, b = 0, None, None
+    if weight is not None:
+        pt = _param(weight, "weight", dim, xt, device)
+        w = weight.data_ptr()
+    if bias is not None:
+        bt = _param(bias, "bias", dim, xt, device)
+        if w is not None and bt != pt:
+            raise TypeError("weight and bias must have one type")
+        pt, b = bt, bias.data_ptr()
+    if out is None:
+        out, ldy = torch.empty(shape, dtype=x.dtype, device=device), dim
+    else:
+        ldy = _given(out, "out", shape, x.dtype, device)
+    mean = torch.empty(shape[:-1], dtype=torch.float32, device=device)
+    rstd = torch.empty_like(mean)
+    _check(_library().ersj_layer_norm(x.data_ptr(), xt, n, dim, ldx, w, b, pt, eps, out.data_ptr(), ldy,
+                                      mean.data_ptr(), rstd.data_ptr(), _raw_stream(device.index)))
     return out, mean, rstd
 
 
@@ -296,38 +298,43 @@ def layer_norm_grad(grad, x, mean, rstd, weight=None, dtype=None, want_x=True, w
     if _type(grad, "grad") != xt:
         raise TypeError("grad must have the type of x")
     device = x.device
-    if grad.shape != x.shape:
-        raise ValueError(f"grad has the shape {list(grad.shape)}, x {list(x.shape)}")
-    with _Place(device, stream) as at:
-        n, ldx = _rows(x, "x")
-        ldg = _rows(grad, "grad")[1]
-        dim = x.shape[-1]
-        for what, t in (("mean", mean), ("rstd", rstd)):
-            if t.dtype != torch.float32 or t.shape != x.shape[:-1] or not t.is_contiguous():
-                raise ValueError(f"{what} must be a contiguous float32 tensor of shape {list(x.shape[:-1])}")
-        _same_device(device, grad=grad, mean=mean, rstd=rstd, weight=weight)
-        pt = 0 if weight is None else _param(weight, "weight", dim, xt)
+    if _elsewhere(device, stream):
+        return _run_elsewhere(device, stream, (grad, x, mean, rstd, weight),
+                              lambda: layer_norm_grad(grad, x, mean, rstd, weight, dtype, want_x, want_params))
+    shape = x.shape
+    if grad.shape != shape:
+        raise ValueError(f"grad has the shape {list(grad.shape)}, x {list(shape)}")
+    _on(device, grad, "grad")
+    n, ldx = _rows(x, "x")
+    dim = shape[-1]
+    for what, t in (("mean", mean), ("rstd", rstd)):
+        if t.dtype != torch.float32 or t.shape != shape[:-1] or not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous float32 tensor of shape {list(shape[:-1])}")
+        _on(device, t, what)
+    if weight is None:
+        dtype = dtype or torch.float32
+        pt, w = _TYPES.get(dtype), None
+        if pt is None or (pt and pt != xt):
+            raise TypeError("dtype must be the type of x or float32")
+    else:
+        pt, w = _param(weight, "weight", dim, xt, device), weight.data_ptr()
         if dtype is None:
-            dtype = torch.float32 if weight is None else weight.dtype
-        if weight is None:
-            pt = _TYPES[dtype]
-        elif _TYPES.get(dtype) != pt:
+            dtype = weight.dtype
+        elif dtype != weight.dtype:
             raise TypeError("the gradients of weight and bias have the weight's type")
-        gx = torch.empty(x.shape, dtype=x.dtype, device=device) if want_x else None
-        gw = gb = work = None
-        work_bytes = 0
-        L = _core().lib()
-        if want_params:
-            gw = torch.empty(dim, dtype=dtype, device=device)
-            gb = torch.empty(dim, dtype=dtype, device=device)
-            work_bytes = L.ersj_layer_norm_grad_work(n, dim)
-            work = torch.empty(work_bytes, dtype=torch.uint8, device=device)
-        _check(L.ersj_layer_norm_grad(grad.data_ptr(), ldg, x.data_ptr(), ldx, xt, n, dim, mean.data_ptr(),
-                                      rstd.data_ptr(), None if weight is None else weight.data_ptr(), pt,
-                                      gx.data_ptr() if want_x else None, dim, gw.data_ptr() if want_params else None,
-                                      gb.data_ptr() if want_params else None, work.data_ptr() if want_params else None,
-                                      work_bytes, at.raw))
-        at.keep(grad, x, mean, rstd, weight)
+    L = _library()
+    gx = torch.empty(shape, dtype=x.dtype, device=device) if want_x else None
+    gw = gb = work = None
+    need = 0
+    if want_params:
+        gw = torch.empty(dim, dtype=dtype, device=device)
+        gb = torch.empty_like(gw)
+        need = L.ersj_layer_norm_grad_work(n, dim)
+        work = torch.empty(need, dtype=torch.uint8, device=device)
+    _check(L.ersj_layer_norm_grad(grad.data_ptr(), _rows(grad, "grad")[1], x.data_ptr(), ldx, xt, n, dim,
+                                  mean.data_ptr(), rstd.data_ptr(), w, pt, gx.data_ptr() if want_x else None, dim,
+                                  gw.data_ptr() if want_params else None, gb.data_ptr() if want_params else None,
+                                  work.data_ptr() if want_params else None, need, _raw_stream(device.index)))
     return gx, gw, gb
 
 
@@ -372,24 +379,31 @@ class GradSet:
             _type(g, f"grads[{i}]")
             if not g.is_contiguous():
                 raise ValueError(f"grads[{i}] must be contiguous")
-            _same_device(self.grads[0].device, **{f"grads[{i}]": g})
+            _on(self.grads[0].device, g, f"grads[{i}]")
             if self.out is not None:
                 o = self.out[i]
                 if not isinstance(o, torch.Tensor) or o.dtype != g.dtype or o.shape != g.shape or not o.is_contiguous():
                     raise ValueError(f"out[{i}] must be a contiguous tensor of the type and shape of grads[{i}]")
-                _same_device(g.device, **{f"out[{i}]": o})
+                _on(g.device, o, f"out[{i}]")
         n = len(self.grads)
         self.device = self.grads[0].device
         ptrs = (ctypes.c_void_p * n)(*[g.data_ptr() for g in self.grads])
         outs = None if self.out is None else (ctypes.c_void_p * n)(*[o.data_ptr() for o in self.out])
         sizes = (ctypes.c_int64 * n)(*[g.numel() for g in self.grads])
         types = (ctypes.c_int32 * n)(*[_TYPES[g.dtype] for g in self.grads])
-        with _Place(self.device, stream) as at:
-            _check(_core().lib().ersj_grads_create(n, ptrs, outs, sizes, types, at.raw, ctypes.byref(self.handle)))
+
+        def create():
+            _check(_library().ersj_grads_create(n, ptrs, outs, sizes, types, _raw_stream(self.device.index),
+                                                ctypes.byref(self.handle)))
+
+        if _elsewhere(self.device, stream):
+            _run_elsewhere(self.device, stream, (), create)
+        else:
+            create()
 
     def free(self):
         if self.handle and self.handle.value:
-            _core().lib().ersj_grads_free(self.handle)
+            _library().ersj_grads_free(self.handle)
             self.handle = ctypes.c_void_p(None)
 
     def __del__(self):
@@ -404,9 +418,11 @@ def clip_grads(grads, max_norm, stream=None):
     most ``max_norm``; the norm before, as a float32 tensor of no dimensions.
     ``grads``: a ``GradSet``, or tensors to clip in place."""
     gs = grads if isinstance(grads, GradSet) else GradSet(grads, stream=stream)
-    with _Place(gs.device, stream) as at:
-        work = torch.empty(GRADS_WORK, dtype=torch.uint8, device=gs.device)
-        norm = torch.empty((), dtype=torch.float32, device=gs.device)
-        _check(_core().lib().ersj_grads_clip(gs.handle, max_norm, norm.data_ptr(), work.data_ptr(), GRADS_WORK, at.raw))
-        at.keep(*gs.grads, *(gs.out or ()))
+    device = gs.device
+    if _elsewhere(device, stream):
+        return _run_elsewhere(device, stream, gs.grads + (gs.out or []), lambda: clip_grads(gs, max_norm))
+    work = torch.empty(GRADS_WORK, dtype=torch.uint8, device=device)
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    _check(_library().ersj_grads_clip(gs.handle, max_norm, norm.data_ptr(), work.data_ptr(), GRADS_WORK,
+                                      _raw_stream(device.index)))
     return norm
