@@ -14,19 +14,62 @@ __device__ __forceinline__ int64_t id_at(const void *ids, int64_t t)
     return (int64_t)((const I *)ids)[t];
 }
 
-template <typename T, typename O, typename I>
+// Bound by memory: rows of the table in, rows of the output out.  A token
+// belongs to a team of L lanes, each with NV vectors of LEN elements (16
+// bytes of the output); a team takes tokens that lie a whole grid apart and
+// has the next token's row and the id after that on the way.  A vector that
+// would pass the row's end begins earlier, so that it ends with the row, and
+// writes its neighbour's values a second time.
+template <typename T, typename O, typename I, int LEN, int L, int NV>
 __global__ __launch_bounds__(kThreads) void k_embed(EmbedArgs a)
 {
-    for (int64_t t = blockIdx.x; t < a.n; t += gridDim.x) {
-        const int64_t id = id_at<I>(a.ids, t);
-        O *out = (O *)a.out + t * a.ld_out;
+    typedef T tvec __attribute__((ext_vector_type(LEN)));
+    typedef O ovec __attribute__((ext_vector_type(LEN)));
+    typedef float fvec __attribute__((ext_vector_type(LEN)));
+    struct __attribute__((packed, aligned(sizeof(T)))) tslot { tvec v; };
+    struct __attribute__((packed, aligned(sizeof(O)))) oslot { ovec v; };
+    const int lane = threadIdx.x & (L - 1);
+    const int c0 = blockIdx.y * (L * NV * LEN);
+    int col[NV];
+    bool on[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int c = c0 + (k * L + lane) * LEN;
+        on[k] = c < a.dim;
+        col[k] = c + LEN <= a.dim ? c : a.dim - LEN;
+    }
+    const int64_t step = (int64_t)gridDim.x * (kThreads / L);
+    int64_t t = (int64_t)blockIdx.x * (kThreads / L) + threadIdx.x / L;
+    if (t >= a.n) return;
+    auto id_of = [&](int64_t at) { return id_at<I>(a.ids, at < a.n ? at : a.n - 1); };
+    auto load = [&](int64_t id, tvec (&x)[NV]) {
+        // the first row in the place of one that is not used
+        const bool use = id >= 0 && id < a.rows && id != a.padding_id;
+        const T *row = (const T *)a.table + (use ? id : 0) * a.ld_table;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (on[k]) x[k] = ((const tslot *)(row + col[k]))->v;
+    };
+    int64_t id = id_of(t), next_id = id_of(t + step);
+    tvec x[NV], y[NV];
+    load(id, x);
+    while (true) {
+        const int64_t after = id_of(t + 2 * step);
+        const bool more = t + step < a.n;
+        if (more) load(next_id, y);
         const bool pad = id >= 0 && id == a.padding_id, bad = id < 0 || id >= a.rows;
-        const T *row = (const T *)a.table + (bad ? 0 : id) * a.ld_table;
-        for (int c = threadIdx.x; c < a.dim; c += kThreads) {
-            float v = pad ? 0.f : __builtin_nanf("");
-            if (!pad && !bad) v = a.scale * (float)row[c];
-            out[c] = (O)v;
+        O *out = (O *)a.out + t * a.ld_out;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            fvec v = __builtin_convertvector(x[k], fvec) * a.scale;
+            if (pad || bad) v = (fvec)(pad ? 0.f : __builtin_nanf(""));
+            if (on[k]) ((oslot *)(out + col[k]))->v = __builtin_convertvector(v, ovec);
+            x[k] = y[k];
         }
+        if (!more) break;
+        t += step;
+        id = next_id;
+        next_id = after;
     }
 }
 
@@ -645,13 +688,53 @@ uint64_t up256(uint64_t b) { return (b + 255) & ~(uint64_t)255; }
 
 }  // namespace
 
+constexpr int kEmbedBlocks = 2048;  // 8 workgroups to each CU
+
+template <typename T, typename O, typename I>
+static void run_embed(const EmbedArgs &a, hipStream_t s)
+{
+    // the smallest team of at least eight lanes that covers the row with up to
+    // four vectors a lane; longer rows are split over the grid's second axis
+    constexpr int kLen = 16 / sizeof(O);
+    const int len = a.dim < kLen ? 1 : kLen;
+    const int vecs = (a.dim + len - 1) / len;
+    int lanes = 8;
+    while (lanes < 64 && lanes * 4 < vecs) lanes *= 2;
+    const int nv = (vecs + lanes - 1) / lanes;
+    const int64_t need = (a.n + kThreads / lanes - 1) / (kThreads / lanes);
+    const dim3 grid((unsigned)(need < kEmbedBlocks ? need : kEmbedBlocks), nv > 4 ? (unsigned)((nv + 3) / 4) : 1u);
+    const dim3 block(kThreads);
+#define CASE(L, NV)                                                     \
+    case L * 8 + NV:                                                    \
+        k_embed<T, O, I, kLen, L, NV><<<grid, block, 0, s>>>(a);        \
+        break;
+    if (len == 1) {
+        k_embed<T, O, I, 1, 8, 1><<<grid, block, 0, s>>>(a);
+        return;
+    }
+    switch (lanes * 8 + (nv < 4 ? nv : 4)) {
+        CASE(8, 1) CASE(8, 2) CASE(8, 3) CASE(8, 4) CASE(16, 3) CASE(16, 4) CASE(32, 3) CASE(32, 4) CASE(64, 3)
+        CASE(64, 4)
+    }
+#undef CASE
+}
+
 hipError_t launch_embed(const EmbedArgs &a, hipStream_t s)
 {
     if (a.n == 0) return hipSuccess;
-    const dim3 grid((unsigned)(a.n < 65536 ? a.n : 65536)), block(kThreads);
-    ERSJ_ELEM_SWITCH(a.table_type, T, ERSJ_ELEM_SWITCH(a.out_type, O,
-        if (a.id_type) k_embed<T, O, int64_t><<<grid, block, 0, s>>>(a);
-        else k_embed<T, O, int32_t><<<grid, block, 0, s>>>(a)))
+#define RUN(T, O)                                      \
+    do {                                               \
+        if (a.id_type) run_embed<T, O, int64_t>(a, s); \
+        else run_embed<T, O, int32_t>(a, s);           \
+    } while (0)
+    switch (a.table_type * 4 + a.out_type) {
+    case kF32 * 4 + kF32: RUN(float, float); break;
+    case kF32 * 4 + kF16: RUN(float, f16_t); break;
+    case kF32 * 4 + kBF16: RUN(float, bf16_t); break;
+    case kF16 * 4 + kF16: RUN(f16_t, f16_t); break;
+    default: RUN(bf16_t, bf16_t); break;
+    }
+#undef RUN
     return hipGetLastError();
 }
 
