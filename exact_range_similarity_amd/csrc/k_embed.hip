@@ -77,9 +77,11 @@ __global__ __launch_bounds__(kThreads) void k_embed(EmbedArgs a)
 //
 // Stable least-significant-digit radix sort of (key, t), key = id or `rows`
 // for tokens that add nothing.  A workgroup takes a run of consecutive
-// entries: one kernel counts the run's digits, the next ranks and moves its
-// entries.  With few runs the second kernel derives its own offsets from the
-// counts of all runs; with more, a scan kernel lies between.  Tokens that fit
+// entries: one kernel counts the runs' digits, the next ranks a run's entries
+// and moves them, to offsets that it derives from the counts of all runs.
+// With many runs a scan kernel lies between.  (Adding each moved entry to the
+// next pass's counts instead of counting anew costs more: device-wide atomics,
+// 44 us for a million entries against 5 us for the kernel.)  Tokens that fit
 // one workgroup are sorted by it in one kernel, through LDS.
 
 constexpr int kSortThreads = 1024;
@@ -87,8 +89,7 @@ constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kMaxDigitBits = 9;
 constexpr int kMaxDigits = 1 << kMaxDigitBits;
 constexpr int kScanRuns = 64;       // more runs than this are scanned by a kernel of their own
-constexpr int kLocalItems = 4;      // entries per thread of the one-workgroup sort
-constexpr int kLocalMax = kSortThreads * kLocalItems;
+constexpr int kLocalMax = kSortThreads * 4;  // entries of the one-workgroup sort
 
 struct SortPlan {
     int passes, bits;
@@ -103,7 +104,9 @@ SortPlan sort_plan(int64_t n, int64_t rows)
     SortPlan p;
     p.passes = (kb + kMaxDigitBits - 1) / kMaxDigitBits;
     p.bits = (kb + p.passes - 1) / p.passes;
-    p.items = n <= (int64_t)kScanRuns * 2 * kSortThreads ? 2 : 4;
+    // short runs while their counts need no scan: more workgroups, fewer steps each
+    const int64_t unit = (int64_t)kScanRuns * kSortThreads;
+    p.items = n <= unit ? 1 : n <= 2 * unit ? 2 : 4;
     const int64_t run = (int64_t)p.items * kSortThreads;
     p.runs = (n + run - 1) / run;
     return p;
@@ -111,17 +114,17 @@ SortPlan sort_plan(int64_t n, int64_t rows)
 
 struct SortSource {
     const void *ids;
-    const uint32_t *keys, *pos;  // null on the first pass
+    const uint2 *entries;  // (key, t); null on the first pass
     int64_t padding_id, rows;
     uint32_t n;
 };
 
 template <typename I>
-__device__ __forceinline__ uint32_t sort_key(const SortSource &s, uint32_t i)
+__device__ __forceinline__ uint2 sort_entry(const SortSource &s, uint32_t i)
 {
-    if (s.keys) return s.keys[i];
+    if (s.entries) return s.entries[i];
     const int64_t id = id_at<I>(s.ids, i);
-    return id < 0 || id >= s.rows || id == s.padding_id ? (uint32_t)s.rows : (uint32_t)id;
+    return make_uint2(id < 0 || id >= s.rows || id == s.padding_id ? (uint32_t)s.rows : (uint32_t)id, i);
 }
 
 template <typename I>
@@ -135,7 +138,7 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_count(SortSource s, int s
     const uint64_t i0 = (uint64_t)blockIdx.x * run;
     const uint32_t i1 = (uint32_t)(i0 + run < s.n ? i0 + run : s.n);
     for (uint32_t i = (uint32_t)i0 + threadIdx.x; i < i1; i += kSortThreads)
-        atomicAdd(&cnt[(sort_key<I>(s, i) >> shift) & (nd - 1)], 1u);
+        atomicAdd(&cnt[(sort_entry<I>(s, i).x >> shift) & (nd - 1)], 1u);
     __syncthreads();
     if ((int)threadIdx.x < nd) counts[(size_t)blockIdx.x * nd + threadIdx.x] = cnt[threadIdx.x];
 }
@@ -205,29 +208,25 @@ __device__ __forceinline__ void wave_ranks(const uint32_t (&dg)[ITEMS], const bo
 
 template <typename I, int ITEMS>
 __global__ __launch_bounds__(kSortThreads) void k_sort_scatter(SortSource s, int shift, int bits,
-                                                               const uint32_t *counts, bool scanned,
-                                                               uint32_t *keys_out, uint32_t *pos_out)
+                                                               const uint32_t *counts, bool scanned, uint2 *out)
 {
     __shared__ uint32_t cnt[kSortWaves][kMaxDigits];
     __shared__ uint32_t halves[2][kSortThreads];
     __shared__ uint32_t wsum[kMaxDigits / 64];
     const uint32_t nd = 1u << bits, tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-    const uint32_t run = kSortThreads * ITEMS;
-    for (uint32_t k = tid; k < kSortWaves * kMaxDigits; k += kSortThreads) (&cnt[0][0])[k] = 0;
+    constexpr uint32_t run = kSortThreads * ITEMS;
 
     // a wave's entries are consecutive
-    uint32_t key[ITEMS], at[ITEMS], dg[ITEMS], rank[ITEMS];
+    uint2 e[ITEMS];
+    uint32_t dg[ITEMS], rank[ITEMS];
     bool ok[ITEMS];
     const uint64_t i0 = (uint64_t)blockIdx.x * run + w * (64 * ITEMS) + lane;
 #pragma unroll
     for (int r = 0; r < ITEMS; ++r) {
         const uint64_t i = i0 + r * 64;
         ok[r] = i < s.n;
-        key[r] = ok[r] ? sort_key<I>(s, (uint32_t)i) : 0;
-        at[r] = ok[r] && s.pos ? s.pos[i] : (uint32_t)i;
-        dg[r] = (key[r] >> shift) & (nd - 1);
+        e[r] = sort_entry<I>(s, ok[r] ? (uint32_t)i : s.n - 1);
     }
-
     // offsets: all smaller digits, then the same digit in earlier runs
     uint32_t total = 0, before = 0;
     if (scanned) {
@@ -238,16 +237,27 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_scatter(SortSource s, int
     } else {
         // kSortThreads / nd threads share a digit's runs
         const uint32_t k = tid & (nd - 1), part = tid >> bits, parts = kSortThreads >> bits;
-#pragma unroll 8
-        for (uint32_t g = part; g < gridDim.x; g += parts) {
-            const uint32_t c = counts[(size_t)g * nd + k];
-            total += c;
-            before += g < blockIdx.x ? c : 0;
+        for (uint32_t g = part; g < gridDim.x; g += parts * 8) {
+            uint32_t c[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const uint32_t q = g + u * parts;
+                c[u] = q < gridDim.x ? counts[(size_t)q * nd + k] : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                total += c[u];
+                before += g + u * parts < blockIdx.x ? c[u] : 0;
+            }
         }
         halves[0][tid] = total;
         halves[1][tid] = before;
+    }
+    for (uint32_t k = tid; k < kSortWaves * nd; k += kSortThreads) cnt[k >> bits][k & (nd - 1)] = 0;
+    if (!scanned) {
         __syncthreads();
         if (tid < nd) {
+            const uint32_t parts = kSortThreads >> bits;
             for (uint32_t j = 1; j < parts; ++j) {
                 total += halves[0][j * nd + tid];
                 before += halves[1][j * nd + tid];
@@ -257,69 +267,66 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_scatter(SortSource s, int
     }
     uint32_t base = digit_prefix(total, wsum) + before;  // its barriers also publish the cleared counters
 
+#pragma unroll
+    for (int r = 0; r < ITEMS; ++r) dg[r] = (e[r].x >> shift) & (nd - 1);
     wave_ranks<ITEMS>(dg, ok, bits, cnt[w], rank);
     __syncthreads();
     if (tid < nd) {
+        uint32_t c[kSortWaves];
+#pragma unroll
+        for (int j = 0; j < kSortWaves; ++j) c[j] = cnt[j][tid];
 #pragma unroll
         for (int j = 0; j < kSortWaves; ++j) {
-            const uint32_t c = cnt[j][tid];
             cnt[j][tid] = base;
-            base += c;
+            base += c[j];
         }
     }
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < ITEMS; ++r) {
-        if (ok[r]) {
-            const uint32_t to = cnt[w][dg[r]] + rank[r];
-            keys_out[to] = key[r];
-            pos_out[to] = at[r];
-        }
-    }
+    for (int r = 0; r < ITEMS; ++r)
+        if (ok[r]) out[cnt[w][dg[r]] + rank[r]] = e[r];
 }
 
-// The whole sort of up to kLocalMax tokens by one workgroup.
-template <typename I>
-__global__ __launch_bounds__(kSortThreads) void k_sort_local(SortSource s, int passes, int bits, uint32_t *keys_out,
-                                                             uint32_t *pos_out)
+// The whole sort of up to kSortThreads * ITEMS tokens by one workgroup.
+template <typename I, int ITEMS>
+__global__ __launch_bounds__(kSortThreads) void k_sort_local(SortSource s, int passes, int bits, uint2 *out)
 {
     __shared__ uint32_t cnt[kSortWaves][kMaxDigits];
-    __shared__ uint32_t keys[kLocalMax], pos[kLocalMax];
+    __shared__ uint2 sorted[kSortThreads * ITEMS];
     __shared__ uint32_t wsum[kMaxDigits / 64];
-    constexpr int ITEMS = kLocalItems;
     const uint32_t nd = 1u << bits, tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-    uint32_t key[ITEMS], at[ITEMS], dg[ITEMS], rank[ITEMS];
+    uint2 e[ITEMS];
+    uint32_t dg[ITEMS], rank[ITEMS];
     bool ok[ITEMS];
-    // the same stretch for every wave, as short as the tokens allow
-    const uint32_t per = (s.n + kSortThreads - 1) / kSortThreads;
-    const uint32_t i0 = w * 64 * per + lane;
+    const uint32_t i0 = w * 64 * ITEMS + lane;
 #pragma unroll
     for (int r = 0; r < ITEMS; ++r) {
         const uint32_t i = i0 + r * 64;
-        ok[r] = r < (int)per && i < s.n;
-        key[r] = ok[r] ? sort_key<I>(s, i) : 0;
-        at[r] = i;
+        ok[r] = i < s.n;
+        e[r] = sort_entry<I>(s, ok[r] ? i : s.n - 1);
     }
     for (int p = 0; p < passes; ++p) {
-        for (uint32_t k = tid; k < kSortWaves * kMaxDigits; k += kSortThreads) (&cnt[0][0])[k] = 0;
+        for (uint32_t k = tid; k < kSortWaves * nd; k += kSortThreads) cnt[k >> bits][k & (nd - 1)] = 0;
         __syncthreads();
 #pragma unroll
-        for (int r = 0; r < ITEMS; ++r) dg[r] = (key[r] >> (p * bits)) & (nd - 1);
+        for (int r = 0; r < ITEMS; ++r) dg[r] = (e[r].x >> (p * bits)) & (nd - 1);
         wave_ranks<ITEMS>(dg, ok, bits, cnt[w], rank);
         __syncthreads();
-        uint32_t total = 0;
+        uint32_t c[kSortWaves], total = 0;
         if (tid < nd) {
 #pragma unroll
             for (int j = 0; j < kSortWaves; ++j) {
-                const uint32_t c = cnt[j][tid];
-                cnt[j][tid] = total;
-                total += c;
+                c[j] = cnt[j][tid];
+                total += c[j];
             }
         }
-        const uint32_t base = digit_prefix(total, wsum);
+        uint32_t base = digit_prefix(total, wsum);
         if (tid < nd) {
 #pragma unroll
-            for (int j = 0; j < kSortWaves; ++j) cnt[j][tid] += base;
+            for (int j = 0; j < kSortWaves; ++j) {
+                cnt[j][tid] = base;
+                base += c[j];
+            }
         }
         __syncthreads();
         const bool last = p == passes - 1;
@@ -327,23 +334,14 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_local(SortSource s, int p
         for (int r = 0; r < ITEMS; ++r) {
             if (!ok[r]) continue;
             const uint32_t to = cnt[w][dg[r]] + rank[r];
-            if (last) {
-                keys_out[to] = key[r];
-                pos_out[to] = at[r];
-            } else {
-                keys[to] = key[r];
-                pos[to] = at[r];
-            }
+            if (last) out[to] = e[r];
+            else sorted[to] = e[r];
         }
         if (last) break;
         __syncthreads();
 #pragma unroll
-        for (int r = 0; r < ITEMS; ++r) {
-            if (ok[r]) {
-                key[r] = keys[i0 + r * 64];
-                at[r] = pos[i0 + r * 64];
-            }
-        }
+        for (int r = 0; r < ITEMS; ++r)
+            if (ok[r]) e[r] = sorted[i0 + r * 64];
     }
 }
 
@@ -365,7 +363,7 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_local(SortSource s, int p
 
 constexpr int kSnap = 8;
 constexpr int kShareMin = 16;
-constexpr int kMaxShares = 8192;  // waves of the sum kernel: 8 per SIMD
+constexpr int kMaxShares = 5120;  // waves of the sum kernel: 5 per SIMD, what its registers allow
 enum { kFirstCut = 1, kInside = 2 };
 
 // What a share leaves to the join: whether it ends a row begun before it
@@ -401,17 +399,17 @@ struct Cut {
 
 // The cut at place `at`, by the 32 lanes of each half of the wave for its own
 // `at`: a 32-way search, then a look at the rest of the row that it falls in.
-__device__ __forceinline__ Cut find_cut(const uint32_t *keys, uint32_t n, uint32_t rows, int64_t at)
+__device__ __forceinline__ Cut find_cut(const uint2 *entries, uint32_t n, uint32_t rows, int64_t at)
 {
     const int lane = threadIdx.x & 31;
     const int half = (threadIdx.x & 32);
-    // least i with i + keys[i] >= at, in [lo, hi]
+    // least i with i + key[i] >= at, in [lo, hi]
     int64_t lo = at > rows ? at - rows : 0, hi = at < n ? at : n;
     while (__ballot(lo < hi)) {
         const int64_t step = (hi - lo + 31) >> 5;
         const int64_t i = lo + (int64_t)lane * step;
         bool less = false;
-        if (lo < hi && i < hi) less = i + (int64_t)keys[i] < at;
+        if (lo < hi && i < hi) less = i + (int64_t)entries[i].x < at;
         const uint32_t m = (uint32_t)(__ballot(less) >> half);
         if (lo < hi) {
             // `less` holds for the first c probes: the answer lies after
@@ -426,9 +424,11 @@ __device__ __forceinline__ Cut find_cut(const uint32_t *keys, uint32_t n, uint32
     r.i = (uint32_t)lo;
     r.v = (uint32_t)(at - lo);
     r.inside = false;
-    const bool begun = r.i > 0 && r.v < rows && keys[r.i - 1] == r.v;
+    if (n == 0) return r;
     const uint32_t j = r.i + lane;
-    const bool same = begun && j < n && keys[j] == r.v;
+    const uint32_t prev = entries[r.i ? r.i - 1 : 0].x, here = entries[j < n ? j : n - 1].x;
+    const bool begun = r.i > 0 && r.v < rows && prev == r.v;
+    const bool same = begun && j < n && here == r.v;
     const uint32_t m = (uint32_t)(__ballot(same) >> half);
     if (begun) {
         if (__popc(m) >= kSnap) r.inside = true;
@@ -444,8 +444,8 @@ __device__ __forceinline__ Cut find_cut(const uint32_t *keys, uint32_t n, uint32
 // the row's end begins LEN before it instead; the columns it shares with its
 // neighbour hold the same sums.
 template <typename T, typename O, int LEN, int NV>
-__global__ __launch_bounds__(kThreads) void k_embed_grad_sum(EmbedGradArgs a, const uint32_t *keys,
-                                                             const uint32_t *pos, int64_t share, uint32_t shares,
+__global__ __launch_bounds__(kThreads) void k_embed_grad_sum(EmbedGradArgs a, const uint2 *entries,
+                                                             int64_t share, uint32_t shares,
                                                              float *part, Note *notes)
 {
     typedef T tvec __attribute__((ext_vector_type(LEN)));
@@ -464,7 +464,7 @@ __global__ __launch_bounds__(kThreads) void k_embed_grad_sum(EmbedGradArgs a, co
 
     int64_t at = (int64_t)(w + (lane >> 5)) * share;
     if (at > total) at = total;
-    const Cut cut = find_cut(keys, n, rows, at);
+    const Cut cut = find_cut(entries, n, rows, at);
     uint32_t i = __builtin_amdgcn_readlane(cut.i, 0), v = __builtin_amdgcn_readlane(cut.v, 0);
     const uint32_t v0 = v;
     const uint32_t i1 = __builtin_amdgcn_readlane(cut.i, 32);
@@ -524,8 +524,9 @@ __global__ __launch_bounds__(kThreads) void k_embed_grad_sum(EmbedGradArgs a, co
         // up to 64 tokens, one to a lane: key and place of the row of grad in bytes
         uint32_t m = i1 - i < 64 ? i1 - i : 64;
         const uint32_t mine = i + (lane < (int)m ? lane : 0);
-        const uint32_t kk = keys[mine];
-        const uint64_t place = (uint64_t)pos[mine] * (uint64_t)a.ld_grad * sizeof(T);
+        const uint2 e = entries[mine];
+        const uint32_t kk = e.x;
+        const uint64_t place = (uint64_t)e.y * (uint64_t)a.ld_grad * sizeof(T);
         const uint32_t place_lo = (uint32_t)place, place_hi = (uint32_t)(place >> 32);
         // tokens that add nothing come last
         const uint32_t real = (uint32_t)__popcll(__ballot(lane < (int)m && kk < rows));
@@ -578,7 +579,7 @@ __global__ __launch_bounds__(kThreads) void k_embed_grad_sum(EmbedGradArgs a, co
 // the parts in order.  More than kJoinAlone parts are added by the whole
 // workgroup: its waves form groups that cover a block of columns, each group
 // adds an equal stretch of the parts, and the groups' sums are added in order.
-constexpr int kJoinThreads = 1024;
+constexpr int kJoinThreads = 512;
 constexpr int kJoinWaves = kJoinThreads / 64;
 constexpr uint32_t kJoinAlone = 16;
 
@@ -633,14 +634,24 @@ __global__ __launch_bounds__(kJoinThreads) void k_embed_grad_join(EmbedGradArgs 
 
     uint32_t parts = 0, b = w;
     const Note note = w < shares ? notes[w] : Note{0, 0};
+    // whether each of the 256 shares before b lies inside one row; for w without
+    // waiting for its own note
+    uint32_t inside[4];
+    auto look = [&]() {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int64_t q = (int64_t)b - 1 - 64 * k - lane;
+            inside[k] = notes[q < 0 || b > shares ? 0 : q].flags & (q < 0 ? 0 : kInside);
+        }
+    };
+    look();
     if (note.flags & kFirstCut) {
-        // b: the first share before w that is not all inside the row, found 256 shares at a time
+        // b: the first share before w that is not all inside the row
         for (bool more = true; more;) {
             uint64_t m[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int64_t q = (int64_t)b - 1 - 64 * k - lane;
-                m[k] = __ballot(q < 0 || !(notes[q < 0 ? 0 : q].flags & kInside));
+                m[k] = __ballot(!inside[k]);
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -651,6 +662,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_embed_grad_join(EmbedGradArgs 
                 } else
                     b -= 64;
             }
+            if (more) look();
         }
         parts = w - b + 1;
         if (parts <= kJoinAlone)
@@ -742,36 +754,35 @@ static uint64_t count_bytes(const SortPlan &p) { return up256(((uint64_t)4 << p.
 
 uint64_t embed_grad_work(int64_t n, int64_t rows, int dim)
 {
+    const SortPlan p = sort_plan(n, rows);
     const SumPlan q = sum_plan(n, rows, dim);
-    return 4 * up256(4 * (uint64_t)n) + count_bytes(sort_plan(n, rows)) + up256(q.shares * sizeof(Note)) +
+    return 2 * up256(8 * (uint64_t)n) + count_bytes(p) + up256(q.shares * sizeof(Note)) +
            (uint64_t)q.shares * 2 * 4 * (uint64_t)dim;
 }
 
 template <typename I>
-static void launch_sort(const SortPlan &p, SortSource &src, uint32_t *const (&buf)[4], uint32_t *counts, hipStream_t s)
+static void launch_sort(const SortPlan &p, SortSource &src, uint2 *const (&buf)[2], uint32_t *counts, hipStream_t s)
 {
     const dim3 block(kSortThreads);
+    if (src.n <= (uint32_t)kSortThreads) k_sort_local<I, 1><<<dim3(1), block, 0, s>>>(src, p.passes, p.bits, buf[0]);
+    else if (src.n <= (uint32_t)kLocalMax) k_sort_local<I, 4><<<dim3(1), block, 0, s>>>(src, p.passes, p.bits, buf[0]);
     if (src.n <= (uint32_t)kLocalMax) {
-        k_sort_local<I><<<dim3(1), block, 0, s>>>(src, p.passes, p.bits, buf[0], buf[1]);
-        src.keys = buf[0];
-        src.pos = buf[1];
+        src.entries = buf[0];
         return;
     }
     const dim3 grid((unsigned)p.runs);
     const bool scan = p.runs > kScanRuns;
     for (int k = 0; k < p.passes; ++k) {
-        uint32_t *ko = buf[2 * (k & 1)], *po = buf[2 * (k & 1) + 1];
+        uint2 *out = buf[k & 1];
         const int shift = k * p.bits;
         k_sort_count<I><<<grid, block, 0, s>>>(src, shift, p.bits, (uint32_t)(p.items * kSortThreads), counts);
         if (scan)
             k_sort_scan<<<dim3(((1u << p.bits) + kWaves - 1) / kWaves), dim3(kThreads), 0, s>>>(
                 counts, (uint32_t)p.runs, p.bits);
-        if (p.items == 2)
-            k_sort_scatter<I, 2><<<grid, block, 0, s>>>(src, shift, p.bits, counts, scan, ko, po);
-        else
-            k_sort_scatter<I, 4><<<grid, block, 0, s>>>(src, shift, p.bits, counts, scan, ko, po);
-        src.keys = ko;
-        src.pos = po;
+        if (p.items == 1) k_sort_scatter<I, 1><<<grid, block, 0, s>>>(src, shift, p.bits, counts, scan, out);
+        else if (p.items == 2) k_sort_scatter<I, 2><<<grid, block, 0, s>>>(src, shift, p.bits, counts, scan, out);
+        else k_sort_scatter<I, 4><<<grid, block, 0, s>>>(src, shift, p.bits, counts, scan, out);
+        src.entries = out;
     }
 }
 
@@ -779,11 +790,11 @@ hipError_t launch_embed_grad(const EmbedGradArgs &a, hipStream_t s)
 {
     const SortPlan p = sort_plan(a.n, a.rows);
     char *at = (char *)a.work;
-    uint32_t *buf[4];
-    for (int k = 0; k < 4; ++k, at += up256(4 * (uint64_t)a.n)) buf[k] = (uint32_t *)at;
+    uint2 *buf[2];
+    for (int k = 0; k < 2; ++k, at += up256(8 * (uint64_t)a.n)) buf[k] = (uint2 *)at;
     uint32_t *counts = (uint32_t *)at;
     at += count_bytes(p);
-    SortSource src{a.ids, nullptr, nullptr, a.padding_id, a.rows, (uint32_t)a.n};
+    SortSource src{a.ids, nullptr, a.padding_id, a.rows, (uint32_t)a.n};
     if (a.n) {
         if (a.id_type) launch_sort<int64_t>(p, src, buf, counts, s);
         else launch_sort<int32_t>(p, src, buf, counts, s);
@@ -796,11 +807,11 @@ hipError_t launch_embed_grad(const EmbedGradArgs &a, hipStream_t s)
 #define SUM(T, O)                                                                                                  \
     do {                                                                                                           \
         if (a.dim < len)                                                                                           \
-            k_embed_grad_sum<T, O, 1, 1><<<grid, block, 0, s>>>(a, src.keys, src.pos, q.share, (uint32_t)q.shares, \
+            k_embed_grad_sum<T, O, 1, 1><<<grid, block, 0, s>>>(a, src.entries, q.share, (uint32_t)q.shares, \
                                                                 part, notes);                                      \
         else                                                                                                       \
             k_embed_grad_sum<T, O, 16 / sizeof(T), sizeof(T) / 2><<<grid, block, 0, s>>>(                          \
-                a, src.keys, src.pos, q.share, (uint32_t)q.shares, part, notes);                                   \
+                a, src.entries, q.share, (uint32_t)q.shares, part, notes);                                   \
     } while (0)
     switch (a.grad_type * 4 + a.out_type) {
     case kF32 * 4 + kF32: SUM(float, float); break;

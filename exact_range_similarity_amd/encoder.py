@@ -48,6 +48,8 @@ _lib = None  # the loaded library, set by declare
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
 
 def _library():
     if _lib is None:
@@ -67,7 +69,7 @@ def _elsewhere(device, stream):
     or stream first (``_run_elsewhere`` does)."""
     if device.type != "cuda":
         raise TypeError("the tensors must live on the GPU")
-    return stream is not None or device.index != torch.cuda.current_device()
+    return stream is not None or device.index != _current_device()
 
 
 def _run_elsewhere(device, stream, tensors, call):
@@ -89,25 +91,28 @@ def _run_elsewhere(device, stream, tensors, call):
 
 
 def _type(t, what):
-    if not isinstance(t, torch.Tensor) or t.dtype not in _TYPES:
-        raise TypeError(f"{what} must be a float32, float16 or bfloat16 tensor")
-    return _TYPES[t.dtype]
+    if isinstance(t, torch.Tensor):
+        code = _TYPES.get(t.dtype)
+        if code is not None:
+            return code
+    raise TypeError(f"{what} must be a float32, float16 or bfloat16 tensor")
 
 
 def _rows(t, what, dim=None):
     """(rows, spacing) of a tensor of rows along its last dimension."""
-    if t.dim() < 1:
+    shape = t.shape
+    if not shape:
         raise ValueError(f"{what} must have at least one dimension")
-    d = t.shape[-1]
+    d = shape[-1]
     if dim is not None and d != dim:
         raise ValueError(f"{what} has rows of {d}, {dim} are expected")
     n = t.numel() // d if d else 0
-    if n <= 1 or t.is_contiguous():
-        if d > 1 and n and t.stride(-1) != 1:
-            raise ValueError(f"{what} rows must be contiguous (stride(-1) == 1)")
+    if t.is_contiguous():
         return n, d
     if d > 1 and t.stride(-1) != 1:
         raise ValueError(f"{what} rows must be contiguous (stride(-1) == 1)")
+    if n == 1:
+        return n, d
     ld = None
     for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
         if size == 1:
@@ -130,9 +135,9 @@ def _on(device, t, what):
 def _param(t, what, dim, row_type, device):
     """Type code of a weight or bias vector."""
     code = _type(t, what)
-    if t.dim() != 1 or t.shape[0] != dim:
+    if t.shape != (dim,):
         raise ValueError(f"{what} must have the shape [{dim}]")
-    if dim > 1 and t.stride(0) != 1:
+    if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
     if code and code != row_type:
         raise TypeError(f"{what} must have the rows' type or float32")
@@ -171,7 +176,7 @@ def embed(weight, ids, scale=1.0, padding_idx=None, dtype=None, out=None, stream
     default; a float32 weight gives any.  Places that hold ``padding_idx`` get
     zeros; any other id outside the table gets NaN.  Differentiable with
     respect to ``weight`` (the gradient is ``embed_grad``'s)."""
-    if torch.is_grad_enabled() and weight.requires_grad:
+    if weight.requires_grad and torch.is_grad_enabled():
         if out is not None:
             raise ValueError("out cannot be given where a gradient is wanted")
         return _Embed.apply(weight, ids, scale, padding_idx, dtype, stream)
@@ -252,8 +257,8 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
     rstd float32 of shape ``x.shape[:-1]``.  ``weight`` and ``bias``: [dim], of
     x's type or float32 (both of one type), or None.  ``out`` may be ``x``.
     Differentiable with respect to x, weight and bias (``layer_norm_grad``)."""
-    if torch.is_grad_enabled() and (x.requires_grad or (weight is not None and weight.requires_grad)
-                                    or (bias is not None and bias.requires_grad)):
+    if ((x.requires_grad or (weight is not None and weight.requires_grad) or (bias is not None and bias.requires_grad))
+            and torch.is_grad_enabled()):
         if out is not None:
             raise ValueError("out cannot be given where a gradient is wanted")
         return _LayerNorm.apply(x, weight, bias, eps, stream)
