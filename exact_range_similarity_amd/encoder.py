@@ -227,14 +227,14 @@ def embed_grad(grad, ids, rows, scale=1.0, padding_idx=None, dtype=None, out=Non
     n, dim = ids.numel(), grad.shape[-1]
     L = _library()
     need = L.ersj_embed_grad_work(n, rows, dim)
-    work = torch.empty(need, dtype=torch.uint8, device=device)
+    work = torch.empty(need, dtype=torch.uint8, device=device) if need else None
     if out is None:
         out, ldo = torch.empty((rows, dim), dtype=dtype, device=device), dim
     else:
         ldo = _given(out, "out", (rows, dim), dtype, device)
     _check(L.ersj_embed_grad(grad.data_ptr(), gt, _rows(grad, "grad")[1], ids.data_ptr(), _ID_TYPES[ids.dtype], n,
                              scale, _padding(padding_idx), out.data_ptr(), _TYPES[dtype], rows, dim, ldo,
-                             1 if accumulate else 0, work.data_ptr(), need, _raw_stream(device.index)))
+                             1 if accumulate else 0, work.data_ptr() if need else None, need, _raw_stream(device.index)))
     return out
 
 

@@ -57,8 +57,9 @@ int ersj_embed(const void *d_table, int32_t table_type, int64_t rows, int32_t di
  * Gradient of the table:
  *   out[v, :] = scale * sum over t with ids[t] = v of grad[t, :].
  * Tokens with the padding id, or with an id outside [0, rows), add nothing.
- * The tokens are sorted by id, and each row's terms are added in the order
- * of t in 32 bits.
+ * Each row's terms are added in 32 bits in an order that the ids alone
+ * determine: a row's tokens side by side, in the order of t, in stretches
+ * whose sums are then added.
  *  d_grad     : device [n][ld_grad] of grad_type.
  *  d_out      : device [rows][ld_out] of out_type: grad_type, or ERSJ_F32.
  *               Every row is written; a row without tokens gets zeros.
@@ -73,7 +74,8 @@ int ersj_embed_grad(const void *d_grad, int32_t grad_type, int64_t ld_grad, cons
                     int64_t n, float scale, int64_t padding_id, void *d_out, int32_t out_type, int64_t rows,
                     int32_t dim, int64_t ld_out, int32_t accumulate, void *d_work, uint64_t d_work_bytes,
                     void *stream);
-/* Bytes of working memory for those sizes (0 for sizes that are refused). */
+/* Bytes of working memory for those sizes (0 also for sizes that are refused,
+ * and for few tokens, where none is needed and d_work may be NULL). */
 uint64_t ersj_embed_grad_work(int64_t n, int64_t rows, int32_t dim);
 
 /*

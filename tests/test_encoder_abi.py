@@ -59,8 +59,8 @@ def embed_grad(**kw):
 @pytest.mark.parametrize("kw", [
     dict(grad=None), dict(grad=FAKE + 1), dict(grad_type=3), dict(ld_grad=3), dict(ids=None), dict(ids=FAKE + 4),
     dict(id_type=-1), dict(n=-1), dict(n=2 ** 31), dict(pad=-5), dict(out=None), dict(out_type=1), dict(rows=0),
-    dict(rows=2 ** 31), dict(dim=0), dict(dim=1 << 20), dict(ld_out=2), dict(work=None), dict(work=FAKE + 64),
-    dict(work_bytes=16),
+    dict(rows=2 ** 31), dict(dim=0), dict(dim=1 << 20), dict(ld_out=2), dict(work=None, n=5000), dict(work=FAKE + 64),
+    dict(work_bytes=16, n=5000),
 ])
 def test_embed_grad_rejects_bad_arguments(kw):
     assert embed_grad(**kw) == ersj.ERR_INVALID_ARG

@@ -622,3 +622,55 @@ def test_offsets_beyond_32_bits():
     assert abs(float(norm) / total - 1) <= 2 * U
     ref = last.to(F64) * (10.0 / (total + 1e-6))
     close(x[-1000:], ref, rounded(ref, ref.abs() * 2 * U, x.dtype))
+
+
+# ---- sizes at which the kernels change their plan ----
+
+@pytest.mark.parametrize("n,rows,dim", [(1024, 40, 16), (1025, 40, 16), (1024, 70000, 9), (1025, 70001, 9), (4096, 511, 8),
+                                        (4097, 511, 8), (4097, 512, 8), (5000, 262143, 4), (5000, 262144, 4),
+                                        (65536, 1000, 8), (65537, 1000, 8), (131072, 300, 5), (131073, 300, 5),
+                                        (270000, 5000, 3), (6000, 2, 33), (300, 100000, 520), (2000, 20, 1030)])
+@pytest.mark.parametrize("act,table", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
+def test_embed_grad_plans(act, table, n, rows, dim):
+    g = gen(n + dim)
+    grad = randn((n, dim), g, act)
+    ids = zipf(n, rows, g)
+    ids[::17] = rows - 1
+    check_embed_grad(ersj.embed_grad(grad, ids, rows, 1.0, 1, TYPES[table]), grad, ids, rows, 1.0, 1)
+    out = randn((rows, dim), g, table)
+    before = out.clone()
+    ersj.embed_grad(grad, ids, rows, 1.0, 1, out=out, accumulate=True)
+    check_embed_grad(out, grad, ids, rows, 1.0, 1, before=before)
+
+
+@pytest.mark.parametrize("n", [200, 1000, 3000, 20000, 200000])
+def test_embed_grad_long_rows(n):
+    # few ids, each of them long: rows cut over many shares, and neighbours of long rows
+    g = gen(n)
+    rows, dim = 400, 40
+    grad = randn((n, dim), g, "bf16")
+    for ids in (torch.randint(0, 3, (n,), generator=g, device=DEV) * 199,
+                torch.where(torch.rand(n, generator=g, device=DEV) < 0.9, 7,
+                            torch.randint(0, rows, (n,), generator=g, device=DEV)),
+                torch.arange(n, device=DEV) * 40 // n + 5):
+        got = ersj.embed_grad(grad, ids, rows, 1.0, None, torch.float32)
+        check_embed_grad(got, grad, ids, rows, 1.0, None)
+        assert torch.equal(got, ersj.embed_grad(grad, ids, rows, 1.0, None, torch.float32))
+
+
+@pytest.mark.parametrize("act", ["f32", "f16"])
+@pytest.mark.parametrize("dim", [3, 4, 15, 16, 17, 31, 33, 63, 65, 127, 129, 255, 256, 257, 511, 513, 1023, 1024, 1025, 2047,
+                                 4095, 4097, 8191, 8193, 16384, 16385, 32769])
+def test_layer_norm_plans(act, dim):
+    x, w, b, dy = norm_inputs(19, dim, act, "f32", True, dim)
+    got = ersj.layer_norm(x, w, b)
+    check_norm(got, x, w, b, 1e-5)
+    check_norm_grad(ersj.layer_norm_grad(dy, x, got[1], got[2], w), dy, x, got[1], got[2], w)
+
+
+@pytest.mark.parametrize("n,dim", [(5000, 6), (3000, 1028), (40000, 40)])
+def test_embed_many_rows(n, dim):
+    g = gen(n)
+    w = randn((n // 3, dim), g)
+    ids = torch.randint(0, n // 3, (n,), generator=g, device=DEV)
+    check_embed(ersj.embed(w, ids, 1.5, 7, torch.bfloat16), w, ids, 1.5, 7)
