@@ -127,40 +127,53 @@ __device__ __forceinline__ uint2 sort_entry(const SortSource &s, uint32_t i)
     return make_uint2(id < 0 || id >= s.rows || id == s.padding_id ? (uint32_t)s.rows : (uint32_t)id, i);
 }
 
-template <typename I>
-__global__ __launch_bounds__(kSortThreads) void k_sort_count(SortSource s, int shift, int bits, uint32_t run,
-                                                             uint32_t *counts)
+template <typename I, int ITEMS>
+__global__ __launch_bounds__(kSortThreads) void k_sort_count(SortSource s, int shift, int bits, uint32_t *counts)
 {
     __shared__ uint32_t cnt[kMaxDigits];
     const int nd = 1 << bits;
+    uint32_t key[ITEMS];
+    const uint64_t i0 = (uint64_t)blockIdx.x * (kSortThreads * ITEMS) + threadIdx.x;
+#pragma unroll
+    for (int r = 0; r < ITEMS; ++r) {
+        const uint64_t i = i0 + r * kSortThreads;
+        key[r] = sort_entry<I>(s, i < s.n ? (uint32_t)i : s.n - 1).x;
+    }
     if ((int)threadIdx.x < nd) cnt[threadIdx.x] = 0;
     __syncthreads();
-    const uint64_t i0 = (uint64_t)blockIdx.x * run;
-    const uint32_t i1 = (uint32_t)(i0 + run < s.n ? i0 + run : s.n);
-    for (uint32_t i = (uint32_t)i0 + threadIdx.x; i < i1; i += kSortThreads)
-        atomicAdd(&cnt[(sort_entry<I>(s, i).x >> shift) & (nd - 1)], 1u);
+#pragma unroll
+    for (int r = 0; r < ITEMS; ++r)
+        if (i0 + r * kSortThreads < s.n) atomicAdd(&cnt[(key[r] >> shift) & (nd - 1)], 1u);
     __syncthreads();
     if ((int)threadIdx.x < nd) counts[(size_t)blockIdx.x * nd + threadIdx.x] = cnt[threadIdx.x];
 }
 
 // Each digit's counts over the runs become their exclusive prefix; the total
-// goes to row `runs`.  One wave per digit.
+// goes to row `runs`.  One wave per digit, four loads of 64 runs at a time.
 __global__ __launch_bounds__(kThreads) void k_sort_scan(uint32_t *counts, uint32_t runs, int bits)
 {
     const int lane = threadIdx.x & 63;
     const uint32_t nd = 1u << bits, k = blockIdx.x * kWaves + (threadIdx.x >> 6);
     if (k >= nd) return;
     uint32_t carry = 0;
-    for (uint32_t g0 = 0; g0 < runs; g0 += 64) {
-        const uint32_t g = g0 + lane;
-        const uint32_t c = g < runs ? counts[(size_t)g * nd + k] : 0;
-        uint32_t inc = c;
-        for (int o = 1; o < 64; o <<= 1) {
-            const uint32_t v = __shfl_up(inc, o, 64);
-            if (lane >= o) inc += v;
+    for (uint32_t g0 = 0; g0 < runs; g0 += 256) {
+        uint32_t c[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const uint32_t g = g0 + 64 * u + lane;
+            c[u] = g < runs ? counts[(size_t)g * nd + k] : 0;
         }
-        if (g < runs) counts[(size_t)g * nd + k] = carry + inc - c;
-        carry += __shfl(inc, 63, 64);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const uint32_t g = g0 + 64 * u + lane;
+            uint32_t inc = c[u];
+            for (int o = 1; o < 64; o <<= 1) {
+                const uint32_t v = __shfl_up(inc, o, 64);
+                if (lane >= o) inc += v;
+            }
+            if (g < runs) counts[(size_t)g * nd + k] = carry + inc - c[u];
+            carry += __shfl(inc, 63, 64);
+        }
     }
     if (lane == 0) counts[(size_t)runs * nd + k] = carry;
 }
@@ -894,12 +907,14 @@ constexpr int kEmbedBlocks = 2048;  // 8 workgroups to each CU
 template <typename T, typename O, typename I>
 static void run_embed(const EmbedArgs &a, hipStream_t s)
 {
-    // the smallest team of at least eight lanes that covers the row with up to
-    // four vectors a lane; longer rows are split over the grid's second axis
+    // the smallest team of at least eight lanes (fewer where the row has fewer
+    // vectors) that covers the row with up to four vectors a lane; longer rows
+    // are split over the grid's second axis
     constexpr int kLen = 16 / sizeof(O);
     const int len = a.dim < kLen ? 1 : kLen;
     const int vecs = (a.dim + len - 1) / len;
-    int lanes = 8;
+    int lanes = 1;
+    while (lanes < 8 && lanes < vecs) lanes *= 2;
     while (lanes < 64 && lanes * 4 < vecs) lanes *= 2;
     const int nv = (vecs + lanes - 1) / lanes;
     const int64_t need = (a.n + kThreads / lanes - 1) / (kThreads / lanes);
@@ -910,11 +925,15 @@ static void run_embed(const EmbedArgs &a, hipStream_t s)
         k_embed<T, O, I, kLen, L, NV><<<grid, block, 0, s>>>(a);        \
         break;
     if (len == 1) {
-        k_embed<T, O, I, 1, 8, 1><<<grid, block, 0, s>>>(a);
-        return;
+        switch (lanes) {
+        case 1: k_embed<T, O, I, 1, 1, 1><<<grid, block, 0, s>>>(a); return;
+        case 2: k_embed<T, O, I, 1, 2, 1><<<grid, block, 0, s>>>(a); return;
+        case 4: k_embed<T, O, I, 1, 4, 1><<<grid, block, 0, s>>>(a); return;
+        default: k_embed<T, O, I, 1, 8, 1><<<grid, block, 0, s>>>(a); return;
+        }
     }
     switch (lanes * 8 + (nv < 4 ? nv : 4)) {
-        CASE(8, 1) CASE(8, 2) CASE(8, 3) CASE(8, 4) CASE(16, 3) CASE(16, 4) CASE(32, 3) CASE(32, 4) CASE(64, 3)
+        CASE(1, 1) CASE(2, 1) CASE(4, 1) CASE(8, 1) CASE(8, 2) CASE(8, 3) CASE(8, 4) CASE(16, 3) CASE(16, 4) CASE(32, 3) CASE(32, 4) CASE(64, 3)
         CASE(64, 4)
     }
 #undef CASE
@@ -950,33 +969,36 @@ uint64_t embed_grad_work(int64_t n, int64_t rows, int dim)
            (uint64_t)q.shares * 2 * 4 * (uint64_t)dim;
 }
 
+template <typename I, int ITEMS>
+static void launch_sort_pass(const SortPlan &p, const SortSource &src, int shift, uint32_t *counts, uint2 *out,
+                             hipStream_t s)
+{
+    const dim3 grid((unsigned)p.runs), block(kSortThreads);
+    const bool scan = p.runs > kScanRuns;
+    k_sort_count<I, ITEMS><<<grid, block, 0, s>>>(src, shift, p.bits, counts);
+    if (scan)
+        k_sort_scan<<<dim3(((1u << p.bits) + kWaves - 1) / kWaves), dim3(kThreads), 0, s>>>(counts, (uint32_t)p.runs,
+                                                                                           p.bits);
+    k_sort_scatter<I, ITEMS><<<grid, block, 0, s>>>(src, shift, p.bits, counts, scan, out);
+}
+
 template <typename I>
 static void launch_sort(const SortPlan &p, SortSource &src, uint2 *const (&buf)[2], uint32_t *counts, hipStream_t s)
 {
-    const dim3 block(kSortThreads);
     if (src.n <= (uint32_t)kLocalMax) {
-        k_sort_local<I, kLocalMax / kSortThreads><<<dim3(1), block, 0, s>>>(src, p.passes, p.bits, buf[0]);
+        k_sort_local<I, kLocalMax / kSortThreads><<<dim3(1), dim3(kSortThreads), 0, s>>>(src, p.passes, p.bits, buf[0]);
         src.entries = buf[0];
         return;
     }
-    const dim3 grid((unsigned)p.runs);
-    const bool scan = p.runs > kScanRuns;
     for (int k = 0; k < p.passes; ++k) {
         uint2 *out = buf[k & 1];
-        const int shift = k * p.bits;
-        k_sort_count<I><<<grid, block, 0, s>>>(src, shift, p.bits, (uint32_t)(p.items * kSortThreads), counts);
-        if (scan)
-            k_sort_scan<<<dim3(((1u << p.bits) + kWaves - 1) / kWaves), dim3(kThreads), 0, s>>>(
-                counts, (uint32_t)p.runs, p.bits);
-        if (p.items == 1) k_sort_scatter<I, 1><<<grid, block, 0, s>>>(src, shift, p.bits, counts, scan, out);
-        else if (p.items == 2) k_sort_scatter<I, 2><<<grid, block, 0, s>>>(src, shift, p.bits, counts, scan, out);
-        else k_sort_scatter<I, 4><<<grid, block, 0, s>>>(src, shift, p.bits, counts, scan, out);
+        if (p.items == 1) launch_sort_pass<I, 1>(p, src, k * p.bits, counts, out, s);
+        else if (p.items == 2) launch_sort_pass<I, 2>(p, src, k * p.bits, counts, out, s);
+        else launch_sort_pass<I, 4>(p, src, k * p.bits, counts, out, s);
         src.entries = out;
     }
 }
 
-// Columns of a wave: 64 lanes of 16 bytes of the 16-bit types, or twice that
-// of 32 bits; single elements in rows shorter than a vector.
 template <typename T, typename O, int LEN, int NV>
 static void launch_few(const EmbedGradArgs &a, int col_blocks, hipStream_t s)
 {
@@ -988,23 +1010,31 @@ static void launch_few(const EmbedGradArgs &a, int col_blocks, hipStream_t s)
     else k_embed_grad_few<T, O, int32_t, LEN, NV><<<grid, block, 0, s>>>(a, own);
 }
 
+template <typename T, typename O, int LEN, int NV>
+static void launch_sum_of(const EmbedGradArgs &a, const uint2 *entries, const SumPlan &q, float *part, Note *notes,
+                          hipStream_t s)
+{
+    if (a.n <= kFewMax) {
+        launch_few<T, O, LEN, NV>(a, q.col_blocks, s);
+        return;
+    }
+    const dim3 grid((unsigned)((q.shares + kWaves - 1) / kWaves), q.col_blocks), block(kThreads);
+    k_embed_grad_sum<T, O, LEN, NV><<<grid, block, 0, s>>>(a, entries, q.share, (uint32_t)q.shares, part, notes);
+    k_embed_grad_join<O><<<dim3((unsigned)((q.shares + kJoinWaves - 1) / kJoinWaves)), dim3(kJoinThreads), 0, s>>>(
+        a, (uint32_t)q.shares, part, notes);
+}
+
+// Narrow rows are spread over all lanes: a token costs the wave as many
+// additions as a lane has columns.
 template <typename T, typename O>
 static void launch_sum(const EmbedGradArgs &a, const uint2 *entries, const SumPlan &q, float *part, Note *notes,
                        hipStream_t s)
 {
-    constexpr int kLen = 16 / sizeof(T), kNv = sizeof(T) / 2;
-    if (a.n <= kFewMax) {
-        if (a.dim < kLen) launch_few<T, O, 1, 1>(a, q.col_blocks, s);
-        else launch_few<T, O, kLen, kNv>(a, q.col_blocks, s);
-        return;
-    }
-    const dim3 grid((unsigned)((q.shares + kWaves - 1) / kWaves), q.col_blocks), block(kThreads);
-    if (a.dim < kLen)
-        k_embed_grad_sum<T, O, 1, 1><<<grid, block, 0, s>>>(a, entries, q.share, (uint32_t)q.shares, part, notes);
-    else
-        k_embed_grad_sum<T, O, kLen, kNv><<<grid, block, 0, s>>>(a, entries, q.share, (uint32_t)q.shares, part, notes);
-    k_embed_grad_join<O><<<dim3((unsigned)((q.shares + kJoinWaves - 1) / kJoinWaves)), dim3(kJoinThreads), 0, s>>>(
-        a, (uint32_t)q.shares, part, notes);
+    if (a.dim <= 64) launch_sum_of<T, O, 1, 1>(a, entries, q, part, notes, s);
+    else if (a.dim <= 128) launch_sum_of<T, O, 2, 1>(a, entries, q, part, notes, s);
+    else if (a.dim <= 256) launch_sum_of<T, O, 4, 1>(a, entries, q, part, notes, s);
+    else if constexpr (sizeof(T) == 4) launch_sum_of<T, O, 4, 2>(a, entries, q, part, notes, s);
+    else launch_sum_of<T, O, 8, 1>(a, entries, q, part, notes, s);
 }
 
 hipError_t launch_embed_grad(const EmbedGradArgs &a, hipStream_t s)

@@ -13,6 +13,10 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Threads of a workgroup whose teams have `lanes` lanes: a team above a wave
+// is a workgroup of its own.
+constexpr int block_of(int lanes) { return lanes > 64 ? lanes : kThreads; }
+
 template <typename E, int LEN>
 struct Slot {
     typedef E vec __attribute__((ext_vector_type(LEN)));
@@ -114,9 +118,9 @@ struct Columns {
 };
 
 template <typename T, typename P, int LEN, int L, int NV>
-__global__ __launch_bounds__(L > kThreads ? L : kThreads) void k_norm(NormArgs a)
+__global__ __launch_bounds__(block_of(L)) void k_norm(NormArgs a)
 {
-    constexpr int kTeams = (L > kThreads ? L : kThreads) / L;
+    constexpr int kTeams = block_of(L) / L;
     constexpr bool kKeep = L <= 256;  // weight and bias stay in registers
     typedef float fvec __attribute__((ext_vector_type(LEN)));
     typedef Slot<T, LEN> X;
@@ -231,9 +235,9 @@ __global__ __launch_bounds__(1024) void k_norm_long(NormArgs a)
 // registers, a workgroup's teams are added in a fixed order at the end, and
 // k_norm_grad_join adds the workgroups' sums, part [workgroup][2][dim].
 template <typename T, typename P, int LEN, int L, int NV>
-__global__ __launch_bounds__(L > kThreads ? L : kThreads) void k_norm_grad(NormGradArgs a, float *part)
+__global__ __launch_bounds__(block_of(L)) void k_norm_grad(NormGradArgs a, float *part)
 {
-    constexpr int kBlock = L > kThreads ? L : kThreads;
+    constexpr int kBlock = block_of(L);
     constexpr int kTeams = kBlock / L;
     constexpr bool kKeep = L <= 256;
     typedef float fvec __attribute__((ext_vector_type(LEN)));
@@ -315,7 +319,9 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void k_norm_grad(NormG
             }
         }
     }
-    if (!part) return;
+    if (!a.gw && !a.gb) return;
+    // the only workgroup writes the results, one of several its part
+    P *gw = part ? nullptr : (P *)a.gw, *gb = part ? nullptr : (P *)a.gb;
     float *out = part + (uint64_t)blockIdx.x * 2 * a.dim;
     typedef Slot<float, LEN> S;
     // a lane's own columns of vector k to p[column] (p in LDS or not)
@@ -330,8 +336,17 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void k_norm_grad(NormG
     if constexpr (L > 64) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            put(out, k, dw[k]);
-            put(out + a.dim, k, db[k]);
+            if (part) {
+                put(out, k, dw[k]);
+                put(out + a.dim, k, db[k]);
+                continue;
+            }
+#pragma unroll
+            for (int j = 0; j < LEN; ++j) {
+                if (k == NV - 1 && j < at.skip) continue;
+                if (gw) gw[at.col[k] + j] = (P)dw[k][j];
+                if (gb) gb[at.col[k] + j] = (P)db[k][j];
+            }
         }
     } else {
         // the teams of a wave by lane exchanges, then the waves in order
@@ -354,7 +369,11 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void k_norm_grad(NormG
             float s = sums[0][i];
 #pragma unroll
             for (int t = 1; t < kBlock / 64; ++t) s += sums[t][i];
-            out[c] = s;
+            if (part) out[c] = s;
+            else if (c < a.dim) {
+                if (gw) gw[c] = (P)s;
+            } else if (gb)
+                gb[c - a.dim] = (P)s;
         }
     }
 }
@@ -434,9 +453,15 @@ __global__ __launch_bounds__(1024) void k_norm_grad_join(const float *part, int 
     }
 }
 
-// Lanes of a team and vectors of a lane for rows of `dim` elements: the
-// smallest team of at least eight lanes (128 consecutive bytes a load) whose
-// lanes need no more than four vectors.  lanes = 0: the row is too long.
+// Lanes of a team and vectors of a lane for rows of `dim` elements.  Within a
+// wave: the smallest team of at least eight lanes (128 consecutive bytes a
+// load) whose lanes need no more than four vectors (1M rows of 384 bf16: 16
+// lanes 295 us, 32 lanes 301, 64 lanes 331).  Teams of a workgroup: up to three
+// vectors, since a fourth costs more occupancy than half-empty lanes cost
+// (gradient over 32,768 x 4096 bf16: 256 lanes of two vectors 155 us, 128 of
+// four 167), but four where the lanes would double for it at 256 (10,000 x
+// 8192 bf16: 110 us, 512 lanes of two 121) and at the longest.  lanes = 0: the
+// row is too long.
 struct Shape {
     int len, lanes, nv;
 };
@@ -452,21 +477,43 @@ Shape shape_of(int type, int dim, int most)
     s.lanes = 1;
     while (s.lanes < 8 && s.lanes < vecs) s.lanes *= 2;
     while (s.lanes < 64 && s.lanes * 4 < vecs) s.lanes *= 2;
-    if (s.lanes * 4 < vecs) s.lanes = 256;
-    while (s.lanes * 4 < vecs) s.lanes *= 2;
-    if (s.lanes > most) s.lanes = 0;
+    if (s.lanes * 4 < vecs) {
+        s.lanes = vecs <= 128 * 3 ? 128 : vecs <= 256 * 4 ? 256 : 512;
+        if (s.lanes < most && vecs > 512 * 3) s.lanes = 1024;
+        if (s.lanes * 4 < vecs) s.lanes = 0;
+    }
     s.nv = s.lanes ? (vecs + s.lanes - 1) / s.lanes : 0;
     return s;
 }
 
-int teams_of(const Shape &s) { return s.lanes > kThreads ? 1 : kThreads / s.lanes; }
+// Workgroups of the norm: one turn each for up to kNormFull workgroups of 256
+// threads, then up to eight turns (four of the large workgroups), which pay
+// for the weights' loads; more workgroups than fit the device start as others
+// end, so that no few are left for a round of their own (30,000 x 4097 f32: 203
+// us, 272 with a fixed 1024 workgroups of 29 turns).
+constexpr int kNormFull = 2048;
 
-constexpr int kNormBlocks = 2048;  // 8 workgroups of 256 threads to each CU
-constexpr int kGradBlocks = 512;   // 2 to each CU, what the registers allow
-
-unsigned blocks_of(int64_t n, const Shape &s, int most)
+unsigned norm_blocks(int64_t n, const Shape &s)
 {
-    const int64_t need = s.lanes ? (n + teams_of(s) - 1) / teams_of(s) : n;
+    const int block = s.lanes ? block_of(s.lanes) : 1024;
+    const int64_t teams = s.lanes ? block / s.lanes : 1, need = (n + teams - 1) / teams;
+    int64_t turns = need / (kNormFull * 256 / block);
+    const int64_t top = block > 256 ? 4 : 8;
+    turns = turns < 1 ? 1 : turns > top ? top : turns;
+    return (unsigned)((need + turns - 1) / turns);
+}
+
+// Workgroups of the gradient: each costs a part of the sums, so no more than
+// the registers let run at once (512 of 256 threads; 512 of 512 where a lane
+// holds little), and at least kGradTurns rows to a team where that leaves one.
+constexpr int kGradTurns = 4;
+
+unsigned grad_blocks(int64_t n, const Shape &s)
+{
+    const int block = s.lanes ? block_of(s.lanes) : 1024;
+    const int64_t rows = (int64_t)kGradTurns * (s.lanes ? block / s.lanes : 1);
+    const int64_t need = (n + rows - 1) / rows;
+    const int64_t most = (s.lanes == 512 && s.len * s.nv <= 12 ? 1024 : 512) * 256 / block;
     return (unsigned)(need < 1 ? 1 : need < most ? need : most);
 }
 
@@ -490,10 +537,12 @@ void by_shape(const Shape &s, A... args)
         CASE(1, 1) CASE(2, 1) CASE(4, 1)
         CASE(8, 1) CASE(8, 2) CASE(8, 3) CASE(8, 4)
         CASE(16, 3) CASE(16, 4) CASE(32, 3) CASE(32, 4) CASE(64, 3) CASE(64, 4)
-        CASE(256, 2) CASE(256, 3) CASE(256, 4) CASE(512, 3) CASE(512, 4)
+        CASE(128, 3) CASE(256, 2) CASE(256, 3) CASE(256, 4) CASE(512, 3)
     }
     if constexpr (F<T, P, LEN, 1024, 4>::kLong) {
-        switch (s.lanes * 8 + s.nv) { CASE(1024, 3) CASE(1024, 4) }
+        switch (s.lanes * 8 + s.nv) { CASE(1024, 2) CASE(1024, 3) CASE(1024, 4) }
+    } else {
+        switch (s.lanes * 8 + s.nv) { CASE(512, 4) }
     }
 #undef CASE
 }
@@ -503,7 +552,7 @@ struct RunNorm {
     static constexpr bool kLong = true;  // 1024 lanes as well
     static void run(const NormArgs *a, unsigned blocks, hipStream_t s)
     {
-        k_norm<T, P, LEN, L, NV><<<dim3(blocks), dim3(L > kThreads ? L : kThreads), 0, s>>>(*a);
+        k_norm<T, P, LEN, L, NV><<<dim3(blocks), dim3(block_of(L)), 0, s>>>(*a);
     }
 };
 
@@ -512,7 +561,7 @@ struct RunGrad {
     static constexpr bool kLong = false;
     static void run(const NormGradArgs *a, float *part, unsigned blocks, hipStream_t s)
     {
-        k_norm_grad<T, P, LEN, L, NV><<<dim3(blocks), dim3(L > kThreads ? L : kThreads), 0, s>>>(*a, part);
+        k_norm_grad<T, P, LEN, L, NV><<<dim3(blocks), dim3(block_of(L)), 0, s>>>(*a, part);
     }
 };
 
@@ -532,7 +581,7 @@ hipError_t launch_layer_norm(const NormArgs &a, hipStream_t s)
 {
     if (a.n == 0) return hipSuccess;
     const Shape sh = shape_of(a.type, a.dim, 1024);
-    const unsigned blocks = blocks_of(a.n, sh, kNormBlocks);
+    const unsigned blocks = norm_blocks(a.n, sh);
     ERSJ_NORM_SWITCH(a.type, a.param_type, T, P,
         if (sh.lanes) by_shape<T, P, RunNorm>(sh, &a, blocks, s);
         else k_norm_long<T, P><<<dim3(blocks), dim3(1024), 0, s>>>(a));
@@ -544,7 +593,9 @@ uint64_t layer_norm_grad_work(int64_t n, int dim)
     // a shape depends on the type: the larger of the two
     uint64_t most = 0;
     for (int type : {(int)kF32, (int)kBF16}) {
-        const uint64_t b = (uint64_t)blocks_of(n, shape_of(type, dim, 512), kGradBlocks) * 2 * 4 * (uint64_t)dim;
+        const Shape sh = shape_of(type, dim, 512);
+        const unsigned blocks = grad_blocks(n, sh);
+        const uint64_t b = blocks == 1 && sh.lanes ? 0 : (uint64_t)blocks * 2 * 4 * (uint64_t)dim;
         if (b > most) most = b;
     }
     return most;
@@ -553,9 +604,10 @@ uint64_t layer_norm_grad_work(int64_t n, int dim)
 hipError_t launch_layer_norm_grad(const NormGradArgs &a, hipStream_t s)
 {
     const Shape sh = shape_of(a.type, a.dim, 512);
-    const unsigned blocks = blocks_of(a.n, sh, kGradBlocks);
-    float *part = a.gw || a.gb ? (float *)a.work : nullptr;
-    if (!part && (!a.gx || a.n == 0)) return hipSuccess;
+    const unsigned blocks = grad_blocks(a.n, sh);
+    const bool params = a.gw || a.gb;
+    if (!params && (!a.gx || a.n == 0)) return hipSuccess;
+    float *part = params && (blocks > 1 || !sh.lanes) ? (float *)a.work : nullptr;
     ERSJ_NORM_SWITCH(a.type, a.param_type, T, P,
         if (sh.lanes) by_shape<T, P, RunGrad>(sh, &a, part, blocks, s);
         else {

@@ -335,11 +335,12 @@ def layer_norm_grad(grad, x, mean, rstd, weight=None, dtype=None, want_x=True, w
         gw = torch.empty(dim, dtype=dtype, device=device)
         gb = torch.empty_like(gw)
         need = L.ersj_layer_norm_grad_work(n, dim)
-        work = torch.empty(need, dtype=torch.uint8, device=device)
+        if need:
+            work = torch.empty(need, dtype=torch.uint8, device=device)
     _check(L.ersj_layer_norm_grad(grad.data_ptr(), _rows(grad, "grad")[1], x.data_ptr(), ldx, xt, n, dim,
                                   mean.data_ptr(), rstd.data_ptr(), w, pt, gx.data_ptr() if want_x else None, dim,
                                   gw.data_ptr() if want_params else None, gb.data_ptr() if want_params else None,
-                                  work.data_ptr() if want_params else None, need, _raw_stream(device.index)))
+                                  work.data_ptr() if need else None, need, _raw_stream(device.index)))
     return gx, gw, gb
 
 

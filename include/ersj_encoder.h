@@ -114,7 +114,8 @@ int ersj_layer_norm_grad(const void *d_grad_y, int64_t ld_grad_y, const void *d_
                          int64_t n, int32_t dim, const float *d_mean, const float *d_rstd, const void *d_weight,
                          int32_t param_type, void *d_grad_x, int64_t ld_grad_x, void *d_grad_weight,
                          void *d_grad_bias, void *d_work, uint64_t d_work_bytes, void *stream);
-/* Bytes of working memory for those sizes (0 for sizes that are refused). */
+/* Bytes of working memory for those sizes (0 also for sizes that are refused,
+ * and for few rows, where none is needed and d_work may be NULL). */
 uint64_t ersj_layer_norm_grad_work(int64_t n, int32_t dim);
 
 /*

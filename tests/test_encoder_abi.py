@@ -94,7 +94,7 @@ def norm_grad(**kw):
 @pytest.mark.parametrize("kw", [
     dict(gy=None), dict(x=None), dict(ld_gy=3), dict(ld_x=1), dict(type=3), dict(n=-1), dict(dim=0), dict(mean=None),
     dict(rstd=None), dict(mean=FAKE + 2), dict(weight=FAKE + 1), dict(param_type=1), dict(ld_gx=3), dict(gw=FAKE + 1),
-    dict(gb=FAKE + 2), dict(work=None), dict(work=FAKE + 8), dict(work_bytes=7), dict(gx=FAKE, ld_gx=6),
+    dict(gb=FAKE + 2), dict(work=None, n=5000), dict(work=FAKE + 8), dict(work_bytes=7, n=5000), dict(gx=FAKE, ld_gx=6),
     dict(gx=2 * FAKE, ld_gx=6),
 ])
 def test_layer_norm_grad_rejects_bad_arguments(kw):
