@@ -8,7 +8,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
-#include <new>
+#include <exception>
 #include <vector>
 
 using namespace ersj;
@@ -253,7 +253,7 @@ int ersj_grads_create(int32_t count, const void *const *d_grad, void *const *d_o
         }
         *out = h;
         return ERSJ_OK;
-    } catch (const std::bad_alloc &) {
+    } catch (const std::exception &) {
         return set_error(ERSJ_ERR_OOM, "host memory for the table of a set of gradients");
     }
 }
@@ -272,7 +272,13 @@ int ersj_grads_clip(const ersj_grads *h, float max_norm, float *d_norm, void *d_
 void ersj_grads_free(ersj_grads *h)
 {
     if (!h) return;
-    if (h->chunks) device_block_put(h->device, h->chunks, h->bytes);
+    if (h->chunks) {
+        try {
+            device_block_put(h->device, h->chunks, h->bytes);
+        } catch (...) {  // no host memory for the pool's entry
+            (void)hipFree(h->chunks);
+        }
+    }
     delete h;
 }
 

@@ -132,6 +132,11 @@ def _on(device, t, what):
         raise ValueError(f"{what} is on {t.device}, expected {device}")
 
 
+def _empty_rows(x):
+    """Contiguous rows of the shape and type of ``x``."""
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+
+
 def _param(t, what, dim, row_type, device):
     """Type code of a weight or bias vector."""
     code = _type(t, what)
@@ -284,7 +289,7 @@ def _layer_norm(x, weight, bias, eps, out, stream):
             raise TypeError("weight and bias must have one type")
         pt, b = bt, bias.data_ptr()
     if out is None:
-        out, ldy = torch.empty(shape, dtype=x.dtype, device=device), dim
+        out, ldy = _empty_rows(x), dim
     else:
         ldy = _given(out, "out", shape, x.dtype, device)
     mean = torch.empty(shape[:-1], dtype=torch.float32, device=device)
@@ -328,7 +333,7 @@ def layer_norm_grad(grad, x, mean, rstd, weight=None, dtype=None, want_x=True, w
         elif dtype != weight.dtype:
             raise TypeError("the gradients of weight and bias have the weight's type")
     L = _library()
-    gx = torch.empty(shape, dtype=x.dtype, device=device) if want_x else None
+    gx = _empty_rows(x) if want_x else None
     gw = gb = work = None
     need = 0
     if want_params:

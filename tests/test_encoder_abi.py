@@ -192,3 +192,19 @@ def test_row_spacing():
             f(bad, "x")
     with pytest.raises(ValueError):
         f(x, "x", 11)
+
+
+def test_hip_failure_without_a_device():
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present; this checks the no-device error path")
+    for rc in (embed(), embed_grad(), embed_grad(n=5000), norm(), norm_grad(), norm_grad(n=5000)):
+        assert rc in (ersj.ERR_HIP, ersj.ERR_OOM)
+    rc, h = create()
+    assert rc in (ersj.ERR_HIP, ersj.ERR_OOM) and h.value is None
+
+
+def test_empty_calls_do_nothing():
+    # nothing to write: no launch, so no device is needed either
+    assert embed(n=0, ids=None, out=None) == ersj.OK
+    assert norm(n=0, x=None, y=None, mean=None, rstd=None) == ersj.OK
+    assert norm_grad(n=0, gy=None, x=None, mean=None, rstd=None, gw=None, gb=None, work=None, work_bytes=0) == ersj.OK
