@@ -90,8 +90,9 @@ __global__ __launch_bounds__(kThreads) void k_embed(EmbedArgs a)
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr int kMaxDigitBits = 9;
+constexpr int kMaxDigitBits = 10;  // a digit's count to each thread
 constexpr int kMaxDigits = 1 << kMaxDigitBits;
+static_assert(kMaxDigits <= kSortThreads, "one thread to a digit");
 // More runs than this are scanned by a kernel of their own: up to it a thread
 // reads the counts of a digit in 64 runs or less in one or two batches of loads.
 constexpr int kScanRuns = 64;

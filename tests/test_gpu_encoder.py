@@ -629,7 +629,8 @@ def test_offsets_beyond_32_bits():
 @pytest.mark.parametrize("n,rows,dim", [(1024, 40, 16), (1025, 40, 16), (1024, 70000, 9), (1025, 70001, 9), (4096, 511, 8),
                                         (4097, 511, 8), (4097, 512, 8), (5000, 262143, 4), (5000, 262144, 4),
                                         (65536, 1000, 8), (65537, 1000, 8), (131072, 300, 5), (131073, 300, 5),
-                                        (270000, 5000, 3), (6000, 2, 33), (300, 100000, 520), (2000, 20, 1030)])
+                                        (270000, 5000, 3), (5000, 1023, 8), (5000, 1024, 8), (300000, 1023, 3),
+                                        (5000, 1048575, 3), (5000, 1048576, 3), (70000, 1048576, 2), (6000, 2, 33), (300, 100000, 520), (2000, 20, 1030)])
 @pytest.mark.parametrize("act,table", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
 def test_embed_grad_plans(act, table, n, rows, dim):
     g = gen(n + dim)
