@@ -28,16 +28,17 @@ __device__ __forceinline__ double block_sum(double v, double *red)
 // after the last whole vector go to the first threads one by one.
 template <typename T>
 struct Chunk {
-    typedef Vec<T> V;
-    typename V::type v[kVecs];
+    typedef Slot<T, 16 / sizeof(T)> V;
+    static constexpr int kLen = 16 / sizeof(T);
+    typename V::vec v[kVecs];
 
     __device__ __forceinline__ void load(const T *p, uint32_t n)
     {
-        const uint32_t vecs = n / V::kLen;
+        const uint32_t vecs = n / kLen;
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
             const uint32_t i = threadIdx.x + k * kThreads;
-            if (i < vecs) v[k] = V::load(p + i * V::kLen);
+            if (i < vecs) v[k] = V::load(p + i * kLen);
         }
     }
 };
@@ -45,22 +46,22 @@ struct Chunk {
 template <typename T>
 __device__ __forceinline__ double chunk_squares(const T *p, uint32_t n)
 {
-    typedef Vec<T> V;
+    constexpr int kLen = 16 / sizeof(T);
     Chunk<T> c;
     c.load(p, n);
-    const uint32_t vecs = n / V::kLen;
+    const uint32_t vecs = n / kLen;
     double s[2] = {0., 0.};
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
         if (threadIdx.x + k * kThreads < vecs) {
 #pragma unroll
-            for (int j = 0; j < V::kLen; ++j) {
+            for (int j = 0; j < kLen; ++j) {
                 const double x = (double)(float)c.v[k][j];
                 s[j & 1] += x * x;
             }
         }
     }
-    const uint32_t i = vecs * V::kLen + threadIdx.x;
+    const uint32_t i = vecs * kLen + threadIdx.x;
     if (i < n) {
         const double x = (double)(float)p[i];
         s[0] += x * x;
@@ -83,19 +84,20 @@ __global__ __launch_bounds__(kThreads) void k_grad_squares(const GradChunk *chun
 template <typename T>
 __device__ __forceinline__ void chunk_scale(const T *in, T *out, uint32_t n, float f)
 {
-    typedef Vec<T> V;
-    typedef float fvec __attribute__((ext_vector_type(16 / sizeof(T))));
+    constexpr int kLen = 16 / sizeof(T);
+    typedef Slot<T, kLen> V;
+    typedef float fvec __attribute__((ext_vector_type(kLen)));
     Chunk<T> c;
     c.load(in, n);
-    const uint32_t vecs = n / V::kLen;
+    const uint32_t vecs = n / kLen;
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
         const uint32_t i = threadIdx.x + k * kThreads;
         if (i < vecs)
-            V::store(out + i * V::kLen,
-                     __builtin_convertvector(__builtin_convertvector(c.v[k], fvec) * f, typename V::type));
+            V::store(out + i * kLen,
+                     __builtin_convertvector(__builtin_convertvector(c.v[k], fvec) * f, typename V::vec));
     }
-    const uint32_t i = vecs * V::kLen + threadIdx.x;
+    const uint32_t i = vecs * kLen + threadIdx.x;
     if (i < n) out[i] = (T)(f * (float)in[i]);
 }
 

@@ -25,11 +25,9 @@ __device__ __forceinline__ int64_t id_at(const void *ids, int64_t t)
 template <typename T, typename O, typename I, int LEN, int L, int NV>
 __global__ __launch_bounds__(kThreads) void k_embed(EmbedArgs a)
 {
-    typedef T tvec __attribute__((ext_vector_type(LEN)));
-    typedef O ovec __attribute__((ext_vector_type(LEN)));
+    typedef Slot<T, LEN> In;
+    typedef Slot<O, LEN> Out;
     typedef float fvec __attribute__((ext_vector_type(LEN)));
-    struct __attribute__((packed, aligned(sizeof(T)))) tslot { tvec v; };
-    struct __attribute__((packed, aligned(sizeof(O)))) oslot { ovec v; };
     const int lane = threadIdx.x & (L - 1);
     const int c0 = blockIdx.y * (L * NV * LEN);
     int col[NV];
@@ -44,16 +42,16 @@ __global__ __launch_bounds__(kThreads) void k_embed(EmbedArgs a)
     int64_t t = (int64_t)blockIdx.x * (kThreads / L) + threadIdx.x / L;
     if (t >= a.n) return;
     auto id_of = [&](int64_t at) { return id_at<I>(a.ids, at < a.n ? at : a.n - 1); };
-    auto load = [&](int64_t id, tvec (&x)[NV]) {
+    auto load = [&](int64_t id, typename In::vec (&x)[NV]) {
         // the first row in the place of one that is not used
         const bool use = id >= 0 && id < a.rows && id != a.padding_id;
         const T *row = (const T *)a.table + (use ? id : 0) * a.ld_table;
 #pragma unroll
         for (int k = 0; k < NV; ++k)
-            if (on[k]) x[k] = ((const tslot *)(row + col[k]))->v;
+            if (on[k]) x[k] = In::load(row + col[k]);
     };
     int64_t id = id_of(t), next_id = id_of(t + step);
-    tvec x[NV], y[NV];
+    typename In::vec x[NV], y[NV];
     load(id, x);
     while (true) {
         const int64_t after = id_of(t + 2 * step);
@@ -65,7 +63,7 @@ __global__ __launch_bounds__(kThreads) void k_embed(EmbedArgs a)
         for (int k = 0; k < NV; ++k) {
             fvec v = __builtin_convertvector(x[k], fvec) * a.scale;
             if (pad || bad) v = (fvec)(pad ? 0.f : __builtin_nanf(""));
-            if (on[k]) ((oslot *)(out + col[k]))->v = __builtin_convertvector(v, ovec);
+            if (on[k]) Out::store(out + col[k], __builtin_convertvector(v, typename Out::vec));
             x[k] = y[k];
         }
         if (!more) break;
@@ -479,13 +477,12 @@ __global__ __launch_bounds__(kThreads) void k_embed_grad_sum(EmbedGradArgs a, co
                                                              int64_t share, uint32_t shares,
                                                              float *part, Note *notes)
 {
-    typedef T tvec __attribute__((ext_vector_type(LEN)));
-    typedef O ovec __attribute__((ext_vector_type(LEN)));
+    typedef Slot<T, LEN> In;
+    typedef Slot<O, LEN> Out;
     typedef float fvec __attribute__((ext_vector_type(LEN)));
-    struct __attribute__((packed, aligned(sizeof(T)))) tslot { tvec v; };
-    struct __attribute__((packed, aligned(sizeof(O)))) oslot { ovec v; };
-    struct __attribute__((packed, aligned(4))) fslot { fvec v; };
-    constexpr int kAhead = 4 / NV;  // tokens of one set of loads; two sets are in flight
+    // tokens of one set of loads, of which two are in flight: more of narrow rows
+    // (1M x 32 bf16: 86 us with eight, 92 with four)
+    constexpr int kAhead = LEN <= 2 ? 8 : 4 / NV;
 
     const int lane = threadIdx.x & 63;
     const uint32_t w = __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + (threadIdx.x >> 6));
@@ -530,7 +527,7 @@ __global__ __launch_bounds__(kThreads) void k_embed_grad_sum(EmbedGradArgs a, co
         if (first) {
 #pragma unroll
             for (int k = 0; k < NV; ++k)
-                if (on[k]) ((fslot *)(part + (uint64_t)w * 2 * a.dim + cols[k]))->v = acc[k];
+                if (on[k]) Slot<float, LEN>::store(part + (uint64_t)w * 2 * a.dim + cols[k], acc[k]);
             flag |= kFirstCut;
         } else if (any || !a.accumulate) {
             O *out = (O *)a.out + (int64_t)v * a.ld_out;
@@ -539,11 +536,11 @@ __global__ __launch_bounds__(kThreads) void k_embed_grad_sum(EmbedGradArgs a, co
             if (a.accumulate) {  // all read before any is written: shifted vectors overlap
 #pragma unroll
                 for (int k = 0; k < NV; ++k)
-                    if (on[k]) acc[k] += __builtin_convertvector(((const oslot *)(out + cols[k]))->v, fvec);
+                    if (on[k]) acc[k] += __builtin_convertvector(Out::load(out + cols[k]), fvec);
             }
 #pragma unroll
             for (int k = 0; k < NV; ++k)
-                if (on[k]) ((oslot *)(out + cols[k]))->v = __builtin_convertvector(acc[k], ovec);
+                if (on[k]) Out::store(out + cols[k], __builtin_convertvector(acc[k], typename Out::vec));
         }
 #pragma unroll
         for (int k = 0; k < NV; ++k) acc[k] = (fvec)0.f;
@@ -564,17 +561,17 @@ __global__ __launch_bounds__(kThreads) void k_embed_grad_sum(EmbedGradArgs a, co
         i = real < m ? i1 : i + m;
         m = real;
         if (m == 0) break;
-        auto load = [&](uint32_t t, tvec (&x)[kAhead][NV]) {
+        auto load = [&](uint32_t t, typename In::vec (&x)[kAhead][NV]) {
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 const uint32_t tu = t + u < m ? t + u : m - 1;
                 const char *row = (const char *)a.grad + (((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)place_hi, tu) << 32) |
                                                           (uint32_t)__builtin_amdgcn_readlane((int)place_lo, tu));
 #pragma unroll
-                for (int k = 0; k < NV; ++k) x[u][k] = ((const tslot *)(row + cols[k] * (uint32_t)sizeof(T)))->v;
+                for (int k = 0; k < NV; ++k) x[u][k] = In::load((const T *)(row + cols[k] * (uint32_t)sizeof(T)));
             }
         };
-        auto add = [&](uint32_t t, const tvec (&x)[kAhead][NV]) {
+        auto add = [&](uint32_t t, const typename In::vec (&x)[kAhead][NV]) {
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 if (t + u >= m) continue;
@@ -585,7 +582,7 @@ __global__ __launch_bounds__(kThreads) void k_embed_grad_sum(EmbedGradArgs a, co
                 any = true;
             }
         };
-        tvec x[kAhead][NV], y[kAhead][NV];
+        typename In::vec x[kAhead][NV], y[kAhead][NV];
         load(0, x);
         for (uint32_t t = 0; t < m; t += 2 * kAhead) {
             if (t + kAhead < m) load(t + kAhead, y);
@@ -598,7 +595,7 @@ __global__ __launch_bounds__(kThreads) void k_embed_grad_sum(EmbedGradArgs a, co
     if (open) {
 #pragma unroll
         for (int k = 0; k < NV; ++k)
-            if (on[k]) ((fslot *)(part + ((uint64_t)w * 2 + 1) * a.dim + cols[k]))->v = acc[k];
+            if (on[k]) Slot<float, LEN>::store(part + ((uint64_t)w * 2 + 1) * a.dim + cols[k], acc[k]);
         flag |= first ? kInside : 0;
     }
     if (lane == 0 && blockIdx.y == 0) notes[w] = Note{v0, flag};
@@ -620,8 +617,7 @@ template <typename O>
 __global__ __launch_bounds__(kJoinThreads) void k_embed_grad_join(EmbedGradArgs a, uint32_t shares,
                                                                   const float *part, const Note *notes)
 {
-    typedef float fvec __attribute__((ext_vector_type(4)));
-    struct __attribute__((packed, aligned(4))) fslot { fvec v; };
+    typedef Slot<float, 4>::vec fvec;
     __shared__ fvec sums[kJoinWaves][64];
     __shared__ uint32_t first[kJoinWaves], row[kJoinWaves], count[kJoinWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -637,7 +633,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_embed_grad_join(EmbedGradArgs 
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
                     const uint32_t q = b + (p + u < p1 ? p + u : p1 - 1);
-                    x[u] = ((const fslot *)(part + ((uint64_t)q * 2 + (q < e ? 1 : 0)) * a.dim + c))->v;
+                    x[u] = Slot<float, 4>::load(part + ((uint64_t)q * 2 + (q < e ? 1 : 0)) * a.dim + c);
                 }
 #pragma unroll
                 for (int u = 0; u < 8; ++u)
@@ -750,11 +746,9 @@ constexpr int kFewWaves = kFewThreads / 64;
 template <typename T, typename O, typename I, int LEN, int NV>
 __global__ __launch_bounds__(kFewThreads) void k_embed_grad_few(EmbedGradArgs a, int own)
 {
-    typedef T tvec __attribute__((ext_vector_type(LEN)));
-    typedef O ovec __attribute__((ext_vector_type(LEN)));
+    typedef Slot<T, LEN> In;
+    typedef Slot<O, LEN> Out;
     typedef float fvec __attribute__((ext_vector_type(LEN)));
-    struct __attribute__((packed, aligned(sizeof(T)))) tslot { tvec v; };
-    struct __attribute__((packed, aligned(sizeof(O)))) oslot { ovec v; };
     constexpr int kPer = kFewMax / kFewThreads;
     constexpr int kAhead = 16 / NV;
     __shared__ uint16_t token[kFewMax], order[kFewMax];
@@ -810,11 +804,11 @@ __global__ __launch_bounds__(kFewThreads) void k_embed_grad_few(EmbedGradArgs a,
         if (a.accumulate) {  // all read before any is written: shifted vectors overlap
 #pragma unroll
             for (int k = 0; k < NV; ++k)
-                if (on[k]) acc[k] += __builtin_convertvector(((const oslot *)(out + cols[k]))->v, fvec);
+                if (on[k]) acc[k] += __builtin_convertvector(Out::load(out + cols[k]), fvec);
         }
 #pragma unroll
         for (int k = 0; k < NV; ++k)
-            if (on[k]) ((oslot *)(out + cols[k]))->v = __builtin_convertvector(acc[k], ovec);
+            if (on[k]) Out::store(out + cols[k], __builtin_convertvector(acc[k], typename Out::vec));
     };
     fvec acc[NV];
     if (total == 0) {
@@ -877,13 +871,13 @@ __global__ __launch_bounds__(kFewThreads) void k_embed_grad_few(EmbedGradArgs a,
 #pragma unroll
         for (int k = 0; k < NV; ++k) acc[k] = (fvec)0.f;
         for (uint32_t p = p0; p < p1; p += kAhead) {
-            tvec x[kAhead][NV];
+            typename In::vec x[kAhead][NV];
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 const uint32_t t = __builtin_amdgcn_readfirstlane(order[p + u < p1 ? p + u : p1 - 1]);
                 const T *row = (const T *)a.grad + (int64_t)t * a.ld_grad;
 #pragma unroll
-                for (int k = 0; k < NV; ++k) x[u][k] = ((const tslot *)(row + cols[k]))->v;
+                for (int k = 0; k < NV; ++k) x[u][k] = In::load(row + cols[k]);
             }
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {

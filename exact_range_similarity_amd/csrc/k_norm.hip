@@ -22,16 +22,6 @@ constexpr int kThreads = 256;
 // is a workgroup of its own.
 constexpr int block_of(int lanes) { return lanes > 64 ? lanes : kThreads; }
 
-template <typename E, int LEN>
-struct Slot {
-    typedef E vec __attribute__((ext_vector_type(LEN)));
-    struct __attribute__((packed, aligned(sizeof(E)))) slot {
-        vec v;
-    };
-    static __device__ __forceinline__ vec load(const E *p) { return ((const slot *)p)->v; }
-    static __device__ __forceinline__ void store(E *p, vec v) { ((slot *)p)->v = v; }
-};
-
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v)
 {
