@@ -376,7 +376,7 @@ class GradSet:
     ``out``: tensors of the same shapes and types that receive the clipped
     gradients; None clips in place.  The set keeps the tensors alive and reads
     their values anew on every call; it is made once for tensors that a
-    training loop reuses."""
+    training loop reuses, and has to outlive a captured graph that clips it."""
 
     def __init__(self, grads, out=None, stream=None):
         self.handle = ctypes.c_void_p()

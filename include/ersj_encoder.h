@@ -86,7 +86,7 @@ uint64_t ersj_embed_grad_work(int64_t n, int64_t rows, int32_t dim);
  *                    (with ld_y = ld_x).
  *  d_weight, d_bias: device [dim] of param_type (type or ERSJ_F32); NULL: 1
  *                    and 0.
- *  eps             : finite, >= 0.
+ *  eps             : finite, >= 0 (with 0, a row of one value gives NaN).
  *  d_mean, d_rstd  : device [n] float; NULL where not wanted.
  * Errors: INVALID_ARG, HIP.
  */
