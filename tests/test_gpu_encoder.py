@@ -630,7 +630,7 @@ def test_offsets_beyond_32_bits():
                                         (4097, 511, 8), (4097, 512, 8), (5000, 262143, 4), (5000, 262144, 4),
                                         (65536, 1000, 8), (65537, 1000, 8), (131072, 300, 5), (131073, 300, 5),
                                         (270000, 5000, 3), (5000, 1023, 8), (5000, 1024, 8), (300000, 1023, 3),
-                                        (5000, 1048575, 3), (5000, 1048576, 3), (70000, 1048576, 2), (6000, 2, 33), (300, 100000, 520), (2000, 20, 1030)])
+                                        (5000, 1048575, 3), (5000, 1048576, 3), (70000, 1048576, 2), (6000, 2, 33), (300, 100000, 520), (2000, 20, 1030), (1500, 20, 65535), (40, 7, 65536)])
 @pytest.mark.parametrize("act,table", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
 def test_embed_grad_plans(act, table, n, rows, dim):
     g = gen(n + dim)
@@ -669,7 +669,7 @@ def test_layer_norm_plans(act, dim):
     check_norm_grad(ersj.layer_norm_grad(dy, x, got[1], got[2], w), dy, x, got[1], got[2], w)
 
 
-@pytest.mark.parametrize("n,dim", [(5000, 6), (3000, 1028), (40000, 40)])
+@pytest.mark.parametrize("n,dim", [(5000, 6), (3000, 1028), (40000, 40), (50, 65535)])
 def test_embed_many_rows(n, dim):
     g = gen(n)
     w = randn((n // 3, dim), g)
