@@ -8,8 +8,8 @@
 // is the mean square of the differences from the mean, which costs a second
 // reduction over registers and nothing in memory, and loses nothing where the
 // mean is large.  1M x 384 bf16: 287 us for 1.54 GB, 5.4 TB/s; gradient over
-// 32,768 x 4096 bf16: 158 us for 0.81 GB, 5.1 TB/s, and over 20,000 x 384 f16 13.8
-// + 3.6 us for 46 MB, where starting, the last turns and the sums' join count.
+// 32,768 x 4096 bf16: 158 us for 0.81 GB, 5.1 TB/s, and over 20,000 x 384 f16 12.6
+// + 3.7 us for 46 MB, where starting, the last turns and the sums' join count.
 #include "encoder_internal.h"
 
 namespace ersj {
