@@ -132,7 +132,7 @@ __global__ __launch_bounds__(block_of(L)) void k_norm(NormArgs a)
             b[k] = pb ? __builtin_convertvector(W::load(pb + at.col[k]), fvec) : (fvec)0.f;
         }
     }
-    const float inv = 1.f / (float)a.dim;
+    const float dim = (float)a.dim;  // divided by, not multiplied with its inverse: an exact sum gives an exact mean
     const int64_t step = (int64_t)gridDim.x * kTeams;
     int64_t r = (int64_t)blockIdx.x * kTeams + threadIdx.x / L;
     typename X::vec next[NV];
@@ -160,7 +160,7 @@ __global__ __launch_bounds__(block_of(L)) void k_norm(NormArgs a)
             for (int j = 0; j < LEN; ++j) s[0] += k < NV - 1 || j >= at.skip ? v[k][j] : 0.f;
         }
         team_sum<L, 1>(s, red, slot);
-        const float mean = s[0] * inv;
+        const float mean = s[0] / dim;
         s[0] = 0.f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -169,7 +169,7 @@ __global__ __launch_bounds__(block_of(L)) void k_norm(NormArgs a)
             for (int j = 0; j < LEN; ++j) s[0] += k < NV - 1 || j >= at.skip ? v[k][j] * v[k][j] : 0.f;
         }
         team_sum<L, 1>(s, red, slot);
-        const float rstd = 1.f / sqrtf(s[0] * inv + a.eps);
+        const float rstd = 1.f / sqrtf(s[0] / dim + a.eps);
         if (r < a.n) {
             if ((threadIdx.x & (L - 1)) == 0) {
                 if (a.mean) a.mean[r] = mean;
@@ -198,21 +198,21 @@ __global__ __launch_bounds__(1024) void k_norm_long(NormArgs a)
     __shared__ float red[2][16][1];
     int slot = 0;
     const P *pw = (const P *)a.weight, *pb = (const P *)a.bias;
-    const float inv = 1.f / (float)a.dim;
+    const float dim = (float)a.dim;
     for (int64_t r = blockIdx.x; r < a.n; r += gridDim.x) {
         const T *x = (const T *)a.x + r * a.ld_x;
         T *y = (T *)a.y + r * a.ld_y;
         float s[1] = {0.f};
         for (int c = threadIdx.x; c < a.dim; c += 1024) s[0] += (float)x[c];
         team_sum<1024, 1>(s, red, slot);
-        const float mean = s[0] * inv;
+        const float mean = s[0] / dim;
         s[0] = 0.f;
         for (int c = threadIdx.x; c < a.dim; c += 1024) {
             const float d = (float)x[c] - mean;
             s[0] += d * d;
         }
         team_sum<1024, 1>(s, red, slot);
-        const float rstd = 1.f / sqrtf(s[0] * inv + a.eps);
+        const float rstd = 1.f / sqrtf(s[0] / dim + a.eps);
         if (threadIdx.x == 0) {
             if (a.mean) a.mean[r] = mean;
             if (a.rstd) a.rstd[r] = rstd;

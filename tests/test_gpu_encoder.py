@@ -675,3 +675,13 @@ def test_embed_many_rows(n, dim):
     w = randn((n // 3, dim), g)
     ids = torch.randint(0, n // 3, (n,), generator=g, device=DEV)
     check_embed(ersj.embed(w, ids, 1.5, 7, torch.bfloat16), w, ids, 1.5, 7)
+
+
+@pytest.mark.parametrize("dim", [3, 7, 100, 384, 1001, 6000])
+def test_layer_norm_constant_rows(dim):
+    # integers whose sums are exact: the mean is exact, so y is the bias itself
+    x = torch.tensor([[3.0], [-7.0], [1000.0], [0.0]], device=DEV).expand(4, dim).contiguous()
+    b = randn(dim, gen(dim))
+    y, mean, rstd = ersj.layer_norm(x, None, b, 1e-5)
+    assert mean.tolist() == [3.0, -7.0, 1000.0, 0.0]
+    assert torch.equal(y, b.expand(4, dim))
