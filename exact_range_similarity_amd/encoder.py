@@ -9,7 +9,8 @@ HIP kernels.  ``embed`` and ``layer_norm`` take part in autograd.
 Tensors are float32, float16 or bfloat16 on the GPU.  A tensor of rows may
 have any leading shape as long as its rows are contiguous and equally spaced.
 ``stream`` (a torch stream or a raw handle; None: the current one) is where
-the work is enqueued; outputs belong to that stream.
+the work is enqueued; outputs belong to that stream, and a backward pass through
+them runs on it.
 """
 import ctypes
 
@@ -88,6 +89,14 @@ def _run_elsewhere(device, stream, tensors, call):
             if t is not None:
                 t.record_stream(stream)
         return result
+
+
+def _apply(device, stream, tensors, call):
+    """``call()``, which makes an autograd node, with the stream current: autograd
+    runs the node's backward pass on the stream that was current when it was
+    made, and that has to be the one to whose memory pool the tensors that the
+    forward pass saves belong."""
+    return _run_elsewhere(device, stream, tensors, call) if _elsewhere(device, stream) else call()
 
 
 def _type(t, what):
@@ -184,7 +193,8 @@ def embed(weight, ids, scale=1.0, padding_idx=None, dtype=None, out=None, stream
     if weight.requires_grad and torch.is_grad_enabled():
         if out is not None:
             raise ValueError("out cannot be given where a gradient is wanted")
-        return _Embed.apply(weight, ids, scale, padding_idx, dtype, stream)
+        return _apply(weight.device, stream, (weight, ids),
+                      lambda: _Embed.apply(weight, ids, scale, padding_idx, dtype))
     return _embed(weight, ids, scale, padding_idx, dtype, out, stream)
 
 
@@ -245,16 +255,16 @@ def embed_grad(grad, ids, rows, scale=1.0, padding_idx=None, dtype=None, out=Non
 
 class _Embed(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, weight, ids, scale, padding_idx, dtype, stream):
+    def forward(ctx, weight, ids, scale, padding_idx, dtype):
         ctx.save_for_backward(ids)
         ctx.args = (weight.shape[0], weight.dtype, scale, padding_idx)
-        return _embed(weight, ids, scale, padding_idx, dtype, None, stream)
+        return _embed(weight, ids, scale, padding_idx, dtype, None, None)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
         rows, dtype, scale, padding_idx = ctx.args
-        return embed_grad(grad.contiguous(), ctx.saved_tensors[0], rows, scale, padding_idx, dtype), None, None, None, None, None
+        return embed_grad(grad.contiguous(), ctx.saved_tensors[0], rows, scale, padding_idx, dtype), None, None, None, None
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
@@ -266,7 +276,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
             and torch.is_grad_enabled()):
         if out is not None:
             raise ValueError("out cannot be given where a gradient is wanted")
-        return _LayerNorm.apply(x, weight, bias, eps, stream)
+        return _apply(x.device, stream, (x, weight, bias), lambda: _LayerNorm.apply(x, weight, bias, eps))
     return _layer_norm(x, weight, bias, eps, out, stream)
 
 
@@ -351,8 +361,8 @@ def layer_norm_grad(grad, x, mean, rstd, weight=None, dtype=None, want_x=True, w
 
 class _LayerNorm(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, bias, eps, stream):
-        y, mean, rstd = _layer_norm(x, weight, bias, eps, None, stream)
+    def forward(ctx, x, weight, bias, eps):
+        y, mean, rstd = _layer_norm(x, weight, bias, eps, None, None)
         ctx.save_for_backward(x, weight, mean, rstd)
         ctx.bias_dtype = None if bias is None else bias.dtype
         ctx.mark_non_differentiable(mean, rstd)
@@ -366,7 +376,7 @@ class _LayerNorm(torch.autograd.Function):
         params = need[1] or need[2]
         dtype = ctx.bias_dtype if weight is None else weight.dtype
         gx, gw, gb = layer_norm_grad(grad.contiguous(), x, mean, rstd, weight, dtype, need[0], params)
-        return gx, gw if need[1] else None, gb if need[2] else None, None, None
+        return gx, gw if need[1] else None, gb if need[2] else None, None
 
 
 class GradSet:

@@ -1,0 +1,99 @@
+"""The encoder operators inside autograd: streams, saved tensors, tensors that
+the operators write."""
+import pytest
+import torch
+
+import exact_range_similarity_amd as ersj
+from exact_range_similarity_amd import encoder
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    ersj.lib()
+
+
+@pytest.fixture(autouse=True)
+def _case(request):
+    say(f"[encoder] {request.node.name}")
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def step_inputs(n, rows, dim, seed):
+    g = gen(seed)
+    table = torch.randn((rows, dim), generator=g, device=DEV)
+    gamma = 1 + 0.1 * torch.randn(dim, generator=g, device=DEV)
+    beta = torch.randn(dim, generator=g, device=DEV)
+    ids = torch.randint(0, rows, (n,), generator=g, device=DEV)
+    dy = torch.randn((n, dim), generator=g, device=DEV)
+    return table, gamma, beta, ids, dy
+
+
+def direct(table, gamma, beta, ids, dy):
+    """The same gradients by the direct calls, whose bits are always the same."""
+    e = ersj.embed(table, ids, 2.0)
+    _, mean, rstd = ersj.layer_norm(e, gamma, beta)
+    gx, gw, gb = ersj.layer_norm_grad(dy, e, mean, rstd, gamma)
+    return ersj.embed_grad(gx, ids, len(table), 2.0), gw, gb
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_backward_runs_on_the_given_stream(raw, monkeypatch):
+    side, streams = torch.cuda.Stream(), []
+
+    def noting(call):
+        def noted(*args, **kw):
+            streams.append(torch.cuda.current_stream().cuda_stream)
+            return call(*args, **kw)
+        return noted
+
+    monkeypatch.setattr(encoder, "layer_norm_grad", noting(encoder.layer_norm_grad))
+    monkeypatch.setattr(encoder, "embed_grad", noting(encoder.embed_grad))
+    table, gamma, beta, ids, dy = step_inputs(3000, 500, 64, 1)
+    want = direct(table, gamma, beta, ids, dy)
+    params = [t.clone().requires_grad_() for t in (table, gamma, beta)]
+    side.wait_stream(torch.cuda.current_stream())
+    given = side.cuda_stream if raw else side
+    # the statistics are dropped here, so that only the node holds them
+    y = ersj.layer_norm(ersj.embed(params[0], ids, 2.0, stream=given), *params[1:], stream=given)[0]
+    torch.cuda.current_stream().wait_stream(side)
+    streams.clear()
+    torch.cuda._sleep(500000)  # the gradient of y comes late
+    y.backward(dy * 1.0)
+    # whatever the backward pass released is handed out on the stream again
+    with torch.cuda.stream(side):
+        junk = [torch.full((size,), float("nan"), device=DEV) for size in (3000, 3000 * 64, 3000, 64) for _ in range(20)]
+    torch.cuda.synchronize()
+    assert streams == [side.cuda_stream] * 2
+    for p, ref in zip(params, want):
+        assert torch.equal(p.grad, ref)
+    del junk
+
+
+def test_backward_of_steps_in_a_row_on_a_stream():
+    side = torch.cuda.Stream()
+    table, gamma, beta, _, _ = step_inputs(10, 500, 64, 2)
+    params = [t.clone().requires_grad_() for t in (table, gamma, beta)]
+    total = [torch.zeros_like(t) for t in params]
+    steps = [step_inputs(2000 + 100 * k, 500, 64, 3 + k)[3:] for k in range(6)]
+    for ids, dy in steps:
+        for t, part in zip(total, direct(table, gamma, beta, ids, dy)):
+            t += part
+    side.wait_stream(torch.cuda.current_stream())
+    for ids, dy in steps:
+        y = ersj.layer_norm(ersj.embed(params[0], ids, 2.0, stream=side), *params[1:], stream=side)[0]
+        torch.cuda.current_stream().wait_stream(side)
+        (y * dy).sum().backward()
+    torch.cuda.synchronize()
+    for p, ref in zip(params, total):
+        assert torch.equal(p.grad, ref)
