@@ -1,5 +1,6 @@
 // Token embedding and the gradient of its table.
 #include "encoder_internal.h"
+#include "embed_few_plan.h"
 
 namespace ersj {
 
@@ -737,14 +738,10 @@ __global__ __launch_bounds__(kJoinThreads) void k_embed_grad_join(EmbedGradArgs 
 // 7.3 against 17.1, 1024 tokens and 32,768 rows of 384 bf16 14.7 against 22.1,
 // 250,000 rows of 64 32 against 32; 1024 tokens of one id and 32,768 rows 26
 // against 22, and the gap widens with more tokens: hence the limit.
-constexpr int kFewMax = 1024;
-constexpr int kFewRows = 64;  // one to a lane
 constexpr uint32_t kFewAlone = 32;
-constexpr int kFewThreads = 512;
-constexpr int kFewWaves = kFewThreads / 64;
 
 template <typename T, typename O, typename I, int LEN, int NV>
-__global__ __launch_bounds__(kFewThreads) void k_embed_grad_few(EmbedGradArgs a, int own)
+__global__ __launch_bounds__(kFewThreads) void k_embed_grad_few(EmbedGradArgs a, int own, int64_t base)
 {
     typedef Slot<T, LEN> In;
     typedef Slot<O, LEN> Out;
@@ -758,7 +755,7 @@ __global__ __launch_bounds__(kFewThreads) void k_embed_grad_few(EmbedGradArgs a,
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint64_t below = ((uint64_t)1 << lane) - 1;
     const uint32_t n = (uint32_t)a.n;
-    const int64_t v0 = (int64_t)blockIdx.x * own, v1 = v0 + own < a.rows ? v0 + own : a.rows;
+    const int64_t v0 = base + (int64_t)blockIdx.x * own, v1 = v0 + own < a.rows ? v0 + own : a.rows;
     const int rows = (int)(v1 - v0);
 
     // the tokens of these rows, in order
@@ -1017,12 +1014,12 @@ static void launch_sort(const SortPlan &p, SortSource &src, uint2 *const (&buf)[
 template <typename T, typename O, int LEN, int NV>
 static void launch_few(const EmbedGradArgs &a, int col_blocks, hipStream_t s)
 {
-    // as many rows to a workgroup as leave four workgroups to each CU, and no more than kFewRows
-    const int64_t want = (a.rows + 1023) / 1024;
-    const int own = want < kFewWaves ? kFewWaves : want > kFewRows ? kFewRows : (int)want;
-    const dim3 grid((unsigned)((a.rows + own - 1) / own), col_blocks), block(kFewThreads);
-    if (a.id_type) k_embed_grad_few<T, O, int64_t, LEN, NV><<<grid, block, 0, s>>>(a, own);
-    else k_embed_grad_few<T, O, int32_t, LEN, NV><<<grid, block, 0, s>>>(a, own);
+    const FewPlan p = few_plan(a.rows);
+    for (int64_t v = 0; v < a.rows; v += p.step) {
+        const dim3 grid(few_groups(p, a.rows, v), col_blocks), block(kFewThreads);
+        if (a.id_type) k_embed_grad_few<T, O, int64_t, LEN, NV><<<grid, block, 0, s>>>(a, p.own, v);
+        else k_embed_grad_few<T, O, int32_t, LEN, NV><<<grid, block, 0, s>>>(a, p.own, v);
+    }
 }
 
 template <typename T, typename O, int LEN, int NV>
