@@ -10,7 +10,8 @@ Tensors are float32, float16 or bfloat16 on the GPU.  A tensor of rows may
 have any leading shape as long as its rows are contiguous and equally spaced.
 ``stream`` (a torch stream or a raw handle; None: the current one) is where
 the work is enqueued; outputs belong to that stream, and a backward pass through
-them runs on it.
+them runs on it.  A tensor given as ``out`` must not require a gradient (unless
+gradients are off); what is written counts for autograd as written in place.
 """
 import ctypes
 
@@ -180,7 +181,14 @@ def _given(out, what, shape, dtype, device):
     if not isinstance(out, torch.Tensor) or out.dtype != dtype or out.shape != shape:
         raise ValueError(f"{what} must be a {dtype} tensor of shape {list(shape)}")
     _on(device, out, what)
+    if out.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{what} must not require a gradient")
     return _rows(out, what)[1]
+
+
+# Tells autograd that a tensor, or each of several, was written, so that a
+# backward pass that saved it is refused instead of using the new values.
+_written = torch.autograd.graph.increment_version
 
 
 def embed(weight, ids, scale=1.0, padding_idx=None, dtype=None, out=None, stream=None):
@@ -212,13 +220,16 @@ def _embed(weight, ids, scale, padding_idx, dtype, out, stream):
         raise TypeError("dtype must be float32, float16 or bfloat16")
     ids = _ids(ids, device)
     shape = ids.shape + (dim,)
-    if out is None:
-        out, ldo = torch.empty(shape, dtype=dtype, device=device), dim
-    else:
+    given = out is not None
+    if given:
         ldo = _given(out, "out", shape, dtype, device)
+    else:
+        out, ldo = torch.empty(shape, dtype=dtype, device=device), dim
     _check(_library().ersj_embed(weight.data_ptr(), wt, rows, dim, _rows(weight, "weight")[1], ids.data_ptr(),
                                  _ID_TYPES[ids.dtype], ids.numel(), scale, _padding(padding_idx), out.data_ptr(),
                                  _TYPES[dtype], ldo, _raw_stream(device.index)))
+    if given:
+        _written(out)
     return out
 
 
@@ -243,13 +254,16 @@ def embed_grad(grad, ids, rows, scale=1.0, padding_idx=None, dtype=None, out=Non
     L = _library()
     need = L.ersj_embed_grad_work(n, rows, dim)
     work = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    if out is None:
-        out, ldo = torch.empty((rows, dim), dtype=dtype, device=device), dim
-    else:
+    given = out is not None
+    if given:
         ldo = _given(out, "out", (rows, dim), dtype, device)
+    else:
+        out, ldo = torch.empty((rows, dim), dtype=dtype, device=device), dim
     _check(L.ersj_embed_grad(grad.data_ptr(), gt, _rows(grad, "grad")[1], ids.data_ptr(), _ID_TYPES[ids.dtype], n,
                              scale, _padding(padding_idx), out.data_ptr(), _TYPES[dtype], rows, dim, ldo,
                              1 if accumulate else 0, work.data_ptr() if need else None, need, _raw_stream(device.index)))
+    if given:
+        _written(out)
     return out
 
 
@@ -298,14 +312,17 @@ def _layer_norm(x, weight, bias, eps, out, stream):
         if w is not None and bt != pt:
             raise TypeError("weight and bias must have one type")
         pt, b = bt, bias.data_ptr()
-    if out is None:
-        out, ldy = _empty_rows(x), dim
-    else:
+    given = out is not None
+    if given:
         ldy = _given(out, "out", shape, x.dtype, device)
+    else:
+        out, ldy = _empty_rows(x), dim
     mean = torch.empty(shape[:-1], dtype=torch.float32, device=device)
     rstd = torch.empty_like(mean)
     _check(_library().ersj_layer_norm(x.data_ptr(), xt, n, dim, ldx, w, b, pt, eps, out.data_ptr(), ldy,
                                       mean.data_ptr(), rstd.data_ptr(), _raw_stream(device.index)))
+    if given:
+        _written(out)
     return out, mean, rstd
 
 
@@ -446,4 +463,5 @@ def clip_grads(grads, max_norm, stream=None):
     norm = torch.empty((), dtype=torch.float32, device=device)
     _check(_library().ersj_grads_clip(gs.handle, max_norm, norm.data_ptr(), work.data_ptr(), GRADS_WORK,
                                       _raw_stream(device.index)))
+    _written(gs.grads if gs.out is None else gs.out)
     return norm

@@ -97,3 +97,67 @@ def test_backward_of_steps_in_a_row_on_a_stream():
     torch.cuda.synchronize()
     for p, ref in zip(params, total):
         assert torch.equal(p.grad, ref)
+
+
+# ---- tensors that the operators write ----
+
+def saved_then(write, t):
+    """The backward pass of a product that saved ``t``, which ``write`` overwrites."""
+    w = torch.ones(t.shape, device=DEV, dtype=t.dtype, requires_grad=True)
+    z = (w * t).sum()
+    write()
+    z.backward()
+
+
+def writes(g):
+    """Each call that writes a tensor of the caller's, as (name, tensor, call)."""
+    x = torch.randn((40, 24), generator=g, device=DEV)
+    ids = torch.randint(0, 40, (40,), generator=g, device=DEV)
+    a, b, c, d, e, f = (torch.randn((40, 24), generator=g, device=DEV) for _ in range(6))
+    kept, target = ersj.GradSet([x, e]), ersj.GradSet([x], [f])
+    return [("embed", a, lambda: ersj.embed(x, ids, out=a)),
+            ("embed_grad", b, lambda: ersj.embed_grad(x, ids, 40, out=b)),
+            ("embed_grad accumulate", b, lambda: ersj.embed_grad(x, ids, 40, out=b, accumulate=True)),
+            ("layer_norm", c, lambda: ersj.layer_norm(c, out=c)),
+            ("layer_norm other", d, lambda: ersj.layer_norm(x, out=d)),
+            ("clip_grads kept", e, lambda: ersj.clip_grads(kept, 1.0)),
+            ("clip_grads into others", f, lambda: ersj.clip_grads(target, 1.0)),
+            ("clip_grads", d, lambda: ersj.clip_grads([a, d], 1.0)),
+            ("clip_grads flat", d, lambda: ersj.clip_grads([d.view(-1)[5:17]], 1.0))]
+
+
+def test_autograd_sees_what_is_written():
+    side = torch.cuda.Stream()
+    for name, t, call in writes(gen(5)):
+        before = t._version
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            saved_then(call, t)
+        assert t._version > before, name
+        torch.cuda.synchronize()
+    x, out = torch.randn((2, 40, 24), generator=gen(6), device=DEV)
+    before = out._version
+    ersj.layer_norm(x, out=out, stream=side)
+    torch.cuda.synchronize()
+    assert out._version > before
+    # inputs keep their versions
+    before = x._version
+    ersj.layer_norm_grad(x, x, *ersj.layer_norm(x)[1:])
+    assert x._version == before
+
+
+def test_an_output_that_requires_a_gradient_is_refused():
+    x = torch.randn((40, 24), generator=gen(7), device=DEV)
+    ids = torch.zeros(40, dtype=torch.int64, device=DEV)
+    out = torch.zeros((40, 24), device=DEV, requires_grad=True)
+    for target in (out, out * 1.0):
+        for call in (lambda: ersj.embed(x, ids, out=target), lambda: ersj.layer_norm(x, out=target),
+                     lambda: ersj.embed_grad(x, ids, 40, out=target),
+                     lambda: ersj.embed_grad(x, ids, 40, out=target, accumulate=True)):
+            with pytest.raises(ValueError, match="gradient"):
+                call()
+            with torch.no_grad():  # as torch's own calls with out do
+                call()
+    with torch.inference_mode():
+        y = torch.zeros((40, 24), device=DEV)
+        ersj.layer_norm(x, out=y)
+    assert torch.equal(y, ersj.layer_norm(x)[0])
