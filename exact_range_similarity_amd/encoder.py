@@ -16,6 +16,7 @@ gradients are off); what is written counts for autograd as written in place.
 import ctypes
 
 import torch
+from torch.autograd import forward_ad
 
 _TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # ERSJ_F32, ERSJ_F16, ERSJ_BF16
 _ID_TYPES = {torch.int32: 0, torch.int64: 1}                      # ERSJ_I32, ERSJ_I64
@@ -51,6 +52,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+# the forward-mode level that is open (-1: none), where torch tells it without a look at a tensor
+_dual_level = (lambda: forward_ad._current_level) if hasattr(forward_ad, "_current_level") else (lambda: 0)
 
 
 def _library():
@@ -104,6 +108,8 @@ def _type(t, what):
     if isinstance(t, torch.Tensor):
         code = _TYPES.get(t.dtype)
         if code is not None:
+            if _dual_level() >= 0 and forward_ad.unpack_dual(t).tangent is not None:
+                raise NotImplementedError(f"{what} has a forward-mode tangent, for which there is no rule")
             return code
     raise TypeError(f"{what} must be a float32, float16 or bfloat16 tensor")
 

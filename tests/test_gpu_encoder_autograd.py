@@ -161,3 +161,32 @@ def test_an_output_that_requires_a_gradient_is_refused():
         y = torch.zeros((40, 24), device=DEV)
         ersj.layer_norm(x, out=y)
     assert torch.equal(y, ersj.layer_norm(x)[0])
+
+
+# ---- forward mode ----
+
+def test_forward_tangents_are_refused():
+    # there is no forward-mode rule: a tangent must not be dropped in silence
+    fwd = torch.autograd.forward_ad
+    g = gen(8)
+    x, t = torch.randn((2, 40, 24), generator=g, device=DEV)
+    v, tv = torch.randn((2, 24), generator=g, device=DEV)
+    ids = torch.randint(0, 40, (40,), generator=g, device=DEV)
+    mean, rstd = ersj.layer_norm(x)[1:]
+    with fwd.dual_level():
+        dx, dv = fwd.make_dual(x, t), fwd.make_dual(v, tv)
+        for call in (lambda: ersj.embed(dx, ids), lambda: ersj.layer_norm(dx), lambda: ersj.layer_norm(x, dv),
+                     lambda: ersj.layer_norm(x, None, dv), lambda: ersj.embed_grad(dx, ids, 40),
+                     lambda: ersj.layer_norm_grad(dx, x, mean, rstd), lambda: ersj.layer_norm_grad(x, dx, mean, rstd),
+                     lambda: ersj.clip_grads([x * 1, dx], 1.0)):
+            with pytest.raises(NotImplementedError):
+                call()
+            with torch.no_grad(), pytest.raises(NotImplementedError):
+                call()
+        w = x.clone().requires_grad_()
+        with pytest.raises(NotImplementedError):
+            ersj.embed(fwd.make_dual(w, t), ids)
+        # tensors without a tangent are as ever
+        assert torch.equal(ersj.embed(x, ids), x[ids])
+        ersj.embed(w, ids).backward(x)
+        assert torch.equal(w.grad, ersj.embed_grad(x, ids, 40))
