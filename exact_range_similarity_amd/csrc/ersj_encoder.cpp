@@ -1,5 +1,5 @@
 // C ABI of the encoder operators (see include/ersj_encoder.h): argument
-// validation, and the chunk table of a set of gradients.
+// validation, and the chunks of a set of gradients.
 #include "ersj_encoder.h"
 #include "encoder_internal.h"
 
@@ -9,7 +9,6 @@
 #include <cstdarg>
 #include <cstdio>
 #include <exception>
-#include <vector>
 
 using namespace ersj;
 
@@ -87,19 +86,65 @@ int check_work(const void *work, uint64_t have, uint64_t need, size_t align)
     return ERSJ_OK;
 }
 
-// Elements of a tensor's first chunk: those after it begin at whole cache
-// lines, wherever the tensor lies in a larger buffer (300 odd-sized bf16 views
-// of 100M elements: 126 us, 130 with chunks that begin as the tensors do).
-int64_t first_chunk(const void *p, int32_t type)
-{
-    return (int64_t)(kGradChunkBytes - ((uintptr_t)p & 127)) / elem_size(type);
-}
-
 #define TRY(expr)                       \
     do {                                \
         int r__ = (expr);               \
         if (r__ != ERSJ_OK) return r__; \
     } while (0)
+
+int check_clip(float max_norm, const float *d_norm, const void *d_work, uint64_t have, uint64_t need)
+{
+    if (!(max_norm >= 0.f)) return refuse("max_norm = %g: must not be negative", (double)max_norm);
+    if (!aligned(d_norm, 4)) return refuse("d_norm is not aligned to 4 bytes");
+    return check_work(d_work, have, need, 8);
+}
+
+// Checks the tensors of a set; *total: how many chunks they have.
+int check_grads(int32_t count, const void *const *d_grad, void *const *d_out, const int64_t *size,
+                const int32_t *type, uint32_t *total)
+{
+    if (count < 1 || count > 65536) return refuse("count = %d: must be in [1, 65536]", count);
+    if (!d_grad || !size || !type) return refuse("d_grad, size or type is NULL");
+    uint64_t chunks = 0;
+    for (int32_t i = 0; i < count; ++i) {
+        if (!is_type(type[i])) return refuse("tensor %d: unknown element type %d", i, type[i]);
+        if (size[i] < 0 || size[i] > (int64_t)1 << 40)
+            return refuse("tensor %d: size %lld is out of range", i, (long long)size[i]);
+        if (size[i] == 0) continue;
+        if (!d_grad[i] || (d_out && !d_out[i])) return refuse("tensor %d is NULL", i);
+        if (!aligned(d_grad[i], elem_size(type[i])) || (d_out && !aligned(d_out[i], elem_size(type[i]))))
+            return refuse("tensor %d is not aligned to its element size", i);
+        const int64_t first = first_chunk(d_grad[i], type[i]), step = kGradChunkBytes / elem_size(type[i]);
+        chunks += 1 + (size[i] > first ? (uint64_t)((size[i] - first + step - 1) / step) : 0);
+    }
+    // half a terabyte, more than the memory of any one device
+    if (chunks > ((uint64_t)1 << 24)) return refuse("the tensors hold too many elements");
+    *total = (uint32_t)chunks;
+    return ERSJ_OK;
+}
+
+// Enqueues the kernels that write the chunks of tensors that check_grads passed.
+hipError_t write_chunks(int32_t count, const void *const *d_grad, void *const *d_out, const int64_t *size,
+                        const int32_t *type, GradChunk *chunks, hipStream_t stream)
+{
+    GradTensors t;
+    t.count = 0;
+    t.end = 0;
+    for (int32_t i = 0; i < count; ++i) {
+        if (size[i]) {
+            const int64_t first = first_chunk(d_grad[i], type[i]), step = kGradChunkBytes / elem_size(type[i]);
+            t.t[t.count++] = GradTensor{d_grad[i], d_out ? d_out[i] : const_cast<void *>(d_grad[i]), size[i], type[i],
+                                        t.end};
+            t.end += 1 + (size[i] > first ? (uint32_t)((size[i] - first + step - 1) / step) : 0);
+        }
+        if (t.count == kGradTensors || (i == count - 1 && t.count)) {
+            const hipError_t e = launch_grads_table(t, chunks, stream);
+            if (e != hipSuccess) return e;
+            t.count = 0;
+        }
+    }
+    return hipSuccess;
+}
 
 }  // namespace
 
@@ -199,40 +244,11 @@ int ersj_grads_create(int32_t count, const void *const *d_grad, void *const *d_o
 {
     if (!out) return refuse("out is NULL");
     *out = nullptr;
-    if (count < 1 || count > 65536) return refuse("count = %d: must be in [1, 65536]", count);
-    if (!d_grad || !size || !type) return refuse("d_grad, size or type is NULL");
-    uint64_t total = 0;
-    for (int32_t i = 0; i < count; ++i) {
-        if (!is_type(type[i])) return refuse("tensor %d: unknown element type %d", i, type[i]);
-        if (size[i] < 0 || size[i] > (int64_t)1 << 40)
-            return refuse("tensor %d: size %lld is out of range", i, (long long)size[i]);
-        if (size[i] == 0) continue;
-        if (!d_grad[i] || (d_out && !d_out[i])) return refuse("tensor %d is NULL", i);
-        if (!aligned(d_grad[i], elem_size(type[i])) || (d_out && !aligned(d_out[i], elem_size(type[i]))))
-            return refuse("tensor %d is not aligned to its element size", i);
-        const int64_t first = first_chunk(d_grad[i], type[i]), step = kGradChunkBytes / elem_size(type[i]);
-        total += 1 + (size[i] > first ? (uint64_t)((size[i] - first + step - 1) / step) : 0);
-    }
-    // half a terabyte, more than the memory of any one device
-    if (total > ((uint64_t)1 << 24)) return refuse("the tensors hold too many elements");
+    uint32_t total = 0;
+    TRY(check_grads(count, d_grad, d_out, size, type, &total));
     try {
-        std::vector<GradChunk> table;
-        table.reserve(total);
-        for (int32_t i = 0; i < count; ++i) {
-            const size_t es = elem_size(type[i]);
-            const int64_t step = kGradChunkBytes / es;
-            int64_t len = first_chunk(d_grad[i], type[i]);
-            for (int64_t k = 0; k < size[i]; k += len, len = step) {
-                GradChunk c{};
-                c.in = (const char *)d_grad[i] + k * es;
-                c.out = d_out ? (char *)d_out[i] + k * es : (char *)const_cast<void *>(d_grad[i]) + k * es;
-                c.count = (uint32_t)(size[i] - k < len ? size[i] - k : len);
-                c.type = type[i];
-                table.push_back(c);
-            }
-        }
         ersj_grads *h = new ersj_grads;
-        h->n_chunks = (uint32_t)total;
+        h->n_chunks = total;
         h->bytes = total * sizeof(GradChunk);
         int r = ERSJ_OK;
         if (total) {
@@ -243,9 +259,9 @@ int ersj_grads_create(int32_t count, const void *const *d_grad, void *const *d_o
                 h->chunks = (GradChunk *)p;
             }
             if (r == ERSJ_OK)
-                r = done(hipMemcpyAsync(h->chunks, table.data(), h->bytes, hipMemcpyHostToDevice,
-                                        (hipStream_t)stream), "copy");
-            if (r == ERSJ_OK) r = done(hipStreamSynchronize((hipStream_t)stream), "copy");
+                r = done(write_chunks(count, d_grad, d_out, size, type, h->chunks, (hipStream_t)stream),
+                         "table of a set of gradients");
+            if (r == ERSJ_OK) r = done(hipStreamSynchronize((hipStream_t)stream), "table of a set of gradients");
         }
         if (r != ERSJ_OK) {
             ersj_grads_free(h);
@@ -254,7 +270,7 @@ int ersj_grads_create(int32_t count, const void *const *d_grad, void *const *d_o
         *out = h;
         return ERSJ_OK;
     } catch (const std::exception &) {
-        return set_error(ERSJ_ERR_OOM, "host memory for the table of a set of gradients");
+        return set_error(ERSJ_ERR_OOM, "host memory for a set of gradients");
     }
 }
 
@@ -262,10 +278,32 @@ int ersj_grads_clip(const ersj_grads *h, float max_norm, float *d_norm, void *d_
                     void *stream)
 {
     if (!h) return refuse("handle is NULL");
-    if (!(max_norm >= 0.f)) return refuse("max_norm = %g: must not be negative", (double)max_norm);
-    if (!aligned(d_norm, 4)) return refuse("d_norm is not aligned to 4 bytes");
-    TRY(check_work(d_work, d_work_bytes, ERSJ_GRADS_WORK, 8));
+    TRY(check_clip(max_norm, d_norm, d_work, d_work_bytes, ERSJ_GRADS_WORK));
     return done(launch_grads_clip(h->chunks, h->n_chunks, max_norm, d_norm, d_work, (hipStream_t)stream),
+                "gradient clipping kernels");
+}
+
+uint64_t ersj_clip_tensors_work(int32_t count, const int64_t *size, const int32_t *type)
+{
+    if (count < 1 || count > 65536 || !size || !type) return 0;
+    uint64_t chunks = 0;  // the most that the tensors have at any alignment
+    for (int32_t i = 0; i < count; ++i) {
+        if (!is_type(type[i]) || size[i] < 0 || size[i] > (int64_t)1 << 40) return 0;
+        if (size[i]) chunks += 2 + (uint64_t)size[i] * elem_size(type[i]) / kGradChunkBytes;
+    }
+    return ERSJ_GRADS_WORK + chunks * sizeof(GradChunk);
+}
+
+int ersj_clip_tensors(int32_t count, const void *const *d_grad, void *const *d_out, const int64_t *size,
+                      const int32_t *type, float max_norm, float *d_norm, void *d_work, uint64_t d_work_bytes,
+                      void *stream)
+{
+    uint32_t total = 0;
+    TRY(check_grads(count, d_grad, d_out, size, type, &total));
+    TRY(check_clip(max_norm, d_norm, d_work, d_work_bytes, ersj_clip_tensors_work(count, size, type)));
+    GradChunk *chunks = (GradChunk *)((char *)d_work + ERSJ_GRADS_WORK);
+    TRY(done(write_chunks(count, d_grad, d_out, size, type, chunks, (hipStream_t)stream), "table of gradients"));
+    return done(launch_grads_clip(chunks, total, max_norm, d_norm, d_work, (hipStream_t)stream),
                 "gradient clipping kernels");
 }
 

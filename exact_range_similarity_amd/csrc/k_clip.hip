@@ -123,7 +123,37 @@ __global__ __launch_bounds__(kThreads) void k_grad_scale(const GradChunk *chunks
     }
 }
 
+// The chunks of up to kGradTensors tensors, one to a thread.
+__global__ __launch_bounds__(kThreads) void k_grad_table(GradTensors t, GradChunk *chunks)
+{
+    const uint32_t c = t.t[0].first + blockIdx.x * kThreads + threadIdx.x;
+    if (c >= t.end) return;
+    int lo = 0, hi = t.count - 1;  // the last tensor whose first chunk is not after c
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (t.t[mid].first <= c) lo = mid;
+        else hi = mid - 1;
+    }
+    const GradTensor g = t.t[lo];
+    const int64_t es = elem_size(g.type), step = kGradChunkBytes / es, lead = first_chunk(g.in, g.type);
+    const uint32_t k = c - g.first;
+    const int64_t at = k ? lead + (int64_t)(k - 1) * step : 0, len = k ? step : lead;
+    GradChunk out;
+    out.in = (const char *)g.in + at * es;
+    out.out = (char *)g.out + at * es;
+    out.count = (uint32_t)(g.size - at < len ? g.size - at : len);
+    out.type = g.type;
+    chunks[c] = out;
+}
+
 }  // namespace
+
+hipError_t launch_grads_table(const GradTensors &t, GradChunk *chunks, hipStream_t s)
+{
+    const uint32_t n = t.end - t.t[0].first;
+    k_grad_table<<<dim3((n + kThreads - 1) / kThreads), dim3(kThreads), 0, s>>>(t, chunks);
+    return hipGetLastError();
+}
 
 hipError_t launch_grads_clip(const GradChunk *chunks, uint32_t n_chunks, float max_norm, float *norm, void *work,
                              hipStream_t s)

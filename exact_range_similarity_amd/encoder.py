@@ -24,7 +24,7 @@ GRADS_WORK = 16384                                                # ERSJ_GRADS_W
 
 ENCODER_SYMBOLS = ("ersj_embed", "ersj_embed_grad", "ersj_embed_grad_work", "ersj_layer_norm",
                    "ersj_layer_norm_grad", "ersj_layer_norm_grad_work", "ersj_grads_create", "ersj_grads_clip",
-                   "ersj_grads_free")
+                   "ersj_grads_free", "ersj_clip_tensors", "ersj_clip_tensors_work")
 
 
 def declare(L):
@@ -41,6 +41,9 @@ def declare(L):
     L.ersj_layer_norm_grad_work.restype = u64
     L.ersj_grads_create.argtypes = [i32, vp, vp, vp, vp, vp, ctypes.POINTER(vp)]
     L.ersj_grads_clip.argtypes = [vp, f32, vp, vp, u64, vp]
+    L.ersj_clip_tensors.argtypes = [i32, vp, vp, vp, vp, f32, vp, vp, u64, vp]
+    L.ersj_clip_tensors_work.argtypes = [i32, vp, vp]
+    L.ersj_clip_tensors_work.restype = u64
     L.ersj_grads_free.argtypes = [vp]
     L.ersj_grads_free.restype = None
     _lib = L
@@ -402,6 +405,31 @@ class _LayerNorm(torch.autograd.Function):
         return gx, gw if need[1] else None, gb if need[2] else None, None
 
 
+def _tensor_arrays(grads, out):
+    """(count, addresses, those of the outputs or None, sizes, types) of tensors
+    to clip, checked, as the entry points take them."""
+    if not grads:
+        raise ValueError("grads is empty")
+    if out is not None and len(out) != len(grads):
+        raise ValueError(f"out holds {len(out)} tensors, grads {len(grads)}")
+    types = []
+    for i, g in enumerate(grads):
+        types.append(_type(g, f"grads[{i}]"))
+        if not g.is_contiguous():
+            raise ValueError(f"grads[{i}] must be contiguous")
+        _on(grads[0].device, g, f"grads[{i}]")
+        if out is not None:
+            o = out[i]
+            if not isinstance(o, torch.Tensor) or o.dtype != g.dtype or o.shape != g.shape or not o.is_contiguous():
+                raise ValueError(f"out[{i}] must be a contiguous tensor of the type and shape of grads[{i}]")
+            _on(g.device, o, f"out[{i}]")
+    n = len(grads)
+    addresses = ctypes.c_void_p * n
+    return (n, addresses(*[g.data_ptr() for g in grads]),
+            None if out is None else addresses(*[o.data_ptr() for o in out]),
+            (ctypes.c_int64 * n)(*[g.numel() for g in grads]), (ctypes.c_int32 * n)(*types))
+
+
 class GradSet:
     """Owner of an ``ersj_grads*``: gradient tensors that are clipped together.
 
@@ -415,30 +443,11 @@ class GradSet:
         self.handle = ctypes.c_void_p()
         self.grads = list(grads)
         self.out = None if out is None else list(out)
-        if not self.grads:
-            raise ValueError("grads is empty")
-        if self.out is not None and len(self.out) != len(self.grads):
-            raise ValueError(f"out holds {len(self.out)} tensors, grads {len(self.grads)}")
-        for i, g in enumerate(self.grads):
-            _type(g, f"grads[{i}]")
-            if not g.is_contiguous():
-                raise ValueError(f"grads[{i}] must be contiguous")
-            _on(self.grads[0].device, g, f"grads[{i}]")
-            if self.out is not None:
-                o = self.out[i]
-                if not isinstance(o, torch.Tensor) or o.dtype != g.dtype or o.shape != g.shape or not o.is_contiguous():
-                    raise ValueError(f"out[{i}] must be a contiguous tensor of the type and shape of grads[{i}]")
-                _on(g.device, o, f"out[{i}]")
-        n = len(self.grads)
+        arrays = _tensor_arrays(self.grads, self.out)
         self.device = self.grads[0].device
-        ptrs = (ctypes.c_void_p * n)(*[g.data_ptr() for g in self.grads])
-        outs = None if self.out is None else (ctypes.c_void_p * n)(*[o.data_ptr() for o in self.out])
-        sizes = (ctypes.c_int64 * n)(*[g.numel() for g in self.grads])
-        types = (ctypes.c_int32 * n)(*[_TYPES[g.dtype] for g in self.grads])
 
         def create():
-            _check(_library().ersj_grads_create(n, ptrs, outs, sizes, types, _raw_stream(self.device.index),
-                                                ctypes.byref(self.handle)))
+            _check(_library().ersj_grads_create(*arrays, _raw_stream(self.device.index), ctypes.byref(self.handle)))
 
         if _elsewhere(self.device, stream):
             _run_elsewhere(self.device, stream, (), create)
@@ -460,14 +469,27 @@ class GradSet:
 def clip_grads(grads, max_norm, stream=None):
     """``ersj_grads_clip``: scale the gradients so that their global norm is at
     most ``max_norm``; the norm before, as a float32 tensor of no dimensions.
-    ``grads``: a ``GradSet``, or tensors to clip in place."""
-    gs = grads if isinstance(grads, GradSet) else GradSet(grads, stream=stream)
-    device = gs.device
+    ``grads``: a ``GradSet``, or tensors to clip in place (``ersj_clip_tensors``;
+    they may be others on every call)."""
+    kept = grads if isinstance(grads, GradSet) else None
+    if kept is None:
+        grads = list(grads)
+        arrays = _tensor_arrays(grads, None)
+        device = grads[0].device
+    else:
+        device = kept.device
     if _elsewhere(device, stream):
-        return _run_elsewhere(device, stream, gs.grads + (gs.out or []), lambda: clip_grads(gs, max_norm))
-    work = torch.empty(GRADS_WORK, dtype=torch.uint8, device=device)
+        tensors = grads if kept is None else kept.grads + (kept.out or [])
+        return _run_elsewhere(device, stream, tensors, lambda: clip_grads(grads, max_norm))
+    L = _library()
+    need = GRADS_WORK if kept else L.ersj_clip_tensors_work(arrays[0], *arrays[3:])
+    work = torch.empty(need, dtype=torch.uint8, device=device)
     norm = torch.empty((), dtype=torch.float32, device=device)
-    _check(_library().ersj_grads_clip(gs.handle, max_norm, norm.data_ptr(), work.data_ptr(), GRADS_WORK,
-                                      _raw_stream(device.index)))
-    _written(gs.grads if gs.out is None else gs.out)
+    end = (max_norm, norm.data_ptr(), work.data_ptr(), need, _raw_stream(device.index))
+    if kept:
+        _check(L.ersj_grads_clip(kept.handle, *end))
+        _written(kept.grads if kept.out is None else kept.out)
+    else:
+        _check(L.ersj_clip_tensors(*arrays, *end))
+        _written(grads)
     return norm

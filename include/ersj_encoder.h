@@ -12,7 +12,8 @@
  * ersj_last_error, arguments validated before any HIP call), and further:
  *  - No call waits for the device, allocates device memory or copies to the
  *    host, except ersj_grads_create and ersj_grads_free.  Every call can be
- *    captured into a graph, those two excepted.
+ *    captured into a graph, those two excepted.  Host arrays are read before
+ *    the call returns.
  *  - Working memory is the caller's (d_work); its contents need no
  *    preparation and mean nothing afterwards.  Calls that overlap in time
  *    need one each.
@@ -130,7 +131,11 @@ uint64_t ersj_layer_norm_grad_work(int64_t n, int32_t dim);
  *  size   : host array [count], elements of each tensor, >= 0, contiguous.
  *  type   : host array [count], ERSJ_F32, ERSJ_F16 or ERSJ_BF16; input and
  *           output have the same type.
- * The stream is synchronised on return.  Errors: INVALID_ARG, HIP, OOM.
+ * For tensors that are clipped many times: the table comes from the library's
+ * device memory, and the call waits for its stream, and for the whole device
+ * where it takes a table that ersj_grads_free has returned since the last such
+ * wait.  For tensors whose addresses change from call to call there is
+ * ersj_clip_tensors.  Errors: INVALID_ARG, HIP, OOM.
  */
 typedef struct ersj_grads ersj_grads;
 int ersj_grads_create(int32_t count, const void *const *d_grad, void *const *d_out, const int64_t *size,
@@ -151,6 +156,21 @@ int ersj_grads_create(int32_t count, const void *const *d_grad, void *const *d_o
 #define ERSJ_GRADS_WORK 16384
 int ersj_grads_clip(const ersj_grads *h, float max_norm, float *d_norm, void *d_work, uint64_t d_work_bytes,
                     void *stream);
+
+/*
+ * ersj_grads_clip of tensors given as to ersj_grads_create, without a handle:
+ * the table is made in d_work by kernels that carry the tensors' addresses in
+ * their arguments, and nothing is waited for.
+ *  d_work   : at least ersj_clip_tensors_work(count, size, type) bytes,
+ *             aligned to 8.
+ * Errors: INVALID_ARG, HIP.
+ */
+int ersj_clip_tensors(int32_t count, const void *const *d_grad, void *const *d_out, const int64_t *size,
+                      const int32_t *type, float max_norm, float *d_norm, void *d_work, uint64_t d_work_bytes,
+                      void *stream);
+/* Bytes of working memory for tensors of those sizes, wherever they lie (0 for
+ * sizes that are refused). */
+uint64_t ersj_clip_tensors_work(int32_t count, const int64_t *size, const int32_t *type);
 
 /* Release the handle (NULL is a no-op).  Work enqueued with it may still be
  * running: its memory is kept, as ersj_free keeps an index's, and handed out
