@@ -532,8 +532,9 @@ __global__ __launch_bounds__(kThreads) void k_embed_grad_sum(EmbedGradArgs a, co
             flag |= kFirstCut;
         } else if (any || !a.accumulate) {
             O *out = (O *)a.out + (int64_t)v * a.ld_out;
+            const float scale = any ? a.scale : 1.f;  // zeros stay zeros under a scale of infinity or NaN
 #pragma unroll
-            for (int k = 0; k < NV; ++k) acc[k] *= a.scale;
+            for (int k = 0; k < NV; ++k) acc[k] *= scale;
             if (a.accumulate) {  // all read before any is written: shifted vectors overlap
 #pragma unroll
                 for (int k = 0; k < NV; ++k)
@@ -794,10 +795,11 @@ __global__ __launch_bounds__(kFewThreads) void k_embed_grad_few(EmbedGradArgs a,
         const int last = c0 + block_cols < a.dim ? c0 + block_cols - LEN : a.dim - LEN;
         cols[k] = (uint32_t)(c0 + c < last ? c0 + c : last);
     }
-    auto write = [&](int r, fvec (&acc)[NV]) {
+    auto write = [&](int r, bool any, fvec (&acc)[NV]) {
         O *out = (O *)a.out + (v0 + r) * a.ld_out;
+        const float scale = any ? a.scale : 1.f;  // zeros stay zeros under a scale of infinity or NaN
 #pragma unroll
-        for (int k = 0; k < NV; ++k) acc[k] *= a.scale;
+        for (int k = 0; k < NV; ++k) acc[k] *= scale;
         if (a.accumulate) {  // all read before any is written: shifted vectors overlap
 #pragma unroll
             for (int k = 0; k < NV; ++k)
@@ -813,7 +815,7 @@ __global__ __launch_bounds__(kFewThreads) void k_embed_grad_few(EmbedGradArgs a,
         for (int r = wave; r < rows; r += kFewWaves) {
 #pragma unroll
             for (int k = 0; k < NV; ++k) acc[k] = (fvec)0.f;
-            write(r, acc);
+            write(r, false, acc);
         }
         return;
     }
@@ -888,7 +890,7 @@ __global__ __launch_bounds__(kFewThreads) void k_embed_grad_few(EmbedGradArgs a,
         const uint32_t c = __builtin_amdgcn_readfirstlane(count[r]), p = __builtin_amdgcn_readfirstlane(first[r]);
         if (c > kFewAlone || (c == 0 && a.accumulate)) continue;
         sum(p, p + c, acc);
-        write(r, acc);
+        write(r, c > 0, acc);
     }
     if (total <= kFewAlone) return;
     for (int r = 0; r < rows; ++r) {  // the same for all waves
@@ -904,7 +906,7 @@ __global__ __launch_bounds__(kFewThreads) void k_embed_grad_few(EmbedGradArgs a,
                 acc[k] = sums[0][k][lane];
                 for (int j = 1; j < kFewWaves; ++j) acc[k] += sums[j][k][lane];
             }
-            write(r, acc);
+            write(r, true, acc);
         }
         __syncthreads();
     }

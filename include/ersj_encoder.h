@@ -63,7 +63,8 @@ int ersj_embed(const void *d_table, int32_t table_type, int64_t rows, int32_t di
  * whose sums are then added.
  *  d_grad     : device [n][ld_grad] of grad_type.
  *  d_out      : device [rows][ld_out] of out_type: grad_type, or ERSJ_F32.
- *               Every row is written; a row without tokens gets zeros.
+ *               Every row is written; a row without tokens gets zeros, also
+ *               where the scale is infinite or NaN.
  *  accumulate : nonzero: add the sums to out instead (rows without tokens
  *               are left alone); the addition is made in 32 bits and rounded
  *               once.
