@@ -5,10 +5,12 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <exception>
+#include <vector>
 
 using namespace ersj;
 
@@ -97,6 +99,47 @@ int check_clip(float max_norm, const float *d_norm, const void *d_work, uint64_t
     if (!(max_norm >= 0.f)) return refuse("max_norm = %g: must not be negative", (double)max_norm);
     if (!aligned(d_norm, 4)) return refuse("d_norm is not aligned to 4 bytes");
     return check_work(d_work, have, need, 8);
+}
+
+// Whether memory that is written for one tensor is read or written for another
+// as well, or for the same one at another place.
+bool shared_memory(int32_t count, const void *const *d_grad, void *const *d_out, const int64_t *size,
+                   const int32_t *type)
+{
+    struct Range {
+        uintptr_t first, end;
+        bool operator<(const Range &r) const { return first < r.first; }
+    };
+    auto range = [&](const void *p, int32_t i) {
+        return Range{(uintptr_t)p, (uintptr_t)p + (uintptr_t)size[i] * elem_size(type[i])};
+    };
+    std::vector<Range> written;
+    written.reserve(count);
+    for (int32_t i = 0; i < count; ++i)
+        if (size[i]) written.push_back(range(d_out ? d_out[i] : d_grad[i], i));
+    if (!std::is_sorted(written.begin(), written.end())) std::sort(written.begin(), written.end());
+    for (size_t k = 1; k < written.size(); ++k)
+        if (written[k].first < written[k - 1].end) return true;
+    for (int32_t i = 0; d_out && i < count; ++i) {
+        if (!size[i] || d_out[i] == d_grad[i]) continue;
+        const Range in = range(d_grad[i], i);
+        // the last range that begins before the input's end
+        auto at = std::lower_bound(written.begin(), written.end(), Range{in.end, 0});
+        if (at != written.begin() && (at - 1)->end > in.first) return true;
+    }
+    return false;
+}
+
+int check_shared_memory(int32_t count, const void *const *d_grad, void *const *d_out, const int64_t *size,
+                        const int32_t *type)
+{
+    try {
+        if (shared_memory(count, d_grad, d_out, size, type))
+            return refuse("tensors share memory that is written");
+    } catch (const std::exception &) {
+        return set_error(ERSJ_ERR_OOM, "host memory for the check of a set of gradients");
+    }
+    return ERSJ_OK;
 }
 
 // Checks the tensors of a set; *total: how many chunks they have.
@@ -253,6 +296,7 @@ int ersj_grads_create(int32_t count, const void *const *d_grad, void *const *d_o
         int r = ERSJ_OK;
         if (total) {
             r = done(hipGetDevice(&h->device), "hipGetDevice");
+            if (r == ERSJ_OK) r = check_shared_memory(count, d_grad, d_out, size, type);
             if (r == ERSJ_OK) {
                 void *p = nullptr;
                 r = done(device_block_get(h->device, h->bytes, &p), "table of a set of gradients");
@@ -301,6 +345,7 @@ int ersj_clip_tensors(int32_t count, const void *const *d_grad, void *const *d_o
     uint32_t total = 0;
     TRY(check_grads(count, d_grad, d_out, size, type, &total));
     TRY(check_clip(max_norm, d_norm, d_work, d_work_bytes, ersj_clip_tensors_work(count, size, type)));
+    TRY(check_shared_memory(count, d_grad, d_out, size, type));
     GradChunk *chunks = (GradChunk *)((char *)d_work + ERSJ_GRADS_WORK);
     TRY(done(write_chunks(count, d_grad, d_out, size, type, chunks, (hipStream_t)stream), "table of gradients"));
     return done(launch_grads_clip(chunks, total, max_norm, d_norm, d_work, (hipStream_t)stream),

@@ -435,9 +435,10 @@ class GradSet:
 
     ``grads``: contiguous GPU tensors on one device, of any types and sizes.
     ``out``: tensors of the same shapes and types that receive the clipped
-    gradients; None clips in place.  The set keeps the tensors alive and reads
-    their values anew on every call; it is made once for tensors that a
-    training loop reuses, and has to outlive a captured graph that clips it."""
+    gradients; None clips in place.  Tensors that share memory are refused where
+    it is written.  The set keeps the tensors alive and reads their values anew
+    on every call; it is made once for tensors that a training loop reuses, and
+    has to outlive a captured graph that clips it."""
 
     def __init__(self, grads, out=None, stream=None):
         self.handle = ctypes.c_void_p()
@@ -470,7 +471,7 @@ def clip_grads(grads, max_norm, stream=None):
     """``ersj_grads_clip``: scale the gradients so that their global norm is at
     most ``max_norm``; the norm before, as a float32 tensor of no dimensions.
     ``grads``: a ``GradSet``, or tensors to clip in place (``ersj_clip_tensors``;
-    they may be others on every call)."""
+    they may be others on every call; none may share memory with another)."""
     kept = grads if isinstance(grads, GradSet) else None
     if kept is None:
         grads = list(grads)

@@ -128,7 +128,8 @@ uint64_t ersj_layer_norm_grad_work(int64_t n, int32_t dim);
  *  d_grad : host array [count] of device pointers (NULL where size is 0).
  *  d_out  : host array [count] of device pointers for the clipped tensors, or
  *           NULL to clip in place.  A tensor's own entry may equal its
- *           d_grad; otherwise no output may overlap an input.
+ *           d_grad; otherwise no output may overlap an input or another
+ *           output (INVALID_ARG).
  *  size   : host array [count], elements of each tensor, >= 0, contiguous.
  *  type   : host array [count], ERSJ_F32, ERSJ_F16 or ERSJ_BF16; input and
  *           output have the same type.
@@ -164,7 +165,7 @@ int ersj_grads_clip(const ersj_grads *h, float max_norm, float *d_norm, void *d_
  * their arguments, and nothing is waited for.
  *  d_work   : at least ersj_clip_tensors_work(count, size, type) bytes,
  *             aligned to 8.
- * Errors: INVALID_ARG, HIP.
+ * Errors: INVALID_ARG, HIP, OOM.
  */
 int ersj_clip_tensors(int32_t count, const void *const *d_grad, void *const *d_out, const int64_t *size,
                       const int32_t *type, float max_norm, float *d_norm, void *d_work, uint64_t d_work_bytes,

@@ -61,3 +61,47 @@ def test_binding_rejects_tensors():
     for bad in ([w.t()], [w, w[:, :3]], []):
         with pytest.raises(ValueError):
             ersj.clip_grads(bad, 1.0)
+
+
+def overlap_cases():
+    a, b, c = FAKE, 2 * FAKE, 3 * FAKE
+    f32, sizes = (0, 0), (100, 50)
+    return [
+        ("one tensor twice", dict(ptrs=(a, a), sizes=(100, 100), types=f32), False),
+        ("a part of another", dict(ptrs=(a, a + 396), sizes=sizes, types=f32), False),
+        ("a part of another, first", dict(ptrs=(a + 196, a), sizes=sizes, types=f32), False),
+        ("a part of another, within", dict(ptrs=(a, a + 40), sizes=sizes, types=f32), False),
+        ("end to end", dict(ptrs=(a, a + 400), sizes=sizes, types=f32), True),
+        ("end to end, 16 bits", dict(ptrs=(a + 100, a), sizes=(100, 50), types=(0, 2)), True),
+        ("empty and anywhere", dict(ptrs=(a, a + 4), sizes=(100, 0), types=f32), True),
+        ("one output for two", dict(ptrs=(a, b), outs=(c, c), sizes=sizes, types=f32), False),
+        ("an output in another's input", dict(ptrs=(a, b), outs=(c, a + 4), sizes=sizes, types=f32), False),
+        ("an output next to its own input", dict(ptrs=(a, b), outs=(a + 4, c), sizes=sizes, types=f32), False),
+        ("inputs exchanged", dict(ptrs=(a, b), outs=(b, a), sizes=sizes, types=f32), False),
+        ("one in place, one not", dict(ptrs=(a, b), outs=(a, c), sizes=sizes, types=f32), True),
+        ("one input for two outputs", dict(ptrs=(a, a), outs=(b, c), sizes=sizes, types=f32), True),
+        ("one input in place and for another output", dict(ptrs=(a, a), outs=(a, c), sizes=sizes, types=f32), False),
+    ]
+
+
+@pytest.mark.parametrize("case", overlap_cases(), ids=lambda c: c[0])
+def test_tensors_that_share_memory(case):
+    # where one workgroup writes what another reads or writes, the result would
+    # depend on which comes first
+    _, kw, fine = case
+    if fine and torch.cuda.is_available():
+        pytest.skip("these pass the checks and would be launched on addresses that do not exist")
+    want = {ersj.ERR_HIP, ersj.ERR_OOM} if fine else {ersj.ERR_INVALID_ARG}
+    assert clip(**kw) in want
+    if not fine:
+        assert b"share" in ersj.lib().ersj_last_error()
+
+
+def test_many_tensors_side_by_side():
+    n, size = 3000, 33
+    ptrs = [FAKE + 4 * size * (i * 7 % n) for i in range(n)]  # in no order
+    kw = dict(sizes=(size,) * n, types=(0,) * n, count=n, work_bytes=1 << 30)
+    if not torch.cuda.is_available():
+        assert clip(ptrs=ptrs, **kw) == ersj.ERR_HIP
+    ptrs[2000] += 4
+    assert clip(ptrs=ptrs, **kw) == ersj.ERR_INVALID_ARG

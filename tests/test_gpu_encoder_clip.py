@@ -119,3 +119,21 @@ def test_clipping_tensors_on_a_stream():
         norm = ersj.clip_grads(grads, 1.0, stream=side if k % 2 else side.cuda_stream)
         torch.cuda.current_stream().wait_stream(side)
         check_clip(norm, grads, before, 1.0)
+
+
+def test_tensors_that_share_memory_are_refused():
+    flat = torch.ones(1000, device=DEV)
+    a, b, c = flat[:400], flat[400:], flat[399:500]
+    other = torch.zeros(1000, device=DEV)
+    ersj.GradSet([a, b])
+    ersj.GradSet([a, c], [other[:400], other[400:501]])  # read twice, written once
+    for grads, out in (([a, a], None), ([a, c], None), ([c, a], None), ([flat, b], None),
+                       ([a, c], [other[:400], other[399:500]]), ([a, b], [a, flat[:600]]), ([a], [flat[1:401]])):
+        with pytest.raises(ersj.ErsjError, match="share"):
+            ersj.GradSet(grads, out)
+        if out is None:
+            with pytest.raises(ersj.ErsjError, match="share"):
+                ersj.clip_grads(grads, 1.0)
+    ersj.clip_grads([a, b[:0], a[:0], b], 1.0)
+    torch.cuda.synchronize()
+    assert bool((flat == flat[0]).all()) and abs(float(flat.norm()) - 1.0) < 1e-3
