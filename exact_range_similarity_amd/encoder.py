@@ -146,6 +146,17 @@ def _rows(t, what, dim=None):
     return n, ld
 
 
+def _as_rows(t):
+    """``t`` itself where its rows are ones that the kernels take, else a copy."""
+    if t.is_contiguous():
+        return t
+    try:
+        _rows(t, "grad")
+    except ValueError:
+        return t.contiguous()
+    return t
+
+
 def _on(device, t, what):
     if t.device != device:
         raise ValueError(f"{what} is on {t.device}, expected {device}")
@@ -287,7 +298,7 @@ class _Embed(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
         rows, dtype, scale, padding_idx = ctx.args
-        return embed_grad(grad.contiguous(), ctx.saved_tensors[0], rows, scale, padding_idx, dtype), None, None, None, None
+        return embed_grad(_as_rows(grad), ctx.saved_tensors[0], rows, scale, padding_idx, dtype), None, None, None, None
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
@@ -401,7 +412,7 @@ class _LayerNorm(torch.autograd.Function):
         need = ctx.needs_input_grad
         params = need[1] or need[2]
         dtype = ctx.bias_dtype if weight is None else weight.dtype
-        gx, gw, gb = layer_norm_grad(grad.contiguous(), x, mean, rstd, weight, dtype, need[0], params)
+        gx, gw, gb = layer_norm_grad(_as_rows(grad), x, mean, rstd, weight, dtype, need[0], params)
         return gx, gw if need[1] else None, gb if need[2] else None, None
 
 

@@ -42,3 +42,31 @@ def test_the_node_is_made_on_the_given_stream(op, monkeypatch):
     seen.clear()
     assert call() == "result"
     assert seen == [[]]
+
+
+@pytest.mark.parametrize("op", ["embed", "layer_norm"])
+def test_spaced_gradients_are_not_copied(op, monkeypatch):
+    # the kernels take rows that are spaced; only what they cannot take is copied
+    seen = []
+    monkeypatch.setattr(encoder, "embed_grad", lambda grad, *a: seen.append(grad))
+    monkeypatch.setattr(encoder, "layer_norm_grad", lambda grad, *a: seen.append(grad) or (None, None, None))
+
+    class Ctx:
+        args = (9, torch.float32, 1.0, None)
+        saved_tensors = (torch.zeros(6), None, None, None)
+        needs_input_grad = (True, False, False, False)
+        bias_dtype = None
+
+    def backward(grad):
+        node = {"embed": lambda: encoder._Embed.backward(Ctx, grad),
+                "layer_norm": lambda: encoder._LayerNorm.backward(Ctx, grad, None, None)}[op]
+        node()
+        return seen.pop()
+
+    wide = torch.randn(6, 20)
+    for grad in (wide, wide[:, 3:11], wide[1:2, :5], wide.view(2, 3, 20)[:, :, 4:7]):
+        got = backward(grad)
+        assert got.data_ptr() == grad.data_ptr() and got.stride() == grad.stride()
+    for grad in (torch.ones(()).expand(6, 8), wide[:1].expand(6, 20), wide.t(), wide[:, ::2], wide.view(2, 3, 20)[:, :2]):
+        got = backward(grad)
+        assert got.is_contiguous() and torch.equal(got, grad)

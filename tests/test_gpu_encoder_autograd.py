@@ -190,3 +190,18 @@ def test_forward_tangents_are_refused():
         assert torch.equal(ersj.embed(x, ids), x[ids])
         ersj.embed(w, ids).backward(x)
         assert torch.equal(w.grad, ersj.embed_grad(x, ids, 40))
+
+
+def test_backward_of_a_part_of_a_wider_tensor():
+    # the gradients arrive as spaced rows, of y and of the embedding
+    table, gamma, beta, ids, dy = step_inputs(3000, 500, 64, 9)
+    more = torch.randn((3000, 37), generator=gen(10), device=DEV)
+    params = [t.clone().requires_grad_() for t in (table, gamma, beta)]
+    e = ersj.embed(params[0], ids, 2.0)
+    y = ersj.layer_norm(e, *params[1:])[0]
+    torch.cat([more, y], dim=1).backward(torch.cat([more, dy], dim=1))
+    for p, ref in zip(params, direct(table, gamma, beta, ids, dy)):
+        assert torch.equal(p.grad, ref)
+    t = table.clone().requires_grad_()
+    torch.cat([more, ersj.embed(t, ids, 2.0)], dim=1).backward(torch.cat([more, dy], dim=1))
+    assert torch.equal(t.grad, ersj.embed_grad(dy, ids, 500, 2.0))
