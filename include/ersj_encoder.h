@@ -22,7 +22,9 @@
  *  - Rows may be spaced by more than their length (ld* counts elements) and
  *    start at any multiple of the element size.
  *  - The same inputs give the same bits on every call: sums are taken in a
- *    fixed order that depends on the sizes alone.
+ *    fixed order.  It depends on the sizes and element types; for the gradient
+ *    of a table on the ids as well; for the global norm on where each tensor
+ *    lies, modulo 128 bytes.
  */
 #ifndef ERSJ_ENCODER_H
 #define ERSJ_ENCODER_H
@@ -58,7 +60,7 @@ int ersj_embed(const void *d_table, int32_t table_type, int64_t rows, int32_t di
  * Gradient of the table:
  *   out[v, :] = scale * sum over t with ids[t] = v of grad[t, :].
  * Tokens with the padding id, or with an id outside [0, rows), add nothing.
- * Each row's terms are added in 32 bits in an order that the ids alone
+ * Each row's terms are added in 32 bits in an order that the ids and sizes
  * determine: a row's tokens side by side, in the order of t, in stretches
  * whose sums are then added.
  *  d_grad     : device [n][ld_grad] of grad_type.
@@ -147,12 +149,13 @@ int ersj_grads_create(int32_t count, const void *const *d_grad, void *const *d_o
  * norm = sqrt(sum of the squares of every element of every tensor), squares
  * and sums in binary64; factor = min(1, max_norm / (norm + 1e-6)); every
  * element is multiplied by the factor (binary64 rounded to 32 bits) in 32
- * bits and rounded once.  A norm of infinity makes the factor 0; a norm of
- * NaN makes it NaN.
- *  max_norm : >= 0 (+inf: the norm alone is wanted; outputs are copies).
+ * bits and rounded once.  A norm of infinity makes the factor 0, with a
+ * max_norm of infinity 1; a norm of NaN makes it NaN.
+ *  max_norm : >= 0 (+inf: the norm alone is wanted; outputs are copies unless
+ *             the norm is NaN).
  *  d_norm   : device float, the norm before clipping; NULL where not wanted.
  *  d_work   : ERSJ_GRADS_WORK bytes, aligned to 8.
- * Calls on one handle may overlap if their d_work and outputs differ.
+ * Calls on one handle write the same outputs and must not overlap in time.
  * Errors: INVALID_ARG, HIP.
  */
 #define ERSJ_GRADS_WORK 16384

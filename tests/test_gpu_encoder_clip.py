@@ -137,3 +137,33 @@ def test_tensors_that_share_memory_are_refused():
     ersj.clip_grads([a, b[:0], a[:0], b], 1.0)
     torch.cuda.synchronize()
     assert bool((flat == flat[0]).all()) and abs(float(flat.norm()) - 1.0) < 1e-3
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_the_norm_at_other_places_in_memory(kind):
+    # sums follow the tensors' places modulo 128 bytes: the same bits at places
+    # that are equal in that, and anywhere the same norm within its rounding
+    g = gen(4)
+    sizes = [70001, 5, 16384, 40000, 129]
+    values = [torch.randn(s, generator=g, device=DEV).mul_(torch.randn(s, generator=g, device=DEV).mul_(3).exp_())
+              .to(TYPES[kind]) for s in sizes]
+    line = 128 // values[0].element_size()
+
+    def placed(lead):
+        tensors = []
+        for i, v in enumerate(values):
+            buf = torch.empty(lead + i + v.numel(), dtype=v.dtype, device=DEV)
+            assert buf.data_ptr() % 128 == 0
+            buf[lead + i:] = v
+            tensors.append(buf[lead + i:])
+        return tensors
+
+    for lead in (0, 1, 3, line // 2, line - 1):
+        results = []
+        for far in (0, line, 3 * line):
+            tensors = placed(lead + far)
+            results.append((ersj.clip_grads(tensors, 5.0), tensors))
+            check_clip(*results[-1], values, 5.0, f"{lead} elements in")
+        for norm, tensors in results[1:]:
+            assert torch.equal(norm, results[0][0])
+            assert all(torch.equal(a, b) for a, b in zip(tensors, results[0][1]))
