@@ -11,7 +11,8 @@ have any leading shape as long as its rows are contiguous and equally spaced.
 ``stream`` (a torch stream or a raw handle; None: the current one) is where
 the work is enqueued; outputs belong to that stream, and a backward pass through
 them runs on it.  A tensor given as ``out`` must not require a gradient (unless
-gradients are off); what is written counts for autograd as written in place.
+gradients are off) nor overlap an input, unless the function says so; what is
+written counts for autograd as written in place.
 """
 import ctypes
 
@@ -55,9 +56,6 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-
-# the forward-mode level that is open (-1: none), where torch tells it without a look at a tensor
-_dual_level = (lambda: forward_ad._current_level) if hasattr(forward_ad, "_current_level") else (lambda: 0)
 
 
 def _library():
@@ -111,7 +109,8 @@ def _type(t, what):
     if isinstance(t, torch.Tensor):
         code = _TYPES.get(t.dtype)
         if code is not None:
-            if _dual_level() >= 0 and forward_ad.unpack_dual(t).tangent is not None:
+            # the forward-mode level that is open, -1: none (torch tells it without a look at a tensor)
+            if getattr(forward_ad, "_current_level", 0) >= 0 and forward_ad.unpack_dual(t).tangent is not None:
                 raise NotImplementedError(f"{what} has a forward-mode tangent, for which there is no rule")
             return code
     raise TypeError(f"{what} must be a float32, float16 or bfloat16 tensor")

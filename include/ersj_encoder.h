@@ -21,6 +21,8 @@
  *    in 32 bits or more; a result is rounded to its type once, to nearest.
  *  - Rows may be spaced by more than their length (ld* counts elements) and
  *    start at any multiple of the element size.
+ *  - An output may lie on an input only where its entry says so.  Overlaps are
+ *    looked for among the tensors of a set of gradients alone.
  *  - The same inputs give the same bits on every call: sums are taken in a
  *    fixed order.  It depends on the sizes and element types; for the gradient
  *    of a table on the ids as well; for the global norm on where each tensor
