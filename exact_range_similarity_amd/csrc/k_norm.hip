@@ -191,7 +191,9 @@ __global__ __launch_bounds__(block_of(L)) void k_norm(NormArgs a)
     }
 }
 
-// Rows longer than the registers of a workgroup: read again for each step.
+// Rows longer than the registers of a workgroup: read again for each step, an
+// element a load.  4096 x 40,000 f32: 614 us, 246 for one reading and the writing
+// at the rate of a copy; 4096 x 65,536 bf16 860 and 202.
 template <typename T, typename P>
 __global__ __launch_bounds__(1024) void k_norm_long(NormArgs a)
 {
@@ -373,6 +375,9 @@ __global__ __launch_bounds__(block_of(L)) void k_norm_grad(NormGradArgs a, float
     }
 }
 
+// The gradient of such rows: twice over them for grad_x here, once for the sums
+// over rows in k_norm_grad_long_part.  4096 x 40,000 f32: 1515 us, 369 for one
+// reading and the writing at the rate of a copy.
 template <typename T, typename P>
 __global__ __launch_bounds__(1024) void k_norm_grad_long(NormGradArgs a)
 {
