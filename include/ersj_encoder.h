@@ -133,7 +133,8 @@ uint64_t ersj_layer_norm_grad_work(int64_t n, int32_t dim);
  *  d_out  : host array [count] of device pointers for the clipped tensors, or
  *           NULL to clip in place.  A tensor's own entry may equal its
  *           d_grad; otherwise no output may overlap an input or another
- *           output (INVALID_ARG).
+ *           output (INVALID_ARG; ersj_grads_create looks for it once it knows
+ *           its device, all other arguments are checked before).
  *  size   : host array [count], elements of each tensor, >= 0, contiguous.
  *  type   : host array [count], ERSJ_F32, ERSJ_F16 or ERSJ_BF16; input and
  *           output have the same type.
