@@ -129,8 +129,8 @@ def _run_own(st):
 
 
 def _held(x):
-    """The values that rows held in 8 bits stand for: multiples by -127 to 127 of
-    a power of two, the smallest that reaches the largest of a run of 32."""
+    """The values that rows held in 8 bits stand for: -127 to 127 times a power of
+    two, the least that reaches the largest value of a run of 32."""
     rows, dim = x.shape
     v = torch.zeros((rows, -(-dim // BLOCK) * BLOCK), device=DEV)
     v[:, :dim] = x
@@ -138,9 +138,10 @@ def _held(x):
     part, exponent = torch.frexp(v.abs().amax(dim=2, keepdim=True))
     e = torch.where(part > 127 / 128, exponent - 6, exponent - 7).clamp(min=-126)
     step, inverse = ((e + 127) << 23).view(torch.float32), ((127 - e) << 23).view(torch.float32)
-    most = torch.finfo(x.dtype).max
-    out = (torch.round(v * inverse) * step).clamp(-most, most)
-    return out.view(rows, -1)[:, :dim].to(x.dtype)
+    # 63 where 64 of them would be beyond the largest value of the type
+    most = torch.where(e == (10 if x.dtype == torch.float16 else 122), 63.0, 127.0)
+    code = torch.minimum(torch.maximum(torch.round(v * inverse), -most), most)
+    return (code * step).view(rows, -1)[:, :dim].to(x.dtype)
 
 
 def _activation(g, act):
@@ -222,9 +223,11 @@ def _held_exact(x):
         # 2^e with the least e for which 127 of them are no less than the largest
         at, e = torch.frexp(torch.linalg.vector_norm(v, ord=float("inf"), dim=1, keepdim=True) / 127)
         e = torch.where(at == 0.5, e - 1, e).clamp(min=-126)
-        out[:, c:c + BLOCK] = torch.ldexp(torch.round(torch.ldexp(v, -e)), e)
-    most = torch.finfo(x.dtype).max
-    return out.clamp(-most, most)
+        top = torch.finfo(x.dtype).max
+        code = torch.round(torch.ldexp(v, -e))
+        code = torch.where(torch.ldexp(code.abs(), e) > top, 63 * code.sign(), code)
+        out[:, c:c + BLOCK] = torch.ldexp(code, e)
+    return out
 
 
 def _phi(g, act):
