@@ -14,8 +14,10 @@ import os
 
 import torch  # loads the HIP runtime the library must share with torch
 
-from . import encoder
-from .encoder import GradSet, clip_grads, embed, embed_grad, layer_norm, layer_norm_grad
+from . import encoder, feedforward
+from .encoder import (GradSet, PackedRows, clip_grads, embed, embed_grad, layer_norm, layer_norm_grad, layer_norm_pack,
+                      pack_rows, unpack_rows)
+from .feedforward import gated, gated_grad
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # ERSJ_LIBRARY selects another build of the same library (for example the

@@ -20,7 +20,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 SOURCES = ["k_index.hip", "k_refine.hip", "k_refine_mfma.hip", "k_refine_m16.hip", "k_refine_g16.hip", "k_expand.hip", "k_knn.hip", "k_scratch.hip",
-           "k_embed.hip", "k_norm.hip", "k_clip.hip", "ersj_api.cpp", "ersj_encoder.cpp"]
+           "k_embed.hip", "k_norm.hip", "k_clip.hip", "k_pack.hip", "k_gated.hip", "ersj_api.cpp", "ersj_encoder.cpp"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-I", INCLUDE, "-I", CSRC,
           "-Wall", "-Wno-unused-result", "-Wno-unused-command-line-argument"]

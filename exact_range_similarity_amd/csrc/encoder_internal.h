@@ -91,8 +91,14 @@ struct NormArgs {
     void *y;
     int64_t ld_y;
     float *mean, *rstd;
+    int8_t *codes;  // NULL, or where the rows are held in 8 bits as well
+    uint8_t *scales;
 };
 hipError_t launch_layer_norm(const NormArgs &a, hipStream_t s);
+// Whether rows of that length are held by the norm's own kernel, and whether
+// its gradient's kernel reads such rows.
+bool norm_holds(int type, int dim);
+bool norm_grad_of_held(int type, int dim);
 
 struct NormGradArgs {
     const void *gy;
@@ -109,6 +115,8 @@ struct NormGradArgs {
     int64_t ld_gx;
     void *gw, *gb;
     void *work;
+    const int8_t *codes;  // where x is NULL: its rows held in 8 bits
+    const uint8_t *scales;
 };
 uint64_t layer_norm_grad_work(int64_t n, int dim);
 hipError_t launch_layer_norm_grad(const NormGradArgs &a, hipStream_t s);

@@ -1,7 +1,7 @@
 // C ABI of the encoder operators (see include/ersj_encoder.h): argument
 // validation, and the chunks of a set of gradients.
 #include "ersj_encoder.h"
-#include "encoder_internal.h"
+#include "feedforward_internal.h"
 
 #include <hip/hip_runtime.h>
 
@@ -15,6 +15,7 @@
 using namespace ersj;
 
 static_assert(ERSJ_F32 == kF32 && ERSJ_F16 == kF16 && ERSJ_BF16 == kBF16, "element types");
+static_assert(ERSJ_PACK_BLOCK == kPackBlock, "rows held in 8 bits");
 static_assert(kGradParts * sizeof(double) == ERSJ_GRADS_WORK, "working memory of ersj_grads_clip");
 
 struct ersj_grads {
@@ -88,11 +89,69 @@ int check_work(const void *work, uint64_t have, uint64_t need, size_t align)
     return ERSJ_OK;
 }
 
+int check_packed(const int8_t *codes, const uint8_t *scales, int64_t n, int32_t dim)
+{
+    if (n > 0 && (!codes || !scales)) return refuse("codes or scales is NULL");
+    if (!pack_fits(n, dim)) return refuse("%lld rows of %d are too many to hold", (long long)n, dim);
+    return ERSJ_OK;
+}
+
 #define TRY(expr)                       \
     do {                                \
         int r__ = (expr);               \
         if (r__ != ERSJ_OK) return r__; \
     } while (0)
+
+int check_norm(const void *d_x, int32_t type, int64_t n, int32_t dim, int64_t ld_x, const void *d_weight,
+               const void *d_bias, int32_t param_type, float eps, const void *d_y, int64_t ld_y, const float *d_mean,
+               const float *d_rstd)
+{
+    TRY(check_rows(n, dim));
+    TRY(check_tensor(d_x, type, ld_x, dim, n > 0, "x"));
+    TRY(check_tensor(d_y, type, ld_y, dim, n > 0, "y"));
+    TRY(check_tensor(d_weight, param_type, dim, dim, false, "weight"));
+    TRY(check_tensor(d_bias, param_type, dim, dim, false, "bias"));
+    if (param_type != ERSJ_F32 && param_type != type)
+        return refuse("weight and bias must have the type of x or 32 bits");
+    if (!(eps >= 0.f) || std::isinf(eps)) return refuse("eps = %g: must be finite and not negative", (double)eps);
+    if (d_y == d_x && ld_y != ld_x) return refuse("y: in place, its row spacing must be that of x");
+    if (!aligned(d_mean, 4) || !aligned(d_rstd, 4)) return refuse("mean and rstd must be aligned to 4 bytes");
+    return ERSJ_OK;
+}
+
+int check_norm_grad(const void *d_grad_y, int64_t ld_grad_y, int32_t type, int64_t n, int32_t dim,
+                    const float *d_mean, const float *d_rstd, const void *d_weight, int32_t param_type,
+                    const void *d_grad_x, int64_t ld_grad_x, const void *d_grad_weight, const void *d_grad_bias)
+{
+    TRY(check_rows(n, dim));
+    TRY(check_tensor(d_grad_y, type, ld_grad_y, dim, n > 0, "grad_y"));
+    TRY(check_tensor(d_grad_x, type, ld_grad_x, dim, false, "grad_x"));
+    TRY(check_tensor(d_weight, param_type, dim, dim, false, "weight"));
+    TRY(check_tensor(d_grad_weight, param_type, dim, dim, false, "grad_weight"));
+    TRY(check_tensor(d_grad_bias, param_type, dim, dim, false, "grad_bias"));
+    if (param_type != ERSJ_F32 && param_type != type)
+        return refuse("weight and its gradients must have the type of x or 32 bits");
+    if (n > 0 && (!d_mean || !d_rstd)) return refuse("mean or rstd is NULL");
+    if (!aligned(d_mean, 4) || !aligned(d_rstd, 4)) return refuse("mean and rstd must be aligned to 4 bytes");
+    if (d_grad_x == d_grad_y && ld_grad_x != ld_grad_y && d_grad_x)
+        return refuse("grad_x: in place, its row spacing must be that of the tensor it replaces");
+    return ERSJ_OK;
+}
+
+constexpr int64_t kMaxGatedRows = (int64_t)1 << 30;
+
+int check_gated(int32_t type, int64_t n, int32_t dim, const void *d_gate, int64_t ld_gate, const void *d_up,
+                int64_t ld_up, int32_t hidden, int32_t act)
+{
+    TRY(check_rows(n, dim));
+    if (n > kMaxGatedRows) return refuse("n = %lld: must be at most 2^30", (long long)n);
+    if (hidden < 1 || hidden > ERSJ_ENCODER_MAX_DIM)
+        return refuse("hidden = %d: must be in [1, %d]", hidden, ERSJ_ENCODER_MAX_DIM);
+    TRY(check_tensor(d_gate, type, ld_gate, dim, true, "gate"));
+    TRY(check_tensor(d_up, type, ld_up, dim, true, "up"));
+    if (act != ERSJ_SILU && act != ERSJ_GELU && act != ERSJ_GELU_TANH) return refuse("unknown activation %d", act);
+    return ERSJ_OK;
+}
 
 int check_clip(float max_norm, const float *d_norm, const void *d_work, uint64_t have, uint64_t need)
 {
@@ -237,17 +296,9 @@ int ersj_layer_norm(const void *d_x, int32_t type, int64_t n, int32_t dim, int64
                     const void *d_bias, int32_t param_type, float eps, void *d_y, int64_t ld_y, float *d_mean,
                     float *d_rstd, void *stream)
 {
-    TRY(check_rows(n, dim));
-    TRY(check_tensor(d_x, type, ld_x, dim, n > 0, "x"));
-    TRY(check_tensor(d_y, type, ld_y, dim, n > 0, "y"));
-    TRY(check_tensor(d_weight, param_type, dim, dim, false, "weight"));
-    TRY(check_tensor(d_bias, param_type, dim, dim, false, "bias"));
-    if (param_type != ERSJ_F32 && param_type != type)
-        return refuse("weight and bias must have the type of x or 32 bits");
-    if (!(eps >= 0.f) || std::isinf(eps)) return refuse("eps = %g: must be finite and not negative", (double)eps);
-    if (d_y == d_x && ld_y != ld_x) return refuse("y: in place, its row spacing must be that of x");
-    if (!aligned(d_mean, 4) || !aligned(d_rstd, 4)) return refuse("mean and rstd must be aligned to 4 bytes");
-    const NormArgs a{d_x, type, n, dim, ld_x, d_weight, d_bias, param_type, eps, d_y, ld_y, d_mean, d_rstd};
+    TRY(check_norm(d_x, type, n, dim, ld_x, d_weight, d_bias, param_type, eps, d_y, ld_y, d_mean, d_rstd));
+    const NormArgs a{d_x, type, n, dim, ld_x, d_weight, d_bias, param_type, eps, d_y, ld_y, d_mean, d_rstd, nullptr,
+                     nullptr};
     return done(launch_layer_norm(a, (hipStream_t)stream), "layer norm kernel");
 }
 
@@ -262,24 +313,166 @@ int ersj_layer_norm_grad(const void *d_grad_y, int64_t ld_grad_y, const void *d_
                          int32_t param_type, void *d_grad_x, int64_t ld_grad_x, void *d_grad_weight,
                          void *d_grad_bias, void *d_work, uint64_t d_work_bytes, void *stream)
 {
-    TRY(check_rows(n, dim));
-    TRY(check_tensor(d_grad_y, type, ld_grad_y, dim, n > 0, "grad_y"));
+    TRY(check_norm_grad(d_grad_y, ld_grad_y, type, n, dim, d_mean, d_rstd, d_weight, param_type, d_grad_x, ld_grad_x,
+                        d_grad_weight, d_grad_bias));
     TRY(check_tensor(d_x, type, ld_x, dim, n > 0, "x"));
-    TRY(check_tensor(d_grad_x, type, ld_grad_x, dim, false, "grad_x"));
-    TRY(check_tensor(d_weight, param_type, dim, dim, false, "weight"));
-    TRY(check_tensor(d_grad_weight, param_type, dim, dim, false, "grad_weight"));
-    TRY(check_tensor(d_grad_bias, param_type, dim, dim, false, "grad_bias"));
-    if (param_type != ERSJ_F32 && param_type != type)
-        return refuse("weight and its gradients must have the type of x or 32 bits");
-    if (n > 0 && (!d_mean || !d_rstd)) return refuse("mean or rstd is NULL");
-    if (!aligned(d_mean, 4) || !aligned(d_rstd, 4)) return refuse("mean and rstd must be aligned to 4 bytes");
-    if ((d_grad_x == d_grad_y && ld_grad_x != ld_grad_y && d_grad_x) ||
-        (d_grad_x == d_x && ld_grad_x != ld_x && d_grad_x))
+    if (d_grad_x == d_x && ld_grad_x != ld_x && d_grad_x)
         return refuse("grad_x: in place, its row spacing must be that of the tensor it replaces");
     if (d_grad_weight || d_grad_bias) TRY(check_work(d_work, d_work_bytes, layer_norm_grad_work(n, dim), 256));
     const NormGradArgs a{d_grad_y, ld_grad_y, d_x, ld_x, type, n, dim, d_mean, d_rstd, d_weight, param_type,
-                         d_grad_x, ld_grad_x, d_grad_weight, d_grad_bias, d_work};
+                         d_grad_x, ld_grad_x, d_grad_weight, d_grad_bias, d_work, nullptr, nullptr};
     return done(launch_layer_norm_grad(a, (hipStream_t)stream), "layer norm gradient kernels");
+}
+
+int ersj_pack_rows(const void *d_x, int32_t type, int64_t n, int32_t dim, int64_t ld_x, int8_t *d_codes,
+                   uint8_t *d_scales, void *stream)
+{
+    TRY(check_rows(n, dim));
+    TRY(check_tensor(d_x, type, ld_x, dim, n > 0, "x"));
+    TRY(check_packed(d_codes, d_scales, n, dim));
+    const PackArgs a{d_x, type, n, dim, ld_x, d_codes, d_scales};
+    return done(launch_pack(a, (hipStream_t)stream), "pack kernel");
+}
+
+int ersj_unpack_rows(const int8_t *d_codes, const uint8_t *d_scales, int64_t n, int32_t dim, void *d_x, int32_t type,
+                     int64_t ld_x, void *stream)
+{
+    TRY(check_rows(n, dim));
+    TRY(check_packed(d_codes, d_scales, n, dim));
+    TRY(check_tensor(d_x, type, ld_x, dim, n > 0, "x"));
+    const UnpackArgs a{d_codes, d_scales, n, dim, d_x, type, ld_x, dim};
+    return done(launch_unpack(a, (hipStream_t)stream), "unpack kernel");
+}
+
+int ersj_layer_norm_pack(const void *d_x, int32_t type, int64_t n, int32_t dim, int64_t ld_x, const void *d_weight,
+                         const void *d_bias, int32_t param_type, float eps, void *d_y, int64_t ld_y, float *d_mean,
+                         float *d_rstd, int8_t *d_codes, uint8_t *d_scales, void *stream)
+{
+    TRY(check_norm(d_x, type, n, dim, ld_x, d_weight, d_bias, param_type, eps, d_y, ld_y, d_mean, d_rstd));
+    TRY(check_packed(d_codes, d_scales, n, dim));
+    const bool own = norm_holds(type, dim);
+    if (!own) {  // before y, which may replace x
+        const PackArgs p{d_x, type, n, dim, ld_x, d_codes, d_scales};
+        TRY(done(launch_pack(p, (hipStream_t)stream), "pack kernel"));
+    }
+    const NormArgs a{d_x, type, n, dim, ld_x, d_weight, d_bias, param_type, eps, d_y, ld_y, d_mean, d_rstd,
+                     own ? d_codes : nullptr, d_scales};
+    return done(launch_layer_norm(a, (hipStream_t)stream), "layer norm kernel");
+}
+
+// The rows that a gradient kernel without a form for held rows reads follow its
+// own working memory.
+static uint64_t norm_grad_packed_rows(int32_t type, int64_t n, int32_t dim)
+{
+    return norm_grad_of_held(type, dim) ? 0 : (uint64_t)n * dim * elem_size(type);
+}
+
+uint64_t ersj_layer_norm_grad_packed_work(int32_t type, int64_t n, int32_t dim)
+{
+    if (!is_type(type) || n < 0 || n > kMaxRows || dim < 1 || dim > ERSJ_ENCODER_MAX_DIM) return 0;
+    return ((layer_norm_grad_work(n, dim) + 255) & ~(uint64_t)255) + norm_grad_packed_rows(type, n, dim);
+}
+
+int ersj_layer_norm_grad_packed(const void *d_grad_y, int64_t ld_grad_y, const int8_t *d_codes,
+                                const uint8_t *d_scales, int32_t type, int64_t n, int32_t dim, const float *d_mean,
+                                const float *d_rstd, const void *d_weight, int32_t param_type, void *d_grad_x,
+                                int64_t ld_grad_x, void *d_grad_weight, void *d_grad_bias, void *d_work,
+                                uint64_t d_work_bytes, void *stream)
+{
+    TRY(check_norm_grad(d_grad_y, ld_grad_y, type, n, dim, d_mean, d_rstd, d_weight, param_type, d_grad_x, ld_grad_x,
+                        d_grad_weight, d_grad_bias));
+    TRY(check_packed(d_codes, d_scales, n, dim));
+    const uint64_t rows = norm_grad_packed_rows(type, n, dim);
+    const uint64_t sums = (layer_norm_grad_work(n, dim) + 255) & ~(uint64_t)255;
+    if (d_grad_weight || d_grad_bias || rows) TRY(check_work(d_work, d_work_bytes, sums + rows, 256));
+    NormGradArgs a{d_grad_y, ld_grad_y, nullptr, dim, type, n, dim, d_mean, d_rstd, d_weight, param_type, d_grad_x,
+                   ld_grad_x, d_grad_weight, d_grad_bias, d_work, d_codes, d_scales};
+    if (rows) {
+        void *x = (char *)d_work + sums;
+        const UnpackArgs u{d_codes, d_scales, n, dim, x, type, dim, dim};
+        TRY(done(launch_unpack(u, (hipStream_t)stream), "unpack kernel"));
+        a.x = x;
+    }
+    return done(launch_layer_norm_grad(a, (hipStream_t)stream), "layer norm gradient kernels");
+}
+
+uint64_t ersj_gated_work(const void *d_x, int32_t type, int64_t n, int32_t dim, int64_t ld_x, const void *d_gate,
+                         int64_t ld_gate, const void *d_up, int64_t ld_up, int32_t hidden)
+{
+    if (!is_type(type) || n < 0 || n > kMaxGatedRows || dim < 1 || dim > ERSJ_ENCODER_MAX_DIM || hidden < 1 ||
+        hidden > ERSJ_ENCODER_MAX_DIM)
+        return 0;
+    GatedArgs a{};
+    a.x = d_x;
+    a.type = type;
+    a.n = n;
+    a.dim = dim;
+    a.ld_x = ld_x;
+    a.gate = d_gate;
+    a.ld_gate = ld_gate;
+    a.up = d_up;
+    a.ld_up = ld_up;
+    a.hidden = hidden;
+    return gated_work(a);
+}
+
+int ersj_gated(const void *d_x, int32_t type, int64_t n, int32_t dim, int64_t ld_x, const void *d_gate,
+               int64_t ld_gate, const void *d_up, int64_t ld_up, int32_t hidden, int32_t activation, void *d_h,
+               int64_t ld_h, void *d_work, uint64_t d_work_bytes, void *stream)
+{
+    TRY(check_gated(type, n, dim, d_gate, ld_gate, d_up, ld_up, hidden, activation));
+    TRY(check_tensor(d_x, type, ld_x, dim, n > 0, "x"));
+    TRY(check_tensor(d_h, type, ld_h, hidden, n > 0, "h"));
+    const GatedArgs a{d_x, type, n, dim, ld_x, d_gate, ld_gate, d_up, ld_up, hidden, activation, d_h, ld_h, d_work};
+    TRY(check_work(d_work, d_work_bytes, gated_work(a), 256));
+    return done(launch_gated(a, (hipStream_t)stream), "gated block kernels");
+}
+
+uint64_t ersj_gated_grad_work(const void *d_x, int32_t type, int64_t n, int32_t dim, int64_t ld_x, const void *d_gate,
+                              int64_t ld_gate, const void *d_up, int64_t ld_up, int32_t hidden, int32_t want_x,
+                              int32_t want_gate, int32_t want_up)
+{
+    if (!is_type(type) || n < 0 || n > kMaxGatedRows || dim < 1 || dim > ERSJ_ENCODER_MAX_DIM || hidden < 1 ||
+        hidden > ERSJ_ENCODER_MAX_DIM)
+        return 0;
+    GatedGradArgs a{};
+    a.x = d_x;
+    a.type = type;
+    a.n = n;
+    a.dim = dim;
+    a.ld_x = ld_x;
+    a.gate = d_gate;
+    a.ld_gate = ld_gate;
+    a.up = d_up;
+    a.ld_up = ld_up;
+    a.hidden = hidden;
+    // only whether they are wanted counts
+    static char wanted;
+    a.gx = want_x ? &wanted : nullptr;
+    a.ggate = want_gate ? &wanted : nullptr;
+    a.gup = want_up ? &wanted : nullptr;
+    return gated_grad_work(a);
+}
+
+int ersj_gated_grad(const void *d_grad_h, int64_t ld_grad_h, const void *d_x, int64_t ld_x, const int8_t *d_codes,
+                    const uint8_t *d_scales, int32_t type, int64_t n, int32_t dim, const void *d_gate, int64_t ld_gate,
+                    const void *d_up, int64_t ld_up, int32_t hidden, int32_t activation, void *d_grad_x,
+                    int64_t ld_grad_x, void *d_grad_gate, int64_t ld_grad_gate, void *d_grad_up, int64_t ld_grad_up,
+                    void *d_work, uint64_t d_work_bytes, void *stream)
+{
+    TRY(check_gated(type, n, dim, d_gate, ld_gate, d_up, ld_up, hidden, activation));
+    TRY(check_tensor(d_grad_h, type, ld_grad_h, hidden, n > 0, "grad_h"));
+    if (d_x && (d_codes || d_scales)) return refuse("x and rows held in 8 bits are both given");
+    if (d_x || !(d_codes || d_scales)) TRY(check_tensor(d_x, type, ld_x, dim, n > 0, "x"));
+    else TRY(check_packed(d_codes, d_scales, n, dim));
+    TRY(check_tensor(d_grad_x, type, ld_grad_x, dim, false, "grad_x"));
+    TRY(check_tensor(d_grad_gate, type, ld_grad_gate, dim, false, "grad_gate"));
+    TRY(check_tensor(d_grad_up, type, ld_grad_up, dim, false, "grad_up"));
+    const GatedGradArgs a{d_grad_h, ld_grad_h, d_x, d_codes, d_scales, type, n, dim, ld_x, d_gate, ld_gate, d_up,
+                          ld_up, hidden, activation, d_grad_x, ld_grad_x, d_grad_gate, d_grad_up, ld_grad_gate,
+                          ld_grad_up, d_work};
+    TRY(check_work(d_work, d_work_bytes, gated_grad_work(a), 256));
+    return done(launch_gated_grad(a, (hipStream_t)stream), "gated block gradient kernels");
 }
 
 int ersj_grads_create(int32_t count, const void *const *d_grad, void *const *d_out, const int64_t *size,

@@ -10,7 +10,7 @@
 // mean is large.  1M x 384 bf16: 287 us for 1.54 GB, 5.4 TB/s; gradient over
 // 32,768 x 4096 bf16: 158 us for 0.81 GB, 5.1 TB/s, and over 20,000 x 384 f16 12.6
 // + 3.7 us for 46 MB, where starting, the last turns and the sums' join count.
-#include "encoder_internal.h"
+#include "feedforward_internal.h"
 
 namespace ersj {
 
@@ -112,7 +112,59 @@ struct Columns {
     }
 };
 
-template <typename T, typename P, int LEN, int L, int NV>
+// The largest magnitude, as bits, over the lanes of a team that share a block
+// of rows held in 8 bits, in each of them.
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_most(uint32_t v)
+{
+    auto with = [&](uint32_t o) { v = o > v ? o : v; };
+    if constexpr (LANES >= 2) with(__builtin_amdgcn_update_dpp(0, v, 0xb1, 0xf, 0xf, true));
+    if constexpr (LANES >= 4) with(__builtin_amdgcn_update_dpp(0, v, 0x4e, 0xf, 0xf, true));
+    if constexpr (LANES >= 8) with(__builtin_amdgcn_update_dpp(0, v, 0x141, 0xf, 0xf, true));
+    return v;
+}
+
+// Holds a lane's columns of a row in 8 bits.  A block's lanes lie side by side
+// in one vector of the team, since teams of fewer lanes have no second one.
+template <typename T, int LEN, int L, int NV, typename V>
+__device__ __forceinline__ void hold_row(const NormArgs &a, const Columns<LEN, L, NV> &at, const V (&v)[NV], int64_t r)
+{
+    constexpr int kLanes = kPackBlock / LEN < L ? kPackBlock / LEN : L;
+    static_assert(L >= kPackBlock / LEN || NV == 1, "a block within a vector");
+    static_assert(kLanes <= 8, "lanes of a block");
+    const int blocks = pack_blocks(a.dim), lane = threadIdx.x & (L - 1);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int j = 0; j < LEN; ++j) {
+            const uint32_t b = k < NV - 1 || j >= at.skip ? __float_as_uint(v[k][j]) & 0x7fffffffu : 0;
+            most = b > most ? b : most;
+        }
+        most = lanes_most<kLanes>(most);
+        const int scale = pack_scale(most);
+        int8_t code[LEN];
+        pack_codes<T, LEN>(v[k], scale, code);
+        const int c = (k * L + lane) * LEN;
+        if (r >= a.n || c >= a.dim) continue;
+        int8_t *to = a.codes + r * a.dim + at.col[k];
+        if (k < NV - 1 || at.skip == 0) {
+            typename Slot<int8_t, LEN>::vec w;
+#pragma unroll
+            for (int j = 0; j < LEN; ++j) w[j] = code[j];
+            Slot<int8_t, LEN>::store(to, w);
+        } else {
+#pragma unroll
+            for (int j = 0; j < LEN; ++j)
+                if (j >= at.skip) to[j] = code[j];
+        }
+        if (c % kPackBlock == 0) a.scales[r * blocks + c / kPackBlock] = (uint8_t)scale;
+    }
+}
+
+// HOLD: the rows are held in 8 bits as well (1M x 384 bf16: one reading of
+// the rows less than a pass of its own).
+template <typename T, typename P, int LEN, int L, int NV, bool HOLD>
 __global__ __launch_bounds__(block_of(L)) void k_norm(NormArgs a)
 {
     constexpr int kTeams = block_of(L) / L;
@@ -153,6 +205,7 @@ __global__ __launch_bounds__(block_of(L)) void k_norm(NormArgs a)
 #pragma unroll
             for (int k = 0; k < NV; ++k) next[k] = X::load(x + at.col[k]);
         }
+        if constexpr (HOLD) hold_row<T>(a, at, v, r);
         float s[1] = {0.f};
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -231,7 +284,56 @@ __global__ __launch_bounds__(1024) void k_norm_long(NormArgs a)
 // The gradient.  dw and db are sums over rows: each team keeps its own in
 // registers, a workgroup's teams are added in a fixed order at the end, and
 // k_norm_grad_join adds the workgroups' sums, part [workgroup][2][dim].
-template <typename T, typename P, int LEN, int L, int NV>
+// A lane's columns of a row of x, as loaded: the values themselves, or the codes
+// of rows held in 8 bits and their scales.  Only the last vector, which may
+// begin before its place, can lie in two blocks.
+template <typename T, int LEN, int NV, bool HELD>
+struct RowOfX {
+    typename Slot<T, LEN>::vec v[NV];
+    template <typename C>
+    __device__ __forceinline__ void load(const NormGradArgs &a, const C &at, int64_t q)
+    {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) v[k] = Slot<T, LEN>::load((const T *)a.x + q * a.ld_x + at.col[k]);
+    }
+    template <typename V, typename C>
+    __device__ __forceinline__ V get(const C &, int k) const
+    {
+        return __builtin_convertvector(v[k], V);
+    }
+};
+
+template <typename T, int LEN, int NV>
+struct RowOfX<T, LEN, NV, true> {
+    typename Slot<int8_t, LEN>::vec code[NV];
+    uint8_t scale[NV], end;
+    template <typename C>
+    __device__ __forceinline__ void load(const NormGradArgs &a, const C &at, int64_t q)
+    {
+        const int8_t *codes = a.codes + q * a.dim;
+        const uint8_t *scales = a.scales + q * pack_blocks(a.dim);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            code[k] = Slot<int8_t, LEN>::load(codes + at.col[k]);
+            scale[k] = scales[at.col[k] / kPackBlock];
+        }
+        end = scales[(at.col[NV - 1] + LEN - 1) / kPackBlock];
+    }
+    template <typename V, typename C>
+    __device__ __forceinline__ V get(const C &at, int k) const
+    {
+        V v = __builtin_convertvector(code[k], V);
+        const float step = pack_step(scale[k]);
+        if (k < NV - 1) return v * step;
+        const float last = pack_step(end);
+        const int own = kPackBlock - at.col[k] % kPackBlock;
+#pragma unroll
+        for (int j = 0; j < LEN; ++j) v[j] *= j < own ? step : last;
+        return v;
+    }
+};
+
+template <typename T, typename P, int LEN, int L, int NV, bool HELD>
 __global__ __launch_bounds__(block_of(L)) void k_norm_grad(NormGradArgs a, float *part)
 {
     constexpr int kBlock = block_of(L);
@@ -255,16 +357,15 @@ __global__ __launch_bounds__(block_of(L)) void k_norm_grad(NormGradArgs a, float
     const float inv = 1.f / (float)a.dim;
     const int64_t step = (int64_t)gridDim.x * kTeams;
     int64_t r = (int64_t)blockIdx.x * kTeams + threadIdx.x / L;
-    typename X::vec nx[NV], ng[NV];
+    RowOfX<T, LEN, NV, HELD> nx;
+    typename X::vec ng[NV];
     float nmean = 0.f, nrstd = 0.f;
     const int64_t turns = (a.n + step - 1) / step;
     if (turns) {
         const int64_t q = r < a.n ? r : a.n - 1;
+        nx.load(a, at, q);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            nx[k] = X::load((const T *)a.x + q * a.ld_x + at.col[k]);
-            ng[k] = X::load((const T *)a.gy + q * a.ld_gy + at.col[k]);
-        }
+        for (int k = 0; k < NV; ++k) ng[k] = X::load((const T *)a.gy + q * a.ld_gy + at.col[k]);
         nmean = a.mean[q];
         nrstd = a.rstd[q];
     }
@@ -274,7 +375,7 @@ __global__ __launch_bounds__(block_of(L)) void k_norm_grad(NormGradArgs a, float
         const bool mine = r < a.n;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            xh[k] = (__builtin_convertvector(nx[k], fvec) - nmean) * rstd;
+            xh[k] = (nx.template get<fvec>(at, k) - nmean) * rstd;
             g[k] = __builtin_convertvector(ng[k], fvec);
             if (mine) {
                 dw[k] += g[k] * xh[k];
@@ -283,11 +384,9 @@ __global__ __launch_bounds__(block_of(L)) void k_norm_grad(NormGradArgs a, float
         }
         if (turn + 1 < turns) {
             const int64_t q = r + step < a.n ? r + step : a.n - 1;
+            nx.load(a, at, q);
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                nx[k] = X::load((const T *)a.x + q * a.ld_x + at.col[k]);
-                ng[k] = X::load((const T *)a.gy + q * a.ld_gy + at.col[k]);
-            }
+            for (int k = 0; k < NV; ++k) ng[k] = X::load((const T *)a.gy + q * a.ld_gy + at.col[k]);
             nmean = a.mean[q];
             nrstd = a.rstd[q];
         }
@@ -552,22 +651,28 @@ hipError_t by_shape(const Shape &s, A... args)
     return hipErrorInvalidConfiguration;  // a shape without a kernel
 }
 
-template <typename T, typename P, int LEN, int L, int NV>
-struct RunNorm {
-    static constexpr bool kLong = true;  // 1024 lanes as well
-    static void run(const NormArgs *a, unsigned blocks, hipStream_t s)
-    {
-        k_norm<T, P, LEN, L, NV><<<dim3(blocks), dim3(block_of(L)), 0, s>>>(*a);
-    }
+template <bool HOLD>
+struct Norm {
+    template <typename T, typename P, int LEN, int L, int NV>
+    struct Run {
+        static constexpr bool kLong = true;  // 1024 lanes as well
+        static void run(const NormArgs *a, unsigned blocks, hipStream_t s)
+        {
+            k_norm<T, P, LEN, L, NV, HOLD><<<dim3(blocks), dim3(block_of(L)), 0, s>>>(*a);
+        }
+    };
 };
 
-template <typename T, typename P, int LEN, int L, int NV>
-struct RunGrad {
-    static constexpr bool kLong = false;
-    static void run(const NormGradArgs *a, float *part, unsigned blocks, hipStream_t s)
-    {
-        k_norm_grad<T, P, LEN, L, NV><<<dim3(blocks), dim3(block_of(L)), 0, s>>>(*a, part);
-    }
+template <bool HELD>
+struct Grad {
+    template <typename T, typename P, int LEN, int L, int NV>
+    struct Run {
+        static constexpr bool kLong = false;
+        static void run(const NormGradArgs *a, float *part, unsigned blocks, hipStream_t s)
+        {
+            k_norm_grad<T, P, LEN, L, NV, HELD><<<dim3(blocks), dim3(block_of(L)), 0, s>>>(*a, part);
+        }
+    };
 };
 
 // Calls ... with T and P for the admissible pairs: P is T or float.
@@ -588,10 +693,15 @@ hipError_t launch_layer_norm(const NormArgs &a, hipStream_t s)
     const Shape sh = shape_of(a.type, a.dim, 1024);
     const unsigned blocks = norm_blocks(a.n, sh);
     ERSJ_NORM_SWITCH(a.type, a.param_type, T, P,
-        if (sh.lanes) return by_shape<T, P, RunNorm>(sh, &a, blocks, s);
+        if (sh.lanes && a.codes) return by_shape<T, P, Norm<true>::template Run>(sh, &a, blocks, s);
+        if (sh.lanes) return by_shape<T, P, Norm<false>::template Run>(sh, &a, blocks, s);
         k_norm_long<T, P><<<dim3(blocks), dim3(1024), 0, s>>>(a));
     return hipGetLastError();
 }
+
+bool norm_holds(int type, int dim) { return shape_of(type, dim, 1024).lanes != 0; }
+
+bool norm_grad_of_held(int type, int dim) { return shape_of(type, dim, 512).lanes != 0; }
 
 uint64_t layer_norm_grad_work(int64_t n, int dim)
 {
@@ -615,7 +725,8 @@ hipError_t launch_layer_norm_grad(const NormGradArgs &a, hipStream_t s)
     float *part = params && (blocks > 1 || !sh.lanes) ? (float *)a.work : nullptr;
     ERSJ_NORM_SWITCH(a.type, a.param_type, T, P,
         if (sh.lanes) {
-            const hipError_t e = by_shape<T, P, RunGrad>(sh, &a, part, blocks, s);
+            const hipError_t e = a.x || !a.n ? by_shape<T, P, Grad<false>::template Run>(sh, &a, part, blocks, s)
+                                             : by_shape<T, P, Grad<true>::template Run>(sh, &a, part, blocks, s);
             if (e != hipSuccess) return e;
         } else {
             // the sums before the gradient of x, which may replace an input

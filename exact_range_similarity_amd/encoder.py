@@ -1,5 +1,6 @@
 """Operators of the encoder whose vectors the join compares: token embedding,
-layer norm, their gradients, and clipping by the global gradient norm.
+layer norm, their gradients, rows held in 8 bits for a backward pass, and
+clipping by the global gradient norm (``feedforward`` has the gated block).
 
 Binding of ``include/ersj_encoder.h``.  The functions carry the C names
 without the ``ersj_`` prefix, check and marshal their arguments, and take
@@ -25,7 +26,11 @@ GRADS_WORK = 16384                                                # ERSJ_GRADS_W
 
 ENCODER_SYMBOLS = ("ersj_embed", "ersj_embed_grad", "ersj_embed_grad_work", "ersj_layer_norm",
                    "ersj_layer_norm_grad", "ersj_layer_norm_grad_work", "ersj_grads_create", "ersj_grads_clip",
-                   "ersj_grads_free", "ersj_clip_tensors", "ersj_clip_tensors_work")
+                   "ersj_grads_free", "ersj_clip_tensors", "ersj_clip_tensors_work", "ersj_pack_rows",
+                   "ersj_unpack_rows", "ersj_layer_norm_pack", "ersj_layer_norm_grad_packed",
+                   "ersj_layer_norm_grad_packed_work", "ersj_gated", "ersj_gated_work", "ersj_gated_grad",
+                   "ersj_gated_grad_work")
+PACK_BLOCK = 32                                                   # ERSJ_PACK_BLOCK
 
 
 def declare(L):
@@ -45,6 +50,21 @@ def declare(L):
     L.ersj_clip_tensors.argtypes = [i32, vp, vp, vp, vp, f32, vp, vp, u64, vp]
     L.ersj_clip_tensors_work.argtypes = [i32, vp, vp]
     L.ersj_clip_tensors_work.restype = u64
+    L.ersj_pack_rows.argtypes = [vp, i32, i64, i32, i64, vp, vp, vp]
+    L.ersj_unpack_rows.argtypes = [vp, vp, i64, i32, vp, i32, i64, vp]
+    L.ersj_layer_norm_pack.argtypes = [vp, i32, i64, i32, i64, vp, vp, i32, f32, vp, i64, vp, vp, vp, vp, vp]
+    L.ersj_layer_norm_grad_packed.argtypes = [vp, i64, vp, vp, i32, i64, i32, vp, vp, vp, i32, vp, i64, vp, vp, vp,
+                                              u64, vp]
+    L.ersj_layer_norm_grad_packed_work.argtypes = [i32, i64, i32]
+    L.ersj_layer_norm_grad_packed_work.restype = u64
+    weights = [vp, i64, vp, i64, i32]
+    L.ersj_gated.argtypes = [vp, i32, i64, i32, i64, *weights, i32, vp, i64, vp, u64, vp]
+    L.ersj_gated_work.argtypes = [vp, i32, i64, i32, i64, *weights]
+    L.ersj_gated_work.restype = u64
+    L.ersj_gated_grad.argtypes = [vp, i64, vp, i64, vp, vp, i32, i64, i32, *weights, i32, vp, i64, vp, i64, vp, i64,
+                                  vp, u64, vp]
+    L.ersj_gated_grad_work.argtypes = [vp, i32, i64, i32, i64, *weights, i32, i32, i32]
+    L.ersj_gated_grad_work.restype = u64
     L.ersj_grads_free.argtypes = [vp]
     L.ersj_grads_free.restype = None
     _lib = L
@@ -300,25 +320,106 @@ class _Embed(torch.autograd.Function):
         return embed_grad(_as_rows(grad), ctx.saved_tensors[0], rows, scale, padding_idx, dtype), None, None, None, None
 
 
-def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
+class PackedRows:
+    """Rows held in 8 bits (``ersj_pack_rows``): ``codes``, int8 of the rows'
+    ``shape``, ``scales``, uint8 with one for each run of 32 along a row, and
+    ``dtype``, the rows' type."""
+
+    __slots__ = ("codes", "scales", "dtype")
+
+    def __init__(self, codes, scales, dtype):
+        if dtype not in _TYPES:
+            raise TypeError("dtype must be float32, float16 or bfloat16")
+        for what, t, kind in (("codes", codes, torch.int8), ("scales", scales, torch.uint8)):
+            if not isinstance(t, torch.Tensor) or t.dtype != kind or not t.is_contiguous():
+                raise ValueError(f"{what} must be a contiguous {kind} tensor")
+        if not codes.dim() or not codes.shape[-1]:
+            raise ValueError("codes must have rows")
+        shape = codes.shape[:-1] + (-(-codes.shape[-1] // PACK_BLOCK),)
+        if scales.shape != shape:
+            raise ValueError(f"scales must have the shape {list(shape)}")
+        _on(codes.device, scales, "scales")
+        self.codes, self.scales, self.dtype = codes, scales, dtype
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+def _empty_packed(shape, dtype, device):
+    codes = torch.empty(shape, dtype=torch.int8, device=device)
+    scales = torch.empty(shape[:-1] + (-(-shape[-1] // PACK_BLOCK),), dtype=torch.uint8, device=device)
+    return PackedRows(codes, scales, dtype)
+
+
+def pack_rows(x, stream=None):
+    """``ersj_pack_rows``: the rows of ``x`` in 8 bits, as ``PackedRows``: whole
+    multiples of a power of two for each run of 32 along a row, off by at most
+    1/128 of the largest of the run.  Not differentiable; ``layer_norm`` and
+    ``gated`` keep their input so with ``pack=True``."""
+    xt = _type(x, "x")
+    device = x.device
+    if _elsewhere(device, stream):
+        return _run_elsewhere(device, stream, (x,), lambda: pack_rows(x))
+    n, ldx = _rows(x, "x")
+    kept = _empty_packed(x.shape, x.dtype, device)
+    _check(_library().ersj_pack_rows(x.data_ptr(), xt, n, x.shape[-1], ldx, kept.codes.data_ptr(),
+                                     kept.scales.data_ptr(), _raw_stream(device.index)))
+    return kept
+
+
+def unpack_rows(packed, out=None, stream=None):
+    """``ersj_unpack_rows``: the values that the rows stand for, in their type."""
+    if not isinstance(packed, PackedRows):
+        raise TypeError("packed must be PackedRows")
+    device = packed.device
+    if _elsewhere(device, stream):
+        return _run_elsewhere(device, stream, (packed.codes, packed.scales, out), lambda: unpack_rows(packed, out))
+    shape = packed.shape
+    dim = shape[-1]
+    given = out is not None
+    if given:
+        ldo = _given(out, "out", shape, packed.dtype, device)
+    else:
+        out, ldo = torch.empty(shape, dtype=packed.dtype, device=device), dim
+    _check(_library().ersj_unpack_rows(packed.codes.data_ptr(), packed.scales.data_ptr(), packed.codes.numel() // dim,
+                                       dim, out.data_ptr(), _TYPES[packed.dtype], ldo, _raw_stream(device.index)))
+    if given:
+        _written(out)
+    return out
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, stream=None, pack=False):
     """``ersj_layer_norm`` over the last dimension: (y, mean, rstd), mean and
     rstd float32 of shape ``x.shape[:-1]``.  ``weight`` and ``bias``: [dim], of
     x's type or float32 (both of one type), or None.  ``out`` may be ``x``.
-    Differentiable with respect to x, weight and bias (``layer_norm_grad``)."""
+    Differentiable with respect to x, weight and bias (``layer_norm_grad``); with
+    ``pack`` the backward pass keeps x in 8 bits (``PackedRows``)."""
     if ((x.requires_grad or (weight is not None and weight.requires_grad) or (bias is not None and bias.requires_grad))
             and torch.is_grad_enabled()):
         if out is not None:
             raise ValueError("out cannot be given where a gradient is wanted")
-        return _apply(x.device, stream, (x, weight, bias), lambda: _LayerNorm.apply(x, weight, bias, eps))
+        node = _LayerNormPacked if pack else _LayerNorm
+        return _apply(x.device, stream, (x, weight, bias), lambda: node.apply(x, weight, bias, eps))
     return _layer_norm(x, weight, bias, eps, out, stream)
 
 
-def _layer_norm(x, weight, bias, eps, out, stream):
+def layer_norm_pack(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
+    """``ersj_layer_norm_pack``: ``layer_norm`` and ``pack_rows`` of x in one pass,
+    (y, mean, rstd, PackedRows), for ``layer_norm_grad``.  Not differentiable."""
+    return _layer_norm(x, weight, bias, eps, out, stream, True)
+
+
+def _layer_norm(x, weight, bias, eps, out, stream, pack=False):
     xt = _type(x, "x")
     device = x.device
     if _elsewhere(device, stream):
         return _run_elsewhere(device, stream, (x, weight, bias, out),
-                              lambda: _layer_norm(x, weight, bias, eps, out, None))
+                              lambda: _layer_norm(x, weight, bias, eps, out, None, pack))
     n, ldx = _rows(x, "x")
     shape = x.shape
     dim = shape[-1]
@@ -338,6 +439,14 @@ def _layer_norm(x, weight, bias, eps, out, stream):
         out, ldy = _empty_rows(x), dim
     mean = torch.empty(shape[:-1], dtype=torch.float32, device=device)
     rstd = torch.empty_like(mean)
+    if pack:
+        kept = _empty_packed(shape, x.dtype, device)
+        _check(_library().ersj_layer_norm_pack(x.data_ptr(), xt, n, dim, ldx, w, b, pt, eps, out.data_ptr(), ldy,
+                                               mean.data_ptr(), rstd.data_ptr(), kept.codes.data_ptr(),
+                                               kept.scales.data_ptr(), _raw_stream(device.index)))
+        if given:
+            _written(out)
+        return out, mean, rstd, kept
     _check(_library().ersj_layer_norm(x.data_ptr(), xt, n, dim, ldx, w, b, pt, eps, out.data_ptr(), ldy,
                                       mean.data_ptr(), rstd.data_ptr(), _raw_stream(device.index)))
     if given:
@@ -347,21 +456,24 @@ def _layer_norm(x, weight, bias, eps, out, stream):
 
 def layer_norm_grad(grad, x, mean, rstd, weight=None, dtype=None, want_x=True, want_params=True, stream=None):
     """``ersj_layer_norm_grad``: (grad of x, of weight, of bias) from ``grad``,
-    the gradient of y, and what ``layer_norm`` returned.  The last two have
+    the gradient of y, and what ``layer_norm`` returned.  ``x``: the rows, or
+    ``PackedRows`` of them (``ersj_layer_norm_grad_packed``).  The last two have
     ``dtype``: the weight's type (the default; float32 without one), x's, or float32.
     What is not wanted comes back as None."""
-    xt = _type(x, "x")
+    packed = x if type(x) is PackedRows else None
+    xt = _type(x, "x") if packed is None else _TYPES[x.dtype]
     if _type(grad, "grad") != xt:
         raise TypeError("grad must have the type of x")
     device = x.device
     if _elsewhere(device, stream):
-        return _run_elsewhere(device, stream, (grad, x, mean, rstd, weight),
+        kept = (x,) if packed is None else (x.codes, x.scales)
+        return _run_elsewhere(device, stream, (grad, *kept, mean, rstd, weight),
                               lambda: layer_norm_grad(grad, x, mean, rstd, weight, dtype, want_x, want_params))
     shape = x.shape
     if grad.shape != shape:
         raise ValueError(f"grad has the shape {list(grad.shape)}, x {list(shape)}")
     _on(device, grad, "grad")
-    n, ldx = _rows(x, "x")
+    n, ldx = _rows(x if packed is None else x.codes, "x")
     dim = shape[-1]
     for what, t in (("mean", mean), ("rstd", rstd)):
         if t.dtype != torch.float32 or t.shape != shape[:-1] or not t.is_contiguous():
@@ -379,15 +491,27 @@ def layer_norm_grad(grad, x, mean, rstd, weight=None, dtype=None, want_x=True, w
         elif dtype != weight.dtype:
             raise TypeError("the gradients of weight and bias have the weight's type")
     L = _library()
-    gx = _empty_rows(x) if want_x else None
+    gx = None
+    if want_x:
+        gx = _empty_rows(x) if packed is None else torch.empty(shape, dtype=x.dtype, device=device)
     gw = gb = work = None
     need = 0
     if want_params:
         gw = torch.empty(dim, dtype=dtype, device=device)
         gb = torch.empty_like(gw)
         need = L.ersj_layer_norm_grad_work(n, dim)
-        if need:
-            work = torch.empty(need, dtype=torch.uint8, device=device)
+    if packed is not None:
+        need = L.ersj_layer_norm_grad_packed_work(xt, n, dim)
+    if need:
+        work = torch.empty(need, dtype=torch.uint8, device=device)
+    if packed is not None:
+        _check(L.ersj_layer_norm_grad_packed(grad.data_ptr(), _rows(grad, "grad")[1], x.codes.data_ptr(),
+                                             x.scales.data_ptr(), xt, n, dim, mean.data_ptr(), rstd.data_ptr(), w, pt,
+                                             gx.data_ptr() if want_x else None, dim,
+                                             gw.data_ptr() if want_params else None,
+                                             gb.data_ptr() if want_params else None, work.data_ptr() if need else None,
+                                             need, _raw_stream(device.index)))
+        return gx, gw, gb
     _check(L.ersj_layer_norm_grad(grad.data_ptr(), _rows(grad, "grad")[1], x.data_ptr(), ldx, xt, n, dim,
                                   mean.data_ptr(), rstd.data_ptr(), w, pt, gx.data_ptr() if want_x else None, dim,
                                   gw.data_ptr() if want_params else None, gb.data_ptr() if want_params else None,
@@ -412,6 +536,27 @@ class _LayerNorm(torch.autograd.Function):
         params = need[1] or need[2]
         dtype = ctx.bias_dtype if weight is None else weight.dtype
         gx, gw, gb = layer_norm_grad(_as_rows(grad), x, mean, rstd, weight, dtype, need[0], params)
+        return gx, gw if need[1] else None, gb if need[2] else None, None
+
+
+class _LayerNormPacked(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps):
+        y, mean, rstd, kept = _layer_norm(x, weight, bias, eps, None, None, True)
+        ctx.save_for_backward(kept.codes, kept.scales, weight, mean, rstd)
+        ctx.dtypes = kept.dtype, None if bias is None else bias.dtype
+        ctx.mark_non_differentiable(mean, rstd)
+        return y, mean, rstd
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad, _mean, _rstd):
+        codes, scales, weight, mean, rstd = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        params = need[1] or need[2]
+        dtype = ctx.dtypes[1] if weight is None else weight.dtype
+        gx, gw, gb = layer_norm_grad(_as_rows(grad), PackedRows(codes, scales, ctx.dtypes[0]), mean, rstd, weight,
+                                     dtype, need[0], params)
         return gx, gw if need[1] else None, gb if need[2] else None, None
 
 

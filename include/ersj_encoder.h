@@ -6,7 +6,9 @@
  * normalises them and pools them into the vector that ersj_build_index then
  * indexes.  These entry points are that encoder's forward and backward
  * passes: token embedding with scaling and its gradient, layer norm and its
- * gradient, and the clipping of all gradients by their global norm.
+ * gradient, the gated feed-forward block and its gradient, rows held in 8 bits
+ * between the two passes, and the clipping of all gradients by their global
+ * norm.
  *
  * Conventions are those of ersj.h (device pointers, streams, error codes,
  * ersj_last_error, arguments validated before any HIP call), and further:
@@ -123,6 +125,92 @@ int ersj_layer_norm_grad(const void *d_grad_y, int64_t ld_grad_y, const void *d_
 /* Bytes of working memory for those sizes (0 also for sizes that are refused,
  * and for few rows, where none is needed and d_work may be NULL). */
 uint64_t ersj_layer_norm_grad_work(int64_t n, int32_t dim);
+
+/*
+ * Rows held in 8 bits, for what a backward pass reads of a forward pass: along
+ * a row, ERSJ_PACK_BLOCK neighbours share a power of two 2^e, with the least
+ * e >= -126 for which none of them is above 127 * 2^e in magnitude, and x is
+ * held as the whole number nearest to x / 2^e (ties to even).  It stands for
+ * code * 2^e, exactly, in the type of the rows.  (With the largest e of a
+ * type, 10 or 122, a code of 64 would be beyond its range: 63 is the most
+ * there.)  A block with a NaN or an infinity stands for NaN throughout.
+ *  d_x      : device [n][ld_x] of type.
+ *  d_codes  : device [n][dim], without gaps.
+ *  d_scales : device [n][(dim + ERSJ_PACK_BLOCK - 1) / ERSJ_PACK_BLOCK],
+ *             e + 127, and 255 for a block that stands for NaN.
+ * Codes and scales are to be unpacked with the type that they were packed
+ * with.  Errors: INVALID_ARG, HIP.
+ */
+#define ERSJ_PACK_BLOCK 32
+int ersj_pack_rows(const void *d_x, int32_t type, int64_t n, int32_t dim, int64_t ld_x, int8_t *d_codes,
+                   uint8_t *d_scales, void *stream);
+int ersj_unpack_rows(const int8_t *d_codes, const uint8_t *d_scales, int64_t n, int32_t dim, void *d_x, int32_t type,
+                     int64_t ld_x, void *stream);
+
+/*
+ * ersj_layer_norm that also holds x in 8 bits, in the same pass over it, and
+ * the gradient of layer norm with rows held so in the place of x.  Mean and
+ * rstd are those of x itself.  Arguments as above; d_grad_x may be d_grad_y
+ * (with the same spacing).
+ *  d_work : at least ersj_layer_norm_grad_packed_work(type, n, dim) bytes,
+ *           aligned to 256 (0: none is needed).
+ * Errors: INVALID_ARG, HIP.
+ */
+int ersj_layer_norm_pack(const void *d_x, int32_t type, int64_t n, int32_t dim, int64_t ld_x, const void *d_weight,
+                         const void *d_bias, int32_t param_type, float eps, void *d_y, int64_t ld_y, float *d_mean,
+                         float *d_rstd, int8_t *d_codes, uint8_t *d_scales, void *stream);
+int ersj_layer_norm_grad_packed(const void *d_grad_y, int64_t ld_grad_y, const int8_t *d_codes,
+                                const uint8_t *d_scales, int32_t type, int64_t n, int32_t dim, const float *d_mean,
+                                const float *d_rstd, const void *d_weight, int32_t param_type, void *d_grad_x,
+                                int64_t ld_grad_x, void *d_grad_weight, void *d_grad_bias, void *d_work,
+                                uint64_t d_work_bytes, void *stream);
+uint64_t ersj_layer_norm_grad_packed_work(int32_t type, int64_t n, int32_t dim);
+
+/*
+ * Gated feed-forward block: g = x gate^T, u = x up^T, h = act(g) * u.
+ *  d_x            : device [n][ld_x] of type; 0 <= n <= 2^30, rows of dim.
+ *  d_gate, d_up   : device [hidden][ld_*] of type, 1 <= hidden <=
+ *                   ERSJ_ENCODER_MAX_DIM.
+ *  activation     : ERSJ_SILU: g / (1 + exp(-g)); ERSJ_GELU: g Phi(g), Phi the
+ *                   normal distribution; ERSJ_GELU_TANH: g / 2 * (1 +
+ *                   tanh(sqrt(2 / pi) * (g + 0.044715 g^3))).
+ *  d_h            : device [n][ld_h] of type.
+ *  d_work         : at least ersj_gated_work(...) bytes, aligned to 256; it
+ *                   takes the arguments of the call, looks at the addresses'
+ *                   alignment alone, and gives 0 where none is needed.
+ * g and u stay in 32 bits.  16-bit types are multiplied as they are; 32-bit
+ * values as three bf16 parts each, with an error of at most 2^-25 of every
+ * product, and an infinity among them counts as NaN.  Errors: INVALID_ARG, HIP.
+ */
+enum { ERSJ_SILU = 0, ERSJ_GELU = 1, ERSJ_GELU_TANH = 2 };
+int ersj_gated(const void *d_x, int32_t type, int64_t n, int32_t dim, int64_t ld_x, const void *d_gate,
+               int64_t ld_gate, const void *d_up, int64_t ld_up, int32_t hidden, int32_t activation, void *d_h,
+               int64_t ld_h, void *d_work, uint64_t d_work_bytes, void *stream);
+uint64_t ersj_gated_work(const void *d_x, int32_t type, int64_t n, int32_t dim, int64_t ld_x, const void *d_gate,
+                         int64_t ld_gate, const void *d_up, int64_t ld_up, int32_t hidden);
+
+/*
+ * Its gradient; g and u are formed again from x:
+ *   du = grad_h * act(g),  dg = grad_h * u * act'(g),
+ *   grad_x = dg gate + du up,  grad_gate = dg^T x,  grad_up = du^T x.
+ *  d_grad_h          : device [n][ld_grad_h] of type.
+ *  d_x               : as above, or NULL, and in its place
+ *  d_codes, d_scales : its rows held in 8 bits.
+ *  d_grad_x          : device [n][ld_grad_x] of type; NULL: not wanted.
+ *  d_grad_gate, d_grad_up : device [hidden][ld_*] of type; NULL: not wanted.
+ *  d_work            : at least ersj_gated_grad_work(...) bytes, aligned to
+ *                      256; want_*: whether that gradient is wanted.
+ * dg and du are rounded to the 16-bit type that they are multiplied in (32-bit
+ * tensors: held in three parts).  Errors: INVALID_ARG, HIP.
+ */
+int ersj_gated_grad(const void *d_grad_h, int64_t ld_grad_h, const void *d_x, int64_t ld_x, const int8_t *d_codes,
+                    const uint8_t *d_scales, int32_t type, int64_t n, int32_t dim, const void *d_gate, int64_t ld_gate,
+                    const void *d_up, int64_t ld_up, int32_t hidden, int32_t activation, void *d_grad_x,
+                    int64_t ld_grad_x, void *d_grad_gate, int64_t ld_grad_gate, void *d_grad_up, int64_t ld_grad_up,
+                    void *d_work, uint64_t d_work_bytes, void *stream);
+uint64_t ersj_gated_grad_work(const void *d_x, int32_t type, int64_t n, int32_t dim, int64_t ld_x, const void *d_gate,
+                              int64_t ld_gate, const void *d_up, int64_t ld_up, int32_t hidden, int32_t want_x,
+                              int32_t want_gate, int32_t want_up);
 
 /*
  * A set of gradient tensors, for clipping by their global norm.  The handle
