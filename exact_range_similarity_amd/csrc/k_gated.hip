@@ -45,8 +45,7 @@ struct ProductArgs {
     // P: along the results' rows (n), Q: across them (m); planes of 16-bit values
     const uint16_t *p[2], *q[2];
     int64_t p_plane, q_plane, ld_p, ld_q;
-    int k;                // of one product, a multiple of 16
-    int p_valid, q_valid; // rows that exist of an operand that lies across k
+    int k;                // of one product, a multiple of 8 where an operand lies along it
     int products;         // of planes
     uint32_t p_planes, q_planes;
     int sources;          // pairs (p[i], q[i]) summed
@@ -62,7 +61,7 @@ struct ProductArgs {
     int64_t ld_gh;
     uint16_t *dg, *du;
     int64_t d_plane, ld_d;
-    int m_pad, n_pad;     // rows and columns of dg and du that are written, with zeros outside the block
+    int n_pad;            // columns of dg and du that are written, zeros behind n
     int act;
 };
 
@@ -74,6 +73,14 @@ __device__ __forceinline__ void dma16(uint32_t lds, uint32_t off, const void *ba
                  :
                  : "s"(lds), "v"(off), "s"(base)
                  : "memory");
+}
+
+// What is loaded in the place of values behind the end of k.
+__device__ const uint32_t kZeros[4] = {0, 0, 0, 0};
+
+__device__ __forceinline__ void dma16_from(uint32_t lds, const void *from)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(lds), "v"(from) : "memory");
 }
 
 template <int N>
@@ -130,7 +137,7 @@ struct Side {
     static constexpr int kPieces = ACROSS ? ROWS / 8 : kSlab / 8;  // of a row of LDS
     static constexpr int kLoadRows = 64 / kPieces;                 // rows of LDS that a wave's load fills
     uint32_t off[kLoads];
-    int piece;  // along k: the lane's piece; across k: its row in the load
+    int piece;  // along k: the lane's piece
 
     // `room`: rows (along k) or columns (across k) from the tile's first that may be read
     __device__ __forceinline__ void init(int wave, int64_t ld, int room)
@@ -143,7 +150,6 @@ struct Side {
                 int c = (lane % kPieces) ^ ((row & 3) << 2);
                 c = c * 8 < room ? c : 0;
                 off[j] = (uint32_t)(row * (int)ld + c * 8) * 2;
-                piece = c;
             } else {
                 piece = (lane % kPieces) ^ ((row >> 1) & 7);
                 off[j] = (uint32_t)((row < room ? row : room - 1) * (int)ld + piece * 8) * 2;
@@ -151,24 +157,16 @@ struct Side {
         }
     }
 
-    // Loads of one slab; `left`: values of k from the slab's first that exist (more than 0).
-    template <typename Base>
-    __device__ __forceinline__ void load(int wave, uint32_t lds, int64_t ld, int left, Base base) const
+    // Load j of a slab at `base`; `left`: values of k from the slab's first on (more than 0).
+    __device__ __forceinline__ void load(int j, int wave, uint32_t lds, int left, const uint16_t *base) const
     {
-        const int lane = threadIdx.x & 63;
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            uint32_t o = off[j];
-            if (left < kSlab) {
-                if constexpr (ACROSS) {
-                    const int row = (j * WAVES + wave) * kLoadRows + lane / kPieces;
-                    if (row >= left) o -= (uint32_t)((row - (left - 1)) * (int)ld) * 2;
-                } else if (piece * 8 >= left) {
-                    o -= (uint32_t)piece * 16;
-                }
-            }
-            dma16(lds + (j * WAVES + wave) * 1024, o, base((j * WAVES + wave) * kLoadRows));
+        const uint32_t to = lds + (j * WAVES + wave) * 1024;
+        if (left >= kSlab) {
+            dma16(to, off[j], base);
+            return;
         }
+        const int k = ACROSS ? (j * WAVES + wave) * kLoadRows + (int)(threadIdx.x & 63) / kPieces : piece * 8;
+        dma16_from(to, k < left ? (const char *)base + off[j] : (const char *)kZeros);
     }
 
     // Values of 8 consecutive k for 32 consecutive rows from `row` (a multiple
@@ -229,7 +227,7 @@ __device__ __forceinline__ float slope_of(int act, float g, float &value)
 
 // T: the 16-bit type multiplied; O: the tensors' type.
 template <typename T, typename O, int BM, int BN, int WM, int WN, bool PA, bool QA, int END>
-__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, (BM / WM) * (BN / WN) == 8 ? 2 : 2) void k_product(ProductArgs a)
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, (BM / WM) * (BN / WN) * 64 == 256 && BM == 256 ? 1 : 2) void k_product(ProductArgs a)
 {
     constexpr int WAVES = (BM / WM) * (BN / WN), MB = WM / 32, NB = WN / 32;
     constexpr bool kPair = END != kStore;  // P's rows alternate between the two weights
@@ -279,26 +277,29 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, (BM / WM) * (BN / WN) =
     const int slabs = (a.k + kSlab - 1) / kSlab, all = slabs * a.products * a.sources;
     const int first = (int)((int64_t)all * part / a.parts), last = (int)((int64_t)all * (part + 1) / a.parts);
 
-    int seg = slabs ? first / slabs : 0, k0 = (first - seg * slabs) * kSlab;  // of the next slab to load
-    auto load = [&](int buf) {
+    // The slab to load next: its operands and how much of k is left.
+    int seg = slabs ? first / slabs : 0, k0 = (first - seg * slabs) * kSlab, left = 0;
+    const uint16_t *pb0 = nullptr, *pb1 = nullptr, *qb = nullptr;
+    auto next_slab = [&]() {
         const int src = seg / a.products, prod = seg - src * a.products;
-        const uint32_t at = lds0 + buf * STAGE;
-        {
-            const int64_t o = ((a.p_planes >> (4 * prod)) & 15) * a.p_plane + (PA ? (int64_t)k0 * a.ld_p + n0 : (int64_t)n0 * a.ld_p + k0);
-            const uint16_t *b0 = a.p[kPair ? 0 : src] + o, *b1 = a.p[1] + o;
-            p.load(wave, at, a.ld_p, (PA ? a.p_valid : a.k) - k0,
-                   [&](int row) { return kPair && (row & 32) ? b1 : b0; });
-        }
-        {
-            const int64_t o = ((a.q_planes >> (4 * prod)) & 15) * a.q_plane + (QA ? (int64_t)k0 * a.ld_q + m0 : m0 * a.ld_q + k0);
-            const uint16_t *b0 = a.q[a.outs == 2 ? which : src] + o;
-            q.load(wave, at + P::kBytes, a.ld_q, (QA ? a.q_valid : a.k) - k0, [&](int) { return b0; });
-        }
+        const int64_t po = ((a.p_planes >> (4 * prod)) & 15) * a.p_plane + (PA ? (int64_t)k0 * a.ld_p + n0 : (int64_t)n0 * a.ld_p + k0);
+        pb0 = a.p[kPair ? 0 : src] + po;
+        pb1 = a.p[1] + po;
+        qb = a.q[a.outs == 2 ? which : src] + ((a.q_planes >> (4 * prod)) & 15) * a.q_plane +
+             (QA ? (int64_t)k0 * a.ld_q + m0 : m0 * a.ld_q + k0);
+        left = a.k - k0;
         k0 += kSlab;
         if (k0 >= a.k) {
             k0 = 0;
             ++seg;
         }
+    };
+    constexpr int kLoads = P::kLoads + Q::kLoads;
+    auto load = [&](int l, uint32_t at) {  // load l of the slab
+        if (l < P::kLoads)
+            p.load(l, wave, at, left, kPair && (((l * WAVES + wave) * P::kLoadRows) & 32) ? pb1 : pb0);
+        else
+            q.load(l - P::kLoads, wave, at + P::kBytes, left, qb);
     };
 
     f32x16 acc[NB][MB];
@@ -308,39 +309,57 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, (BM / WM) * (BN / WN) =
         for (int j = 0; j < MB; ++j) acc[i][j] = (f32x16)0.f;
 
     const int wn = (wave % (BN / WN)) * WN, wm = (wave / (BN / WN)) * WM;
-    auto step = [&](const char *at, int kk) {
-        s16x8 fp[NB], fq[MB];
-#pragma unroll
-        for (int i = 0; i < NB; ++i) fp[i] = P::fragment(at, wn + i * 32, kk);
-#pragma unroll
-        for (int j = 0; j < MB; ++j) fq[j] = Q::fragment(at + P::kBytes, wm + j * 32, kk);
-#pragma unroll
-        for (int i = 0; i < NB; ++i)
-#pragma unroll
-            for (int j = 0; j < MB; ++j) acc[i][j] = mma<T>(fp[i], fq[j], acc[i][j]);
+    // Two slabs are in LDS or on their way.  A slab's four steps each multiply
+    // what the step before read from LDS and read what the next one multiplies;
+    // the last step begins with the slab's only barrier, behind which the next
+    // slab is whole and this one's place is free for the slab after it.
+    s16x8 fp[2][NB], fq[2][MB];
+    auto read = [&](int set, int r, const char *at, int kk) {  // fragment r of a step
+        if (r < NB) fp[set][r] = P::fragment(at, wn + r * 32, kk);
+        else fq[set][r - NB] = Q::fragment(at + P::kBytes, wm + (r - NB) * 32, kk);
     };
-
-    int kc = k0;  // of the slab that is multiplied
-    if (first < last) load(0);
-    for (int t = first; t < last; ++t) {
-        const int buf = (t - first) & 1;
-        if (t + 1 < last) {
-            load(buf ^ 1);
-            wait_loads<P::kLoads + Q::kLoads>();
-        } else {
-            wait_loads<0>();
-        }
-        barrier();  // the slab is in LDS, of all waves
-        const char *at = lds + buf * STAGE;
-        if (a.k - kc >= kSlab) {
+    constexpr int kCells = NB * MB, kReads = NB + MB;
+    const int count = last - first;
+    for (int b = 0; b < 2; ++b)
+        if (b < count) {
+            next_slab();
 #pragma unroll
-            for (int kk = 0; kk < kSlab / 16; ++kk) step(at, kk);
-        } else {
-            for (int kk = 0; kk < (a.k - kc) / 16; ++kk) step(at, kk);
+            for (int l = 0; l < kLoads; ++l) load(l, lds0 + b * STAGE);
         }
-        kc += kSlab;
-        if (kc >= a.k) kc = 0;
-        barrier();  // all waves have read it
+    if (count) {
+        if (count > 1) wait_loads<kLoads>();
+        else wait_loads<0>();
+        barrier();
+#pragma unroll
+        for (int r = 0; r < kReads; ++r) read(0, r, lds, 0);
+    }
+    for (int t = 0; t < count; ++t) {
+        const char *at = lds + (t & 1) * STAGE, *other = lds + (1 - (t & 1)) * STAGE;
+        const uint32_t free = lds0 + (t & 1) * STAGE;
+        const bool more = t + 2 < count;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            if (kk == 3) {
+                // this wave's loads of the next slab, and its reads of this one
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+                barrier();
+                if (more) next_slab();
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int c = 0; c < kCells; ++c) {
+                const int i = c / MB, j = c % MB;
+                acc[i][j] = mma<T>(fp[kk & 1][i], fq[kk & 1][j], acc[i][j]);
+                if (kk == 3 && more) {
+#pragma unroll
+                    for (int l = c * kLoads / kCells; l < (c + 1) * kLoads / kCells; ++l) load(l, free);
+                }
+#pragma unroll
+                for (int r = c * kReads / kCells; r < (c + 1) * kReads / kCells; ++r)
+                    read((kk + 1) & 1, r, kk == 3 ? other : at, (kk + 1) & 3);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
     }
 
     // a lane's place: row m of the results and, in register 4 g + e of block i, column 8 g + e
@@ -390,21 +409,19 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, (BM / WM) * (BN / WN) =
                             for (int e = 0; e < 4; ++e)
                                 if (n + e < a.n) out[n + e] = (O)v[e];
                     } else {
-                        if (m >= a.m_pad || n >= a.n_pad) continue;
+                        if (m >= a.m || n >= a.n_pad) continue;
                         const O *gh = (const O *)a.gh + m * a.ld_gh;
                         f32x4 d = (f32x4)0.f;
-                        if (m < a.m) {
-                            if (n + 3 < a.n) d = __builtin_convertvector(Slot<O, 4>::load(gh + n), f32x4);
-                            else
-                                for (int e = 0; e < 4; ++e)
-                                    if (n + e < a.n) d[e] = (float)gh[n + e];
-                        }
+                        if (n + 3 < a.n) d = __builtin_convertvector(Slot<O, 4>::load(gh + n), f32x4);
+                        else
+                            for (int e = 0; e < 4; ++e)
+                                if (n + e < a.n) d[e] = (float)gh[n + e];
                         f32x4 dg, du;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             float value;
                             const float s = slope_of<FAST>(a.act, acc[i][j][4 * g + e], value);
-                            const bool in = m < a.m && n + e < a.n;
+                            const bool in = n + e < a.n;
                             dg[e] = in ? d[e] * acc[i + 1][j][4 * g + e] * s : 0.f;
                             du[e] = in ? d[e] * value : 0.f;
                         }
@@ -457,7 +474,7 @@ __global__ __launch_bounds__(256) void k_product_join(const float *part, int par
 }
 
 // A matrix [n][dim] as the products read it: 16-bit values with rows of `pad`
-// (a multiple of 16) and zeros behind the row's end; three planes for 32 bits.
+// (a multiple of 8) and zeros behind the row's end; three planes for 32 bits.
 template <typename S>
 __global__ __launch_bounds__(256) void k_lay(const S *src, int64_t ld, int64_t n, int dim, int pad, uint16_t *out)
 {
@@ -495,7 +512,7 @@ unsigned blocks_for(int64_t threads)
     return (unsigned)(b < 1 ? 1 : b > 65536 ? 65536 : b);
 }
 
-int pad16(int64_t v) { return (int)((v + 15) & ~(int64_t)15); }
+int pad8(int v) { return (v + 7) & ~7; }
 
 // A matrix as an operand: in place, or laid out in the working memory.
 struct Operand {
@@ -516,16 +533,16 @@ struct Room {
 };
 
 // In place where the loads can take it: 16-bit values, rows that begin at 16
-// bytes and hold whole steps of 16, spaced so that a tile's offsets fit 32 bits.
+// bytes and hold whole pieces of 16 bytes, spaced so that a tile's offsets fit 32 bits.
 Operand operand(Room &room, const void *p, int type, int64_t n, int dim, int64_t ld)
 {
     Operand o;
-    if (p && type != kF32 && dim % 16 == 0 && ld % 8 == 0 && ((uintptr_t)p & 15) == 0 && ld < (1 << 22)) {
+    if (p && type != kF32 && dim % 8 == 0 && ld % 8 == 0 && ((uintptr_t)p & 15) == 0 && ld < (1 << 22)) {
         o.p = (const uint16_t *)p;
         o.ld = ld;
         return o;
     }
-    const int pad = pad16(dim);
+    const int pad = pad8(dim);
     o.laid = true;
     o.ld = pad;
     o.plane = n * pad;
@@ -547,13 +564,12 @@ template <typename T, typename O, bool PA, bool QA, int END>
 hipError_t run_product(ProductArgs &a, bool large, hipStream_t s)
 {
     const int bm = large ? 256 : 128, bn = (large ? 256 : 128) / (END == kStore ? 1 : 2);
-    const int mspan = END == kGateGrad ? a.m_pad : a.m, nspan = END == kGateGrad ? a.n_pad : a.n;
-    a.mt = (mspan + bm - 1) / bm;
-    a.nt = (nspan + bn - 1) / bn;
+    a.mt = (a.m + bm - 1) / bm;
+    a.nt = (a.n + bn - 1) / bn;
     const int64_t count = (int64_t)a.mt * a.nt * a.parts * a.outs;
-    if (count * (large ? 512 : 256) >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
+    if (count * 256 >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
     const unsigned blocks = (unsigned)count;
-    if (large) k_product<T, O, 256, 256, 128, 64, PA, QA, END><<<blocks, 512, 0, s>>>(a);
+    if (large) k_product<T, O, 256, 256, 128, 128, PA, QA, END><<<blocks, 256, 0, s>>>(a);
     else k_product<T, O, 128, 128, 64, 64, PA, QA, END><<<blocks, 256, 0, s>>>(a);
     return hipGetLastError();
 }
@@ -610,7 +626,7 @@ struct GradPlan {
     Operand x, gate, up;
     uint16_t *dg, *du;
     int64_t d_plane;
-    int m_pad, n_pad, outs;
+    int n_pad, outs;
     float *part;
     int x_parts, w_parts;
     bool x_large, w_large;
@@ -624,13 +640,12 @@ GradPlan plan(const GatedGradArgs &a)
     f.x = operand(room, a.x, a.type, a.n, a.dim, a.ld_x);
     weights(room, a.gate, a.ld_gate, a.up, a.ld_up, a.type, a.hidden, a.dim, f.gate, f.up);
     const int planes = a.type == kF32 ? 3 : 1;
-    f.m_pad = pad16(a.n);
-    f.n_pad = pad16(a.hidden);
-    f.d_plane = (int64_t)f.m_pad * f.n_pad;
+    f.n_pad = pad8(a.hidden);
+    f.d_plane = a.n * f.n_pad;
     f.dg = (uint16_t *)room.take((uint64_t)f.d_plane * 2 * planes);
     f.du = (uint16_t *)room.take((uint64_t)f.d_plane * 2 * planes);
     f.outs = (a.ggate != nullptr) + (a.gup != nullptr);
-    const int64_t m = (int64_t)f.outs * a.hidden, slabs_x = (f.n_pad + 63) / 64, slabs_w = ((int64_t)f.m_pad + 63) / 64;
+    const int64_t m = (int64_t)f.outs * a.hidden, slabs_x = (f.n_pad + 63) / 64, slabs_w = (a.n + 63) / 64;
     f.x_large = large_tiles(a.n, a.dim);
     f.w_large = large_tiles(m, a.dim);
     f.x_parts = a.gx && a.n && !f.x_large ? parts_of(a.n, a.dim, slabs_x * 2 * (planes == 3 ? 6 : 1)) : 1;
@@ -669,7 +684,7 @@ ProductArgs projections(const Operand &gate, const Operand &up, const Operand &x
     p.ld_q = x.ld;
     p.p_plane = gate.plane;
     p.q_plane = x.plane;
-    p.k = pad16(dim);
+    p.k = pad8(dim);
     p.products = type != kF32 ? 1 : held ? 3 : 6;
     p.p_planes = type != kF32 ? 0 : held ? kPlanes3 : kPlanes6P;
     p.q_planes = type != kF32 || held ? 0 : kPlanes6Q;
@@ -726,7 +741,6 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s)
         p.du = f.du;
         p.d_plane = f.d_plane;
         p.ld_d = f.n_pad;
-        p.m_pad = f.m_pad;
         p.n_pad = f.n_pad;
         TRY_HIP((product<false, false, kGateGrad>(p, a.type, large_tiles(a.n, 2 * (int64_t)a.hidden), s)));
     }
@@ -740,8 +754,7 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s)
         x.ld_q = f.n_pad;
         x.p_plane = f.gate.plane;
         x.q_plane = f.d_plane;
-        x.k = f.n_pad;
-        x.p_valid = a.hidden;
+        x.k = a.hidden;
         x.products = a.type == kF32 ? 6 : 1;
         x.p_planes = a.type == kF32 ? kPlanes6P : 0;
         x.q_planes = a.type == kF32 ? kPlanes6Q : 0;
@@ -751,7 +764,7 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s)
         x.part = f.part;
         x.m = (int)a.n;
         x.n = a.dim;
-        x.n_room = pad16(a.dim);
+        x.n_room = pad8(a.dim);
         x.out[0] = a.gx;
         x.ld_out[0] = a.ld_gx;
         TRY_HIP((product<true, false, kStore>(x, a.type, f.x_large, s)));
@@ -766,9 +779,7 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s)
         w.ld_q = f.n_pad;
         w.p_plane = f.x.plane;
         w.q_plane = f.d_plane;
-        w.k = f.m_pad;
-        w.p_valid = (int)a.n;
-        w.q_valid = f.m_pad;
+        w.k = (int)a.n;
         w.products = a.type != kF32 ? 1 : a.x ? 6 : 3;
         w.p_planes = a.type != kF32 || !a.x ? 0 : kPlanes6P;
         w.q_planes = a.type != kF32 ? 0 : a.x ? kPlanes6Q : kPlanes3;
@@ -778,7 +789,7 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s)
         w.part = f.part;
         w.m = a.hidden;
         w.n = a.dim;
-        w.n_room = pad16(a.dim);
+        w.n_room = pad8(a.dim);
         w.m_room = f.n_pad;
         w.out[0] = a.ggate ? a.ggate : a.gup;
         w.out[1] = a.gup;
