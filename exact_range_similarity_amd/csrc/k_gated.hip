@@ -41,6 +41,24 @@ constexpr uint32_t kPlanes6P = 0x010201, kPlanes6Q = 0x001021, kPlanes3 = 0x012;
 
 enum { kStore, kGate, kGateGrad };
 
+// Division of numbers below 2^31 by a number known on the host.
+struct Divide {
+    uint32_t by, factor, shift;
+    void set(uint32_t d)
+    {
+        by = d;
+        uint32_t bits = 0;
+        while (((uint64_t)1 << bits) < d) ++bits;
+        // 2^p / d rounded up, p = 31 + bits: exact quotients below 2^31
+        factor = d == 1 ? 0 : (uint32_t)((((uint64_t)1 << (31 + bits)) + d - 1) / d);
+        shift = d == 1 ? 0 : bits - 1;
+    }
+    __device__ __forceinline__ int operator()(int n) const
+    {
+        return by == 1 ? n : (int)(__umulhi((uint32_t)n, factor) >> shift);
+    }
+};
+
 struct ProductArgs {
     // P: along the results' rows (n), Q: across them (m); planes of 16-bit values
     const uint16_t *p[2], *q[2];
@@ -48,11 +66,13 @@ struct ProductArgs {
     int k;                // of one product, a multiple of 8 where an operand lies along it
     int products;         // of planes
     uint32_t p_planes, q_planes;
-    int sources;          // pairs (p[i], q[i]) summed
+    int sources;          // pairs (p[i], q[i]) summed, 1 or 2
     int m, n;
     int n_room;           // columns that may be read of P across k (a multiple of 8)
     int m_room;           // the same of Q
     int mt, nt, parts, outs;
+    int slabs, all, len;  // slabs of a product, of all sources and products, of a part
+    Divide by_slabs, by_out, by_tiles, by_column, by_rest;
     void *out[2];
     int64_t ld_out[2];
     float *part;          // [parts][outs][m][n] where parts > 1
@@ -65,21 +85,13 @@ struct ProductArgs {
     int act;
 };
 
-// 16 bytes from `base` + `off` of each lane to LDS, lane by lane from `lds`.
-__device__ __forceinline__ void dma16(uint32_t lds, uint32_t off, const void *base)
-{
-    // the wait state that a write of m0 needs before it is used
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :
-                 : "s"(lds), "v"(off), "s"(base)
-                 : "memory");
-}
-
 // What is loaded in the place of values behind the end of k.
 __device__ const uint32_t kZeros[4] = {0, 0, 0, 0};
 
-__device__ __forceinline__ void dma16_from(uint32_t lds, const void *from)
+// 16 bytes from each lane's address to LDS, lane by lane from `lds`.
+__device__ __forceinline__ void dma16(uint32_t lds, const void *from)
 {
+    // the wait state that a write of m0 needs before it is used
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(lds), "v"(from) : "memory");
 }
 
@@ -157,16 +169,12 @@ struct Side {
         }
     }
 
-    // Load j of a slab at `base`; `left`: values of k from the slab's first on (more than 0).
+    // Load j of a slab at `base`, of which the first `left` values of k exist.
+    // (Without a branch, so that all of a slab's loads fit between the products.)
     __device__ __forceinline__ void load(int j, int wave, uint32_t lds, int left, const uint16_t *base) const
     {
-        const uint32_t to = lds + (j * WAVES + wave) * 1024;
-        if (left >= kSlab) {
-            dma16(to, off[j], base);
-            return;
-        }
         const int k = ACROSS ? (j * WAVES + wave) * kLoadRows + (int)(threadIdx.x & 63) / kPieces : piece * 8;
-        dma16_from(to, k < left ? (const char *)base + off[j] : (const char *)kZeros);
+        dma16(lds + (j * WAVES + wave) * 1024, k < left ? (const char *)base + off[j] : (const char *)kZeros);
     }
 
     // Values of 8 consecutive k for 32 consecutive rows from `row` (a multiple
@@ -190,7 +198,8 @@ struct Side {
     }
 };
 
-// act(g) and its derivative.
+// exp(v); FAST: the hardware's exponential, off by about |v| 2^-24 of the result,
+// for results of 16 bits.
 template <bool FAST>
 __device__ __forceinline__ float exp_of(float v)
 {
@@ -198,96 +207,157 @@ __device__ __forceinline__ float exp_of(float v)
 }
 
 template <bool FAST>
+__device__ __forceinline__ float inverse(float v)
+{
+    return FAST ? __builtin_amdgcn_rcpf(v) : 1.f / v;
+}
+
+// The normal distribution Phi(g) and its density phi(g).  FAST: the upper tail
+// of z = |g| is exp(-z^2/2) R(z), R as a polynomial in t = 1 / (1 + 0.32 z),
+// fitted to 1.4e-6 of the tail, which shares the density's exponential (erff:
+// 67M values of a block 374 us, 329 with this).
+template <bool FAST>
+__device__ __forceinline__ float normal(float g, float &density)
+{
+    const float e = exp_of<FAST>(-0.5f * g * g);
+    density = 0.39894228040143268f * e;
+    if constexpr (!FAST) return 0.5f * (1.f + erff(g * 0.70710678118654752f));
+    const float z = fabsf(g), t = __builtin_amdgcn_rcpf(1.f + 0.32f * z);
+    float r = 0.0323464572429657f;
+    r = r * t + -0.11485423147678375f;
+    r = r * t + 0.09560500830411911f;
+    r = r * t + 0.022990422323346138f;
+    r = r * t + 0.09457922726869583f;
+    r = r * t + 0.11398735642433167f;
+    r = r * t + 0.12768389284610748f;
+    r = r * t + 0.12766137719154358f;
+    const float q = e * r * t;
+    return g < 0.f ? q : 1.f - q;
+}
+
+// act(g) and its derivative.
+template <bool FAST>
 __device__ __forceinline__ float act_of(int act, float g)
 {
-    if (act == 0) return g / (1.f + exp_of<FAST>(-g));
-    if (act == 1) return 0.5f * g * (1.f + erff(g * 0.70710678118654752f));
+    if (act == 1) {
+        float density;
+        return g * normal<FAST>(g, density);
+    }
     const float k = 0.79788456080286536f;
-    return g / (1.f + exp_of<FAST>(-2.f * k * (g + 0.044715f * g * g * g)));
+    return g * inverse<FAST>(1.f + exp_of<FAST>(act == 0 ? -g : -2.f * k * (g + 0.044715f * g * g * g)));
 }
 
 template <bool FAST>
 __device__ __forceinline__ float slope_of(int act, float g, float &value)
 {
-    if (act == 0) {
-        const float s = 1.f / (1.f + exp_of<FAST>(-g));
-        value = g * s;
-        return s * (1.f + g * (1.f - s));
-    }
     if (act == 1) {
-        const float c = 0.5f * (1.f + erff(g * 0.70710678118654752f));
+        float density;
+        const float c = normal<FAST>(g, density);
         value = g * c;
-        return c + g * 0.39894228040143268f * exp_of<FAST>(-0.5f * g * g);
+        return c + g * density;
     }
     const float k = 0.79788456080286536f;
-    const float s = 1.f / (1.f + exp_of<FAST>(-2.f * k * (g + 0.044715f * g * g * g)));
+    const float s = inverse<FAST>(1.f + exp_of<FAST>(act == 0 ? -g : -2.f * k * (g + 0.044715f * g * g * g)));
     value = g * s;
-    return s + g * s * (1.f - s) * 2.f * k * (1.f + 3 * 0.044715f * g * g);
+    if (act == 0) return s * (1.f + g * (1.f - s));
+    return s + value * (1.f - s) * 2.f * k * (1.f + 3 * 0.044715f * g * g);
 }
 
+// What a workgroup works on next: a tile of one of the outputs, over a part of k.
+struct Unit {
+    int64_t m0;
+    int n0, part, which, first, last;  // slabs [first, last) of all sources and products
+};
+
 // T: the 16-bit type multiplied; O: the tensors' type.
-template <typename T, typename O, int BM, int BN, int WM, int WN, bool PA, bool QA, int END>
-__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, (BM / WM) * (BN / WN) * 64 == 256 && BM == 256 ? 1 : 2) void k_product(ProductArgs a)
+template <typename T, typename O, int BM, int BN, bool PA, bool QA, int END>
+__global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs a)
 {
-    constexpr int WAVES = (BM / WM) * (BN / WN), MB = WM / 32, NB = WN / 32;
+    constexpr int WAVES = 4, WM = BM / 2, WN = BN / 2, MB = WM / 32, NB = WN / 32;
     constexpr bool kPair = END != kStore;  // P's rows alternate between the two weights
     constexpr int CN = kPair ? BN / 2 : BN;
     constexpr bool FAST = sizeof(O) == 2;
     typedef Side<BN, WAVES, PA> P;
     typedef Side<BM, WAVES, QA> Q;
     constexpr int STAGE = P::kBytes + Q::kBytes;
-    __shared__ __align__(1024) char lds[2 * STAGE];
+    constexpr int kTurn = sizeof(O) == 2 ? WM * 64 : 0;  // a wave's room to turn 32 columns of its results
+    __shared__ __align__(1024) char lds[2 * STAGE + WAVES * kTurn];
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_char *)lds;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
 
-    // Workgroups go to the eight dies in turn: each die gets a stretch of the
-    // tiles, which lie in columns of eight rows of tiles, for its own cache.
-    const int tiles = a.mt * a.nt;
-    const int total = tiles * a.parts * a.outs;
-    int id = blockIdx.x;
-    {
-        const int q = total >> 3, r = total & 7, die = id & 7;
-        id = die * q + (die < r ? die : r) + (id >> 3);
-    }
-    const int which = id / (tiles * a.parts);
-    id -= which * tiles * a.parts;
-    const int part = id / tiles;
-    id -= part * tiles;
-    const int group = id / (8 * a.nt), rows = a.mt - group * 8 < 8 ? a.mt - group * 8 : 8;
-    id -= group * 8 * a.nt;
-    const int tm = group * 8 + id % rows, tn = id / rows;
-    const int64_t m0 = (int64_t)tm * BM;
-    const int n0 = tn * CN;
+    // Workgroups go to the eight dies in turn.  A die works through a stretch of
+    // the units of its own, whose tiles lie in columns of eight rows of tiles,
+    // so that what its workgroups read at a time stays in its cache.
+    const int total = a.by_out.by * a.outs;
+    const int die = blockIdx.x & 7, stride = (int)gridDim.x >> 3;
+    const int share = total >> 3, rest = total & 7;
+    const int end = (die + 1) * share + (die < rest ? die + 1 : rest);
+    int unit = die * share + (die < rest ? die : rest) + (int)(blockIdx.x >> 3);
+    if (unit >= end) return;
+    auto decode = [&](int id) {
+        Unit u;
+        u.which = a.by_out(id);
+        id -= u.which * a.by_out.by;
+        u.part = a.by_tiles(id);
+        id -= u.part * a.by_tiles.by;
+        const int group = a.by_column(id);
+        id -= group * a.by_column.by;
+        const bool whole = group * 8 + 8 <= a.mt;
+        const int tn = whole ? id >> 3 : a.by_rest(id);
+        u.n0 = tn * CN;
+        u.m0 = (int64_t)(group * 8 + id - tn * (whole ? 8 : (int)a.by_rest.by)) * BM;
+        u.first = u.part * a.len;
+        u.last = u.first + a.len < a.all ? u.first + a.len : a.all;
+        return u;
+    };
 
+    // The loads run two slabs ahead of the products, across units.
     P p;
     Q q;
-    p.init(wave, a.ld_p, PA ? a.n_room - n0 : a.n - n0);
-    if constexpr (kPair) {
-        // row r of the slab is row n0 + (r / 64) * 32 + r % 32 of Wg (r / 32 even) or Wu
-        const int r = lane / P::kPieces;
+    Unit lu = decode(unit);
+    int lunit = unit, pos = lu.first, seg = a.by_slabs(lu.first), k0 = (lu.first - seg * a.slabs) * kSlab, left = 0;
+    bool edge = false;  // the offsets are those of a tile at the block's edge
+    auto offsets = [&]() {
+        p.init(wave, a.ld_p, PA ? a.n_room - lu.n0 : a.n - lu.n0);
+        if constexpr (kPair) {
+            // row r of the slab is row n0 + (r / 64) * 32 + r % 32 of Wg (r / 32 even) or Wu
+            const int r = lane / P::kPieces;
 #pragma unroll
-        for (int j = 0; j < P::kLoads; ++j) {
-            const int row = (j * WAVES + wave) * P::kLoadRows + r;
-            const int of = (row >> 6) * 32 + (row & 31);
-            p.off[j] = (uint32_t)((of < a.n - n0 ? of : a.n - n0 - 1) * (int)a.ld_p + p.piece * 8) * 2;
+            for (int j = 0; j < P::kLoads; ++j) {
+                const int row = (j * WAVES + wave) * P::kLoadRows + r;
+                const int of = (row >> 6) * 32 + (row & 31);
+                p.off[j] = (uint32_t)((of < a.n - lu.n0 ? of : a.n - lu.n0 - 1) * (int)a.ld_p + p.piece * 8) * 2;
+            }
         }
-    }
-    q.init(wave, a.ld_q, QA ? a.m_room - (int)m0 : (a.m - m0 < BM ? (int)(a.m - m0) : BM));
-
-    const int slabs = (a.k + kSlab - 1) / kSlab, all = slabs * a.products * a.sources;
-    const int first = (int)((int64_t)all * part / a.parts), last = (int)((int64_t)all * (part + 1) / a.parts);
-
-    // The slab to load next: its operands and how much of k is left.
-    int seg = slabs ? first / slabs : 0, k0 = (first - seg * slabs) * kSlab, left = 0;
+        const int64_t room = (QA ? a.m_room : a.m) - lu.m0;
+        q.init(wave, a.ld_q, room < BM ? (int)room : BM);
+        edge = lu.n0 + CN > a.n || lu.m0 + BM > a.m;
+    };
+    offsets();
     const uint16_t *pb0 = nullptr, *pb1 = nullptr, *qb = nullptr;
     auto next_slab = [&]() {
-        const int src = seg / a.products, prod = seg - src * a.products;
-        const int64_t po = ((a.p_planes >> (4 * prod)) & 15) * a.p_plane + (PA ? (int64_t)k0 * a.ld_p + n0 : (int64_t)n0 * a.ld_p + k0);
+        if (pos == lu.last) {
+            lunit += stride;
+            if (lunit >= end) {  // there is none: zeros are loaded and not read
+                lunit = end;
+                left = 0;
+                return;
+            }
+            lu = decode(lunit);
+            pos = lu.first;
+            seg = a.by_slabs(pos);
+            k0 = (pos - seg * a.slabs) * kSlab;
+            if (edge || lu.n0 + CN > a.n || lu.m0 + BM > a.m) offsets();
+        }
+        const int src = seg >= a.products, prod = seg - src * a.products;
+        const int64_t po = ((a.p_planes >> (4 * prod)) & 15) * a.p_plane +
+                           (PA ? (int64_t)k0 * a.ld_p + lu.n0 : (int64_t)lu.n0 * a.ld_p + k0);
         pb0 = a.p[kPair ? 0 : src] + po;
         pb1 = a.p[1] + po;
-        qb = a.q[a.outs == 2 ? which : src] + ((a.q_planes >> (4 * prod)) & 15) * a.q_plane +
-             (QA ? (int64_t)k0 * a.ld_q + m0 : m0 * a.ld_q + k0);
+        qb = a.q[a.outs == 2 ? lu.which : src] + ((a.q_planes >> (4 * prod)) & 15) * a.q_plane +
+             (QA ? (int64_t)k0 * a.ld_q + lu.m0 : lu.m0 * a.ld_q + k0);
         left = a.k - k0;
+        ++pos;
         k0 += kSlab;
         if (k0 >= a.k) {
             k0 = 0;
@@ -302,13 +372,13 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, (BM / WM) * (BN / WN) *
             q.load(l - P::kLoads, wave, at + P::kBytes, left, qb);
     };
 
+    const int wn = (wave & 1) * WN, wm = (wave >> 1) * WM;
     f32x16 acc[NB][MB];
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
         for (int j = 0; j < MB; ++j) acc[i][j] = (f32x16)0.f;
 
-    const int wn = (wave % (BN / WN)) * WN, wm = (wave / (BN / WN)) * WM;
     // Two slabs are in LDS or on their way.  A slab's four steps each multiply
     // what the step before read from LDS and read what the next one multiplies;
     // the last step begins with the slab's only barrier, behind which the next
@@ -319,136 +389,262 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, (BM / WM) * (BN / WN) *
         else fq[set][r - NB] = Q::fragment(at + P::kBytes, wm + (r - NB) * 32, kk);
     };
     constexpr int kCells = NB * MB, kReads = NB + MB;
-    const int count = last - first;
-    for (int b = 0; b < 2; ++b)
-        if (b < count) {
-            next_slab();
+    for (int b = 0; b < 2; ++b) {
+        next_slab();
 #pragma unroll
-            for (int l = 0; l < kLoads; ++l) load(l, lds0 + b * STAGE);
-        }
-    if (count) {
-        if (count > 1) wait_loads<kLoads>();
-        else wait_loads<0>();
-        barrier();
-#pragma unroll
-        for (int r = 0; r < kReads; ++r) read(0, r, lds, 0);
+        for (int l = 0; l < kLoads; ++l) load(l, lds0 + b * STAGE);
     }
-    for (int t = 0; t < count; ++t) {
-        const char *at = lds + (t & 1) * STAGE, *other = lds + (1 - (t & 1)) * STAGE;
-        const uint32_t free = lds0 + (t & 1) * STAGE;
-        const bool more = t + 2 < count;
+    wait_loads<0>();
+    barrier();
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            if (kk == 3) {
-                // this wave's loads of the next slab, and its reads of this one
-                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-                barrier();
-                if (more) next_slab();
-            }
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int c = 0; c < kCells; ++c) {
-                const int i = c / MB, j = c % MB;
-                acc[i][j] = mma<T>(fp[kk & 1][i], fq[kk & 1][j], acc[i][j]);
-                if (kk == 3 && more) {
-#pragma unroll
-                    for (int l = c * kLoads / kCells; l < (c + 1) * kLoads / kCells; ++l) load(l, free);
-                }
-#pragma unroll
-                for (int r = c * kReads / kCells; r < (c + 1) * kReads / kCells; ++r)
-                    read((kk + 1) & 1, r, kk == 3 ? other : at, (kk + 1) & 3);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        }
-    }
+    for (int r = 0; r < kReads; ++r) read(0, r, lds, 0);
 
-    // a lane's place: row m of the results and, in register 4 g + e of block i, column 8 g + e
-    const int ln = (lane >> 5) * 4;
+    char *turn = lds + 2 * STAGE + wave * kTurn;
+    int buf = 0;
+    for (; unit < end; unit += stride) {
+        const Unit u = decode(unit);
+        for (int t = u.first; t < u.last; ++t) {
+            const char *at = lds + buf * STAGE, *other = lds + (1 - buf) * STAGE;
+            const uint32_t free = lds0 + buf * STAGE;
+            buf ^= 1;
 #pragma unroll
-    for (int j = 0; j < MB; ++j) {
-        const int64_t m = m0 + wm + j * 32 + (lane & 31);
-        if constexpr (END == kStore) {
-            if (m >= a.m) continue;
-            float *part_out = a.parts > 1 ? a.part + (((int64_t)part * a.outs + which) * a.m + m) * a.n : nullptr;
-            O *out = (O *)a.out[which] + m * a.ld_out[which];
-#pragma unroll
-            for (int i = 0; i < NB; ++i)
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int n = n0 + wn + i * 32 + g * 8 + ln;
-                    f32x4 v;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * g + e];
-                    if (a.parts > 1) {
-                        if (n + 3 < a.n) Slot<float, 4>::store(part_out + n, v);
-                        else
-                            for (int e = 0; e < 4; ++e)
-                                if (n + e < a.n) part_out[n + e] = v[e];
-                    } else {
-                        if (n + 3 < a.n) Slot<O, 4>::store(out + n, __builtin_convertvector(v, typename Slot<O, 4>::vec));
-                        else
-                            for (int e = 0; e < 4; ++e)
-                                if (n + e < a.n) out[n + e] = (O)v[e];
-                    }
+            for (int kk = 0; kk < 4; ++kk) {
+                if (kk == 3) {
+                    // this wave's loads of the next slab, and its reads of this one
+                    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+                    barrier();
+                    next_slab();
                 }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int c = 0; c < kCells; ++c) {
+                    const int i = c / MB, j = c % MB;
+                    acc[i][j] = mma<T>(fp[kk & 1][i], fq[kk & 1][j], acc[i][j]);
+                    if (kk == 3) {
+#pragma unroll
+                        for (int l = c * kLoads / kCells; l < (c + 1) * kLoads / kCells; ++l) load(l, free);
+                    }
+#pragma unroll
+                    for (int r = c * kReads / kCells; r < (c + 1) * kReads / kCells; ++r)
+                        read((kk + 1) & 1, r, kk == 3 ? other : at, (kk + 1) & 3);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        }
+
+        // A lane's place: row j * 32 + lane % 32 of the wave's and, in register
+        // 4 g + e of block i, column i * 32 + 8 g + 4 (lane / 32) + e.
+        const int ln = (lane >> 5) * 4;
+        const int64_t mw = u.m0 + wm;
+        const int nw = u.n0 + (kPair ? wn / 2 : wn);
+        // Rows of 32 columns of 16 bits, turned through LDS so that a lane moves
+        // 16 bytes and four lanes a row; pieces of 16 bytes are exchanged by the
+        // row, so that all banks take part.
+        auto place = [&](int row, int piece) { return turn + row * 64 + ((piece ^ ((row >> 2) & 3)) << 4); };
+        auto put = [&](int j, int g, typename Slot<T, 4>::vec v) {
+            *(typename Slot<T, 4>::vec *)(place(j * 32 + (lane & 31), g) + (lane >> 5) * 8) = v;
+        };
+        auto store = [&](T *out, int64_t ld, int col, int64_t width) {  // the wave's rows, columns from col on
+#pragma unroll
+            for (int r = 0; r < WM / 16; ++r) {
+                const int row = r * 16 + (lane >> 2), c = col + (lane & 3) * 8;
+                const typename Slot<T, 8>::vec v = *(const typename Slot<T, 8>::vec *)place(row, lane & 3);
+                if (mw + row >= a.m) continue;
+                T *to = out + (mw + row) * ld + c;
+                if (c + 8 <= width) Slot<T, 8>::store(to, v);
+                else
+                    for (int e = 0; e < 8; ++e)
+                        if (c + e < width) to[e] = v[e];
+            }
+        };
+        auto quad = [&](const f32x16 &v, int g) { return (f32x4){v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]}; };
+        if constexpr (END == kStore) {
+            if (a.parts > 1 || sizeof(O) == 4) {
+                // 32 bits: a lane's four neighbours as they are
+                float *out;
+                int64_t ld;
+                if (a.parts > 1) {
+                    out = a.part + ((int64_t)u.part * a.outs + u.which) * a.m * a.n;
+                    ld = a.n;
+                } else {
+                    out = (float *)a.out[u.which];
+                    ld = a.ld_out[u.which];
+                }
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+#pragma unroll
+                    for (int j = 0; j < MB; ++j) {
+                        const int64_t m = mw + j * 32 + (lane & 31);
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            const int n = nw + i * 32 + g * 8 + ln;
+                            const f32x4 v = quad(acc[i][j], g);
+                            if (m >= a.m) continue;
+                            if (n + 3 < a.n) Slot<float, 4>::store(out + m * ld + n, v);
+                            else
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (n + e < a.n) out[m * ld + n + e] = v[e];
+                        }
+                    }
+            } else if constexpr (sizeof(O) == 2) {
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+#pragma unroll
+                    for (int j = 0; j < MB; ++j)
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+                            put(j, g, __builtin_convertvector(quad(acc[i][j], g), typename Slot<T, 4>::vec));
+                    store((T *)a.out[u.which], a.ld_out[u.which], nw + i * 32, a.n);
+                }
+            }
         } else {
 #pragma unroll
-            for (int i = 0; i < NB; i += 2)
+            for (int i = 0; i < NB; i += 2) {
+                const int col = nw + i * 16;
+                if constexpr (END == kGateGrad && sizeof(O) == 2) {
+                    // grad_h to the lanes that hold g and u
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int n = n0 + (wn + i * 32) / 2 + g * 8 + ln;
-                    if constexpr (END == kGate) {
-                        if (m >= a.m) continue;
-                        f32x4 v;
+                    for (int r = 0; r < WM / 16; ++r) {
+                        const int row = r * 16 + (lane >> 2), c = col + (lane & 3) * 8;
+                        typename Slot<T, 8>::vec v = (typename Slot<T, 8>::vec)(T)0.f;
+                        if (mw + row < a.m) {
+                            const T *from = (const T *)a.gh + (mw + row) * a.ld_gh + c;
+                            if (c + 8 <= a.n) v = Slot<T, 8>::load(from);
+                            else
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            v[e] = act_of<FAST>(a.act, acc[i][j][4 * g + e]) * acc[i + 1][j][4 * g + e];
-                        O *out = (O *)a.out[0] + m * a.ld_out[0];
-                        if (n + 3 < a.n) Slot<O, 4>::store(out + n, __builtin_convertvector(v, typename Slot<O, 4>::vec));
-                        else
-                            for (int e = 0; e < 4; ++e)
-                                if (n + e < a.n) out[n + e] = (O)v[e];
-                    } else {
-                        if (m >= a.m || n >= a.n_pad) continue;
-                        const O *gh = (const O *)a.gh + m * a.ld_gh;
-                        f32x4 d = (f32x4)0.f;
-                        if (n + 3 < a.n) d = __builtin_convertvector(Slot<O, 4>::load(gh + n), f32x4);
-                        else
-                            for (int e = 0; e < 4; ++e)
-                                if (n + e < a.n) d[e] = (float)gh[n + e];
-                        f32x4 dg, du;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float value;
-                            const float s = slope_of<FAST>(a.act, acc[i][j][4 * g + e], value);
-                            const bool in = n + e < a.n;
-                            dg[e] = in ? d[e] * acc[i + 1][j][4 * g + e] * s : 0.f;
-                            du[e] = in ? d[e] * value : 0.f;
+                                for (int e = 0; e < 8; ++e) v[e] = c + e < a.n ? from[e] : (T)0.f;
                         }
-                        const int64_t at = m * a.ld_d + n;
-                        if constexpr (sizeof(O) == 2) {
-                            *(typename Slot<T, 4>::vec *)(a.dg + at) = __builtin_convertvector(dg, typename Slot<T, 4>::vec);
-                            *(typename Slot<T, 4>::vec *)(a.du + at) = __builtin_convertvector(du, typename Slot<T, 4>::vec);
-                        } else {
+                        *(typename Slot<T, 8>::vec *)place(row, lane & 3) = v;
+                    }
+                }
 #pragma unroll
-                            for (int k = 0; k < 3; ++k) {
-                                s16x4 x, y;
+                for (int j = 0; j < MB; ++j) {
+                    __builtin_amdgcn_sched_barrier(0);  // one block at a time, for the registers' sake
+                    const int64_t m = mw + j * 32 + (lane & 31);
+                    if constexpr (END == kGate) {
+                        f32x16 h;
+                        switch (a.act) {
+                        case 0:
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    float v = dg[e], w = du[e];
-                                    x[e] = (short)part_of(v);
-                                    y[e] = (short)part_of(w);
-                                    dg[e] = v;
-                                    du[e] = w;
-                                }
-                                *(s16x4 *)(a.dg + k * a.d_plane + at) = x;
-                                *(s16x4 *)(a.du + k * a.d_plane + at) = y;
+                            for (int e = 0; e < 16; ++e) h[e] = act_of<FAST>(0, acc[i][j][e]) * acc[i + 1][j][e];
+                            break;
+                        case 1:
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) h[e] = act_of<FAST>(1, acc[i][j][e]) * acc[i + 1][j][e];
+                            break;
+                        default:
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) h[e] = act_of<FAST>(2, acc[i][j][e]) * acc[i + 1][j][e];
+                        }
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            const f32x4 v = quad(h, g);
+                            if constexpr (sizeof(O) == 2) {
+                                put(j, g, __builtin_convertvector(v, typename Slot<T, 4>::vec));
+                            } else if (m < a.m) {
+                                const int n = col + g * 8 + ln;
+                                float *out = (float *)a.out[0] + m * a.ld_out[0];
+                                if (n + 3 < a.n) Slot<float, 4>::store(out + n, v);
+                                else
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+                                        if (n + e < a.n) out[n + e] = v[e];
                             }
+                        }
+                    } else {
+                        // g and u give way to dg and du
+                        f32x16 d;
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            f32x4 v = (f32x4)0.f;
+                            if constexpr (sizeof(O) == 2) {
+                                v = __builtin_convertvector(*(const typename Slot<T, 4>::vec *)(
+                                        place(j * 32 + (lane & 31), g) + (lane >> 5) * 8), f32x4);
+                            } else {
+                                const int n = col + g * 8 + ln;
+                                const float *gh = (const float *)a.gh + m * a.ld_gh;
+                                if (m < a.m && n + 3 < a.n) v = Slot<float, 4>::load(gh + n);
+                                else
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) v[e] = m < a.m && n + e < a.n ? gh[n + e] : 0.f;
+                            }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) d[4 * g + e] = v[e];
+                        }
+                        auto both = [&](int act) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                float value;
+                                const float s = slope_of<FAST>(act, acc[i][j][e], value);
+                                acc[i][j][e] = d[e] * acc[i + 1][j][e] * s;
+                                acc[i + 1][j][e] = d[e] * value;
+                            }
+                        };
+                        switch (a.act) {
+                        case 0: both(0); break;
+                        case 1: both(1); break;
+                        default: both(2);
                         }
                     }
                 }
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (sizeof(O) == 2) {
+                    if constexpr (END == kGateGrad) {
+                        // zeros behind the block's columns come from the zeros in the place of grad_h
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                            for (int j = 0; j < MB; ++j)
+#pragma unroll
+                                for (int g = 0; g < 4; ++g)
+                                    put(j, g, __builtin_convertvector(quad(acc[i + half][j], g), typename Slot<T, 4>::vec));
+                            store((T *)(half ? a.du : a.dg), a.ld_d, col, a.n_pad);
+                        }
+                    } else {
+                        store((T *)a.out[0], a.ld_out[0], col, a.n);
+                    }
+                } else if constexpr (END == kGateGrad) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+#pragma unroll
+                        for (int j = 0; j < MB; ++j) {
+                            const int64_t m = mw + j * 32 + (lane & 31);
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                const int n = col + g * 8 + ln;
+                                f32x4 v = quad(acc[i + half][j], g);
+                                if (m >= a.m || n >= a.n_pad) continue;
+                                uint16_t *to = (half ? a.du : a.dg) + m * a.ld_d + n;
+#pragma unroll
+                                for (int k = 0; k < 3; ++k) {
+                                    s16x4 x;
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        float f = v[e];
+                                        x[e] = (short)part_of(f);
+                                        v[e] = f;
+                                    }
+                                    *(s16x4 *)(to + k * a.d_plane) = x;
+                                }
+                            }
+                        }
+                }
+            }
         }
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int j = 0; j < MB; ++j) acc[i][j] = (f32x16)0.f;
     }
+}
+
+// Zeros, for the gradients of weights that no row meets.
+template <typename O>
+__global__ __launch_bounds__(256) void k_zero(O *out, int64_t ld, int m, int n)
+{
+    for (int64_t r = blockIdx.x; r < m; r += gridDim.x)
+        for (int c = threadIdx.x; c < n; c += 256) out[r * ld + c] = (O)0.f;
 }
 
 // Sums of the parts of a product, in order.
@@ -563,14 +759,32 @@ hipError_t lay(const Operand &o, const void *src, int type, int64_t n, int dim, 
 template <typename T, typename O, bool PA, bool QA, int END>
 hipError_t run_product(ProductArgs &a, bool large, hipStream_t s)
 {
+    // that end's code for 32 bits is too long for the large tile
+    constexpr bool kLarge = !(END == kGateGrad && sizeof(O) == 4);
+    large = large && kLarge;
     const int bm = large ? 256 : 128, bn = (large ? 256 : 128) / (END == kStore ? 1 : 2);
     a.mt = (a.m + bm - 1) / bm;
     a.nt = (a.n + bn - 1) / bn;
+    a.slabs = (a.k + kSlab - 1) / kSlab;
+    a.all = a.slabs * a.products * a.sources;
+    a.len = (a.all + a.parts - 1) / a.parts;
+    a.parts = (a.all + a.len - 1) / a.len;  // none is empty
     const int64_t count = (int64_t)a.mt * a.nt * a.parts * a.outs;
-    if (count * 256 >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
-    const unsigned blocks = (unsigned)count;
-    if (large) k_product<T, O, 256, 256, 128, 128, PA, QA, END><<<blocks, 256, 0, s>>>(a);
-    else k_product<T, O, 128, 128, 64, 64, PA, QA, END><<<blocks, 256, 0, s>>>(a);
+    if (count >= (int64_t)1 << 31) return hipErrorInvalidConfiguration;
+    a.by_slabs.set(a.slabs);
+    a.by_out.set(a.mt * a.nt * a.parts);
+    a.by_tiles.set(a.mt * a.nt);
+    a.by_column.set(8 * a.nt);
+    a.by_rest.set(a.mt % 8 ? a.mt % 8 : 8);
+    // as many workgroups as run at once, a multiple of the dies
+    const int64_t most = large ? 256 : 512;
+    const unsigned blocks = (unsigned)(count < most ? (count + 7) & ~(int64_t)7 : most);
+    if constexpr (kLarge)
+        if (large) {
+            k_product<T, O, 256, 256, PA, QA, END><<<blocks, 256, 0, s>>>(a);
+            return hipGetLastError();
+        }
+    k_product<T, O, 128, 128, PA, QA, END><<<blocks, 256, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -582,8 +796,15 @@ hipError_t product(ProductArgs &a, int type, bool large, hipStream_t s)
     return run_product<bf16_t, bf16_t, PA, QA, END>(a, large, s);
 }
 
-// Whether the tiles of 256 x 256 give every compute unit one.
-bool large_tiles(int64_t m, int64_t n) { return ((m + 255) / 256) * ((n + 255) / 256) >= 256; }
+// Whether tiles of 256 x 256 are taken: where every compute unit gets one and
+// the sum is long enough.  Two workgroups of 128 x 128 overlap one's end with the
+// other's products; one of 256 x 256 reads less (`slabs` of k; 65,536 x 384 x
+// 1024 bf16, 6 slabs: 130 us with 128, 204 with 256; 8192 x 4096 x 11008, 64
+// slabs: 1702 and 1440).
+bool large_tiles(int64_t m, int64_t n, int64_t slabs)
+{
+    return slabs >= 24 && ((m + 255) / 256) * ((n + 255) / 256) >= 256;
+}
 
 // Into how many parts the sum over k is cut so that the device is filled.
 int parts_of(int64_t m, int64_t n, int64_t slabs)
@@ -646,10 +867,11 @@ GradPlan plan(const GatedGradArgs &a)
     f.du = (uint16_t *)room.take((uint64_t)f.d_plane * 2 * planes);
     f.outs = (a.ggate != nullptr) + (a.gup != nullptr);
     const int64_t m = (int64_t)f.outs * a.hidden, slabs_x = (f.n_pad + 63) / 64, slabs_w = (a.n + 63) / 64;
-    f.x_large = large_tiles(a.n, a.dim);
-    f.w_large = large_tiles(m, a.dim);
-    f.x_parts = a.gx && a.n && !f.x_large ? parts_of(a.n, a.dim, slabs_x * 2 * (planes == 3 ? 6 : 1)) : 1;
-    f.w_parts = f.outs && !f.w_large ? parts_of(m, a.dim, slabs_w * (planes == 1 ? 1 : a.x ? 6 : 3)) : 1;
+    const int64_t all_x = slabs_x * 2 * (planes == 3 ? 6 : 1), all_w = slabs_w * (planes == 1 ? 1 : a.x ? 6 : 3);
+    f.x_large = large_tiles(a.n, a.dim, all_x);
+    f.w_large = large_tiles(m, a.dim, all_w);
+    f.x_parts = a.gx && a.n && !f.x_large ? parts_of(a.n, a.dim, all_x) : 1;
+    f.w_parts = f.outs && !f.w_large ? parts_of(m, a.dim, all_w) : 1;
     uint64_t part = 0;
     if (f.x_parts > 1) part = (uint64_t)f.x_parts * a.n * a.dim * 4;
     if (f.w_parts > 1) {
@@ -715,7 +937,7 @@ hipError_t launch_gated(const GatedArgs &a, hipStream_t s)
     ProductArgs p = projections(f.gate, f.up, f.x, a.type, false, a.n, a.dim, a.hidden, a.act);
     p.out[0] = a.h;
     p.ld_out[0] = a.ld_h;
-    return product<false, false, kGate>(p, a.type, large_tiles(a.n, 2 * (int64_t)a.hidden), s);
+    return product<false, false, kGate>(p, a.type, large_tiles(a.n, 2 * (int64_t)a.hidden, (int64_t)p.products * ((p.k + 63) / 64)), s);
 }
 
 uint64_t gated_grad_work(const GatedGradArgs &a) { return plan(a).bytes; }
@@ -742,7 +964,7 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s)
         p.d_plane = f.d_plane;
         p.ld_d = f.n_pad;
         p.n_pad = f.n_pad;
-        TRY_HIP((product<false, false, kGateGrad>(p, a.type, large_tiles(a.n, 2 * (int64_t)a.hidden), s)));
+        TRY_HIP((product<false, false, kGateGrad>(p, a.type, large_tiles(a.n, 2 * (int64_t)a.hidden, (int64_t)p.products * ((p.k + 63) / 64)), s)));
     }
     if (a.gx && a.n) {
         ProductArgs x{};
@@ -769,6 +991,14 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s)
         x.ld_out[0] = a.ld_gx;
         TRY_HIP((product<true, false, kStore>(x, a.type, f.x_large, s)));
         TRY_HIP(join(x, a.type, s));
+    }
+    if (f.outs && a.n == 0) {
+        for (int i = 0; i < 2; ++i) {
+            void *out = i ? a.gup : a.ggate;
+            const int64_t ld = i ? a.ld_gup : a.ld_ggate;
+            if (out) ERSJ_ELEM_SWITCH(a.type, O, k_zero<O><<<blocks_for(a.hidden * 256), 256, 0, s>>>((O *)out, ld, a.hidden, a.dim));
+        }
+        return hipGetLastError();
     }
     if (f.outs) {
         ProductArgs w{};

@@ -19,7 +19,7 @@ ACTIVATIONS = ["silu", "gelu", "gelu_tanh"]
 KAPPA = math.sqrt(2 / math.pi)
 
 
-def act_ref(g, act):
+def act_ref(g, act, dtype=torch.float32):
     """act(g), act'(g) and a bound on the 32-bit evaluation of each at an exact g.
 
     exp by the hardware's exponential of a rounded product: relative error at
@@ -32,8 +32,11 @@ def act_ref(g, act):
     if act == "gelu":
         phi = 0.5 * torch.erfc(-g / math.sqrt(2))
         dens = torch.exp(-0.5 * g * g) / math.sqrt(2 * math.pi)
-        # the distribution as half of 1 + erf: off by some u at most, however small it is
-        return g * phi, phi + g * dens, g.abs() * 6 * U, 6 * U + g.abs() * dens * (g * g + 10) * U
+        # the distribution as half of 1 + erf: off by some u at most, however small it is; for 16
+        # bits its upper tail by exp and a polynomial, fitted to 1.4e-6 of the tail
+        tail = torch.minimum(phi, 1 - phi) * (0.0 if dtype == torch.float32 else 1.4e-6 + (g * g + 10) * U)
+        return (g * phi, phi + g * dens, g.abs() * (6 * U + tail),
+                6 * U + tail + g.abs() * dens * (g * g + 10) * U)
     z = KAPPA * (g + 0.044715 * g ** 3)
     s = torch.sigmoid(2 * z)
     rel = (2 * z.abs() * 6 + 10) * U  # the argument itself is off by a few u
@@ -60,7 +63,7 @@ def forward(x, w_gate, w_up, act, held=False):
     g, u = a @ wg.t(), a @ wu.t()
     eg = sum_error(k, x.dtype, a.abs() @ wg.abs().t(), held)
     eu = sum_error(k, x.dtype, a.abs() @ wu.abs().t(), held)
-    return g, u, eg, eu, act_ref(g, act)
+    return g, u, eg, eu, act_ref(g, act, x.dtype)
 
 
 def check_gated(got, x, w_gate, w_up, act, label=""):
