@@ -29,15 +29,14 @@ typedef __attribute__((address_space(3))) char lds_char;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef f16_t f16x8 __attribute__((ext_vector_type(8)));
 typedef bf16_t bf16x8 __attribute__((ext_vector_type(8)));
-
-constexpr int kSlab = 64;
 
 // Which planes are multiplied in turn, four bits each, smallest products first:
 // one plane, three of both operands, three of one of them.
 constexpr uint32_t kPlanes6P = 0x010201, kPlanes6Q = 0x001021, kPlanes3 = 0x012;
+
+constexpr int kSlab = 64, kSteps = kSlab / 32, kStages = 2;
 
 enum { kStore, kGate, kGateGrad };
 
@@ -85,14 +84,25 @@ struct ProductArgs {
     int act;
 };
 
-// What is loaded in the place of values behind the end of k.
-__device__ const uint32_t kZeros[4] = {0, 0, 0, 0};
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-// 16 bytes from each lane's address to LDS, lane by lane from `lds`.
-__device__ __forceinline__ void dma16(uint32_t lds, const void *from)
+// A buffer at `base` whose last bytes lie behind all offsets in use: kOutside
+// is outside of it, and a load from there gives zeros.
+constexpr uint32_t kOutside = 0xffffffffu;
+__device__ __forceinline__ u32x4 buffer_at(const void *base)
+{
+    const uint64_t b = (uint64_t)base;
+    return (u32x4){(uint32_t)b, (uint32_t)(b >> 32) & 0xffffu, 0xfffffff0u, 0x00020000u};
+}
+
+// 16 bytes from each lane's offset to LDS, lane by lane from `lds`.
+__device__ __forceinline__ void dma16(uint32_t lds, uint32_t off, u32x4 buffer)
 {
     // the wait state that a write of m0 needs before it is used
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(lds), "v"(from) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(off), "s"(buffer)
+                 : "memory");
 }
 
 template <int N>
@@ -107,12 +117,12 @@ __device__ __forceinline__ void barrier()
 }
 
 template <typename T>
-__device__ __forceinline__ f32x16 mma(s16x8 a, s16x8 b, f32x16 c)
+__device__ __forceinline__ f32x4 mma(s16x8 a, s16x8 b, f32x4 c)
 {
     if constexpr (sizeof(T) == 2 && __is_same(T, f16_t))
-        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
     else
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
 template <typename T>
@@ -138,10 +148,10 @@ __device__ __forceinline__ uint16_t part_of(float &v)
 }
 
 // One operand of a tile: its loads to LDS and its fragments.  ROWS values
-// across k.  Along k (ACROSS false) a row of LDS holds 64 values of k, its
-// 16-byte pieces exchanged by bits 1 to 3 of the row; across k it holds the
-// tile's ROWS values at one k, its pieces exchanged in groups of four by the
-// low bits of k.  Either way a wave's reads fall on all banks.
+// across k.  Along k (ACROSS false) a row of LDS holds kSlab values of k, its
+// 16-byte pieces exchanged by the row so that 16 neighbouring rows cover all
+// banks; across k it holds the tile's ROWS values at one k, its pieces exchanged
+// in pairs by bits 0, 1 and 3 of k.  Either way a wave's reads fall on all banks.
 template <int ROWS, int WAVES, bool ACROSS>
 struct Side {
     static constexpr int kBytes = ROWS * kSlab * 2;
@@ -151,6 +161,11 @@ struct Side {
     uint32_t off[kLoads];
     int piece;  // along k: the lane's piece
 
+    static __device__ __forceinline__ int exchange(int row)
+    {
+        return ACROSS ? (row & 3) << 1 | (row & 8) : (row >> 1) & 7;
+    }
+
     // `room`: rows (along k) or columns (across k) from the tile's first that may be read
     __device__ __forceinline__ void init(int wave, int64_t ld, int room)
     {
@@ -159,41 +174,41 @@ struct Side {
         for (int j = 0; j < kLoads; ++j) {
             const int row = (j * WAVES + wave) * kLoadRows + r;
             if constexpr (ACROSS) {
-                int c = (lane % kPieces) ^ ((row & 3) << 2);
+                int c = (lane % kPieces) ^ exchange(row);
                 c = c * 8 < room ? c : 0;
                 off[j] = (uint32_t)(row * (int)ld + c * 8) * 2;
             } else {
-                piece = (lane % kPieces) ^ ((row >> 1) & 7);
+                piece = (lane % kPieces) ^ exchange(row);
                 off[j] = (uint32_t)((row < room ? row : room - 1) * (int)ld + piece * 8) * 2;
             }
         }
     }
 
-    // Load j of a slab at `base`, of which the first `left` values of k exist.
-    // (Without a branch, so that all of a slab's loads fit between the products.)
-    __device__ __forceinline__ void load(int j, int wave, uint32_t lds, int left, const uint16_t *base) const
+    // Load j of a slab, of which the first `left` values of k exist.  (Without a
+    // branch, so that a slab's loads fit between the products.)
+    __device__ __forceinline__ void load(int j, int wave, uint32_t lds, int left, u32x4 buffer) const
     {
         const int k = ACROSS ? (j * WAVES + wave) * kLoadRows + (int)(threadIdx.x & 63) / kPieces : piece * 8;
-        dma16(lds + (j * WAVES + wave) * 1024, k < left ? (const char *)base + off[j] : (const char *)kZeros);
+        dma16(lds + (j * WAVES + wave) * 1024, k < left ? off[j] : kOutside, buffer);
     }
 
-    // Values of 8 consecutive k for 32 consecutive rows from `row` (a multiple
-    // of 32), for the matrix instruction of the slab's values 16 kk to 16 kk + 15.
+    // Values of 8 consecutive k for 16 consecutive rows from `row` (a multiple
+    // of 16), for the matrix instruction of the slab's values 32 kk to 32 kk + 31.
     static __device__ __forceinline__ s16x8 fragment(const char *lds, int row, int kk)
     {
         const int lane = threadIdx.x & 63;
         if constexpr (ACROSS) {
-            const int k = kk * 16 + (lane >> 5) * 8 + ((lane & 15) >> 2);
-            const int col = row + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
-            const int at = k * (ROWS * 2) + (((col >> 3) ^ ((k & 3) << 2)) << 4) + (col & 7) * 2;
+            const int k = kk * 32 + (lane >> 4) * 8 + ((lane & 15) >> 2), col = row + (lane & 3) * 4;
+            // four values of k on have the same exchange
+            const int at = k * (ROWS * 2) + (((col >> 3) ^ exchange(k)) << 4) + (col & 7) * 2;
             typedef __attribute__((address_space(3))) s16x4 *ptr;
             const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(lds_char *)(lds + at));
             const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(lds_char *)(lds + at + 4 * ROWS * 2));
             return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
         } else {
-            const int r = row + (lane & 31);
-            const int c = (kk * 2 + (lane >> 5)) ^ ((r >> 1) & 7);
-            return *(const s16x8 *)(lds + r * 128 + c * 16);
+            const int r = row + (lane & 15);
+            const int c = (kk * 4 + (lane >> 4)) ^ exchange(r);
+            return *(const s16x8 *)(lds + r * (kSlab * 2) + c * 16);
         }
     }
 };
@@ -273,7 +288,7 @@ struct Unit {
 template <typename T, typename O, int BM, int BN, bool PA, bool QA, int END>
 __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs a)
 {
-    constexpr int WAVES = 4, WM = BM / 2, WN = BN / 2, MB = WM / 32, NB = WN / 32;
+    constexpr int WAVES = 4, WM = BM / 2, WN = BN / 2, MB = WM / 16, NB = WN / 16;
     constexpr bool kPair = END != kStore;  // P's rows alternate between the two weights
     constexpr int CN = kPair ? BN / 2 : BN;
     constexpr bool FAST = sizeof(O) == 2;
@@ -281,7 +296,7 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
     typedef Side<BM, WAVES, QA> Q;
     constexpr int STAGE = P::kBytes + Q::kBytes;
     constexpr int kTurn = sizeof(O) == 2 ? WM * 64 : 0;  // a wave's room to turn 32 columns of its results
-    __shared__ __align__(1024) char lds[2 * STAGE + WAVES * kTurn];
+    __shared__ __align__(1024) char lds[kStages * STAGE + WAVES * kTurn];
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_char *)lds;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
 
@@ -311,11 +326,11 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
         return u;
     };
 
-    // The loads run two slabs ahead of the products, across units.
+    // The loads run up to two slabs ahead of the products, across units.
     P p;
     Q q;
     Unit lu = decode(unit);
-    int lunit = unit, pos = lu.first, seg = a.by_slabs(lu.first), k0 = (lu.first - seg * a.slabs) * kSlab, left = 0;
+    int lunit = unit, pos = lu.first, left = 0;
     bool edge = false;  // the offsets are those of a tile at the block's edge
     auto offsets = [&]() {
         p.init(wave, a.ld_p, PA ? a.n_room - lu.n0 : a.n - lu.n0);
@@ -334,8 +349,24 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
         edge = lu.n0 + CN > a.n || lu.m0 + BM > a.m;
     };
     offsets();
-    const uint16_t *pb0 = nullptr, *pb1 = nullptr, *qb = nullptr;
+    // Where the next slab lies, how much of k it has, and how many more slabs
+    // follow it side by side: most turns only move on.
+    u32x4 pb0 = (u32x4)0u, pb1 = (u32x4)0u, qb = (u32x4)0u;
+    int run = 0;
+    auto move = [](u32x4 &b, uint32_t by) {
+        const uint64_t to = ((uint64_t)b[1] << 32 | b[0]) + by;
+        b[0] = (uint32_t)to;
+        b[1] = (uint32_t)(to >> 32);
+    };
+    const uint32_t p_step = kSlab * 2 * (PA ? (uint32_t)a.ld_p : 1u), q_step = kSlab * 2 * (QA ? (uint32_t)a.ld_q : 1u);
     auto next_slab = [&]() {
+        if (--run > 0) {
+            move(pb0, p_step);
+            if constexpr (kPair) move(pb1, p_step);
+            move(qb, q_step);
+            left -= kSlab;
+            return;
+        }
         if (pos == lu.last) {
             lunit += stride;
             if (lunit >= end) {  // there is none: zeros are loaded and not read
@@ -345,24 +376,19 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
             }
             lu = decode(lunit);
             pos = lu.first;
-            seg = a.by_slabs(pos);
-            k0 = (pos - seg * a.slabs) * kSlab;
             if (edge || lu.n0 + CN > a.n || lu.m0 + BM > a.m) offsets();
         }
+        const int seg = a.by_slabs(pos), at = pos - seg * a.slabs, k0 = at * kSlab;
         const int src = seg >= a.products, prod = seg - src * a.products;
         const int64_t po = ((a.p_planes >> (4 * prod)) & 15) * a.p_plane +
                            (PA ? (int64_t)k0 * a.ld_p + lu.n0 : (int64_t)lu.n0 * a.ld_p + k0);
-        pb0 = a.p[kPair ? 0 : src] + po;
-        pb1 = a.p[1] + po;
-        qb = a.q[a.outs == 2 ? lu.which : src] + ((a.q_planes >> (4 * prod)) & 15) * a.q_plane +
-             (QA ? (int64_t)k0 * a.ld_q + lu.m0 : lu.m0 * a.ld_q + k0);
+        pb0 = buffer_at(a.p[kPair ? 0 : src] + po);
+        if constexpr (kPair) pb1 = buffer_at(a.p[1] + po);
+        qb = buffer_at(a.q[a.outs == 2 ? lu.which : src] + ((a.q_planes >> (4 * prod)) & 15) * a.q_plane +
+                       (QA ? (int64_t)k0 * a.ld_q + lu.m0 : lu.m0 * a.ld_q + k0));
         left = a.k - k0;
-        ++pos;
-        k0 += kSlab;
-        if (k0 >= a.k) {
-            k0 = 0;
-            ++seg;
-        }
+        run = a.slabs - at < lu.last - pos ? a.slabs - at : lu.last - pos;
+        pos += run;
     };
     constexpr int kLoads = P::kLoads + Q::kLoads;
     auto load = [&](int l, uint32_t at) {  // load l of the slab
@@ -373,94 +399,111 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
     };
 
     const int wn = (wave & 1) * WN, wm = (wave >> 1) * WM;
-    f32x16 acc[NB][MB];
+    f32x4 acc[NB][MB];
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
-        for (int j = 0; j < MB; ++j) acc[i][j] = (f32x16)0.f;
+        for (int j = 0; j < MB; ++j) acc[i][j] = (f32x4)0.f;
 
-    // Two slabs are in LDS or on their way.  A slab's four steps each multiply
+    // kStages slabs are in LDS or on their way.  A slab's steps each multiply
     // what the step before read from LDS and read what the next one multiplies;
     // the last step begins with the slab's only barrier, behind which the next
-    // slab is whole and this one's place is free for the slab after it.
+    // slab is whole and this one's place is free for the slab kStages later.
+    // (Four slabs of 32 in the same room are no faster, 1240 and 1309 us for dx of
+    // 8192 x 4096 x 11008, and slower in tiles of 128, where barriers come often.)
     s16x8 fp[2][NB], fq[2][MB];
-    auto read = [&](int set, int r, const char *at, int kk) {  // fragment r of a step
-        if (r < NB) fp[set][r] = P::fragment(at, wn + r * 32, kk);
-        else fq[set][r - NB] = Q::fragment(at + P::kBytes, wm + (r - NB) * 32, kk);
+    // fragment r of a step, in the order in which the products need them
+    auto read = [&](int set, int r, const char *at, int kk) {
+        if (r == 0 || r > MB) fp[set][r ? r - MB : 0] = P::fragment(at, wn + (r ? r - MB : 0) * 16, kk);
+        else fq[set][r - 1] = Q::fragment(at + P::kBytes, wm + (r - 1) * 16, kk);
     };
     constexpr int kCells = NB * MB, kReads = NB + MB;
-    for (int b = 0; b < 2; ++b) {
+    // reads done before product c: all in the first half of a step
+    auto next_read = [](int c) constexpr { return c * 2 < kCells ? c * 2 * kReads / kCells : kReads; };
+    for (int b = 0; b < kStages; ++b) {
         next_slab();
 #pragma unroll
         for (int l = 0; l < kLoads; ++l) load(l, lds0 + b * STAGE);
     }
-    wait_loads<0>();
+    wait_loads<kLoads>();
     barrier();
 #pragma unroll
     for (int r = 0; r < kReads; ++r) read(0, r, lds, 0);
 
-    char *turn = lds + 2 * STAGE + wave * kTurn;
+    char *turn = lds + kStages * STAGE + wave * kTurn;
     int buf = 0;
     for (; unit < end; unit += stride) {
         const Unit u = decode(unit);
         for (int t = u.first; t < u.last; ++t) {
-            const char *at = lds + buf * STAGE, *other = lds + (1 - buf) * STAGE;
+            const char *at = lds + buf * STAGE;
             const uint32_t free = lds0 + buf * STAGE;
-            buf ^= 1;
+            buf = (buf + 1) % kStages;
+            const char *other = lds + buf * STAGE;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                if (kk == 3) {
+            for (int kk = 0; kk < kSteps; ++kk) {
+                if (kk == kSteps - 1) {
+                    next_slab();
                     // this wave's loads of the next slab, and its reads of this one
                     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
                     barrier();
-                    next_slab();
                 }
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int c = 0; c < kCells; ++c) {
                     const int i = c / MB, j = c % MB;
                     acc[i][j] = mma<T>(fp[kk & 1][i], fq[kk & 1][j], acc[i][j]);
-                    if (kk == 3) {
+                    if (kk == kSteps - 1) {
 #pragma unroll
                         for (int l = c * kLoads / kCells; l < (c + 1) * kLoads / kCells; ++l) load(l, free);
                     }
 #pragma unroll
-                    for (int r = c * kReads / kCells; r < (c + 1) * kReads / kCells; ++r)
-                        read((kk + 1) & 1, r, kk == 3 ? other : at, (kk + 1) & 3);
+                    for (int r = next_read(c); r < next_read(c + 1); ++r)
+                        read((kk + 1) & 1, r, kk == kSteps - 1 ? other : at, (kk + 1) % kSteps);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
 
-        // A lane's place: row j * 32 + lane % 32 of the wave's and, in register
-        // 4 g + e of block i, column i * 32 + 8 g + 4 (lane / 32) + e.
-        const int ln = (lane >> 5) * 4;
+        // A lane's place: row j * 16 + lane % 16 of the wave's and, in register e
+        // of block i, column i * 16 + 4 (lane / 16) + e.
+        const int ln = (lane >> 4) * 4, lm = lane & 15;
         const int64_t mw = u.m0 + wm;
         const int nw = u.n0 + (kPair ? wn / 2 : wn);
         // Rows of 32 columns of 16 bits, turned through LDS so that a lane moves
         // 16 bytes and four lanes a row; pieces of 16 bytes are exchanged by the
         // row, so that all banks take part.
+        typedef Slot<T, 4> S4;
+        typedef Slot<T, 8> S8;
         auto place = [&](int row, int piece) { return turn + row * 64 + ((piece ^ ((row >> 2) & 3)) << 4); };
-        auto put = [&](int j, int g, typename Slot<T, 4>::vec v) {
-            *(typename Slot<T, 4>::vec *)(place(j * 32 + (lane & 31), g) + (lane >> 5) * 8) = v;
+        auto mine = [&](int j, int half) {  // this lane's four of a block's half of 16 columns
+            return (typename S4::vec *)(place(j * 16 + lm, half * 2 + (lane >> 5)) + ((lane >> 4) & 1) * 8);
         };
+        auto put = [&](int j, int half, f32x4 v) { *mine(j, half) = __builtin_convertvector(v, typename S4::vec); };
         auto store = [&](T *out, int64_t ld, int col, int64_t width) {  // the wave's rows, columns from col on
 #pragma unroll
             for (int r = 0; r < WM / 16; ++r) {
                 const int row = r * 16 + (lane >> 2), c = col + (lane & 3) * 8;
-                const typename Slot<T, 8>::vec v = *(const typename Slot<T, 8>::vec *)place(row, lane & 3);
+                const typename S8::vec v = *(const typename S8::vec *)place(row, lane & 3);
                 if (mw + row >= a.m) continue;
                 T *to = out + (mw + row) * ld + c;
-                if (c + 8 <= width) Slot<T, 8>::store(to, v);
+                if (c + 8 <= width) S8::store(to, v);
                 else
+#pragma unroll
                     for (int e = 0; e < 8; ++e)
                         if (c + e < width) to[e] = v[e];
             }
         };
-        auto quad = [&](const f32x16 &v, int g) { return (f32x4){v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]}; };
+        auto store32 = [&](float *out, int64_t ld, int j, int n, f32x4 v) {  // a lane's four of 32 bits as they are
+            const int64_t m = mw + j * 16 + lm;
+            if (m >= a.m) return;
+            if (n + 3 < a.n) Slot<float, 4>::store(out + m * ld + n, v);
+            else
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n + e < a.n) out[m * ld + n + e] = v[e];
+        };
         if constexpr (END == kStore) {
             if (a.parts > 1 || sizeof(O) == 4) {
-                // 32 bits: a lane's four neighbours as they are
                 float *out;
                 int64_t ld;
                 if (a.parts > 1) {
@@ -473,112 +516,83 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
 #pragma unroll
                 for (int i = 0; i < NB; ++i)
 #pragma unroll
-                    for (int j = 0; j < MB; ++j) {
-                        const int64_t m = mw + j * 32 + (lane & 31);
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const int n = nw + i * 32 + g * 8 + ln;
-                            const f32x4 v = quad(acc[i][j], g);
-                            if (m >= a.m) continue;
-                            if (n + 3 < a.n) Slot<float, 4>::store(out + m * ld + n, v);
-                            else
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (n + e < a.n) out[m * ld + n + e] = v[e];
-                        }
-                    }
+                    for (int j = 0; j < MB; ++j) store32(out, ld, j, nw + i * 16 + ln, acc[i][j]);
             } else if constexpr (sizeof(O) == 2) {
 #pragma unroll
-                for (int i = 0; i < NB; ++i) {
+                for (int i = 0; i < NB; i += 2) {
 #pragma unroll
-                    for (int j = 0; j < MB; ++j)
-#pragma unroll
-                        for (int g = 0; g < 4; ++g)
-                            put(j, g, __builtin_convertvector(quad(acc[i][j], g), typename Slot<T, 4>::vec));
-                    store((T *)a.out[u.which], a.ld_out[u.which], nw + i * 32, a.n);
+                    for (int j = 0; j < MB; ++j) {
+                        put(j, 0, acc[i][j]);
+                        put(j, 1, acc[i + 1][j]);
+                    }
+                    store((T *)a.out[u.which], a.ld_out[u.which], nw + i * 16, a.n);
                 }
             }
         } else {
+            // blocks i and i + 1 hold g, the two after them u
 #pragma unroll
-            for (int i = 0; i < NB; i += 2) {
-                const int col = nw + i * 16;
+            for (int i = 0; i < NB; i += 4) {
+                const int col = nw + i * 8;
                 if constexpr (END == kGateGrad && sizeof(O) == 2) {
                     // grad_h to the lanes that hold g and u
 #pragma unroll
                     for (int r = 0; r < WM / 16; ++r) {
                         const int row = r * 16 + (lane >> 2), c = col + (lane & 3) * 8;
-                        typename Slot<T, 8>::vec v = (typename Slot<T, 8>::vec)(T)0.f;
+                        typename S8::vec v = (typename S8::vec)(T)0.f;
                         if (mw + row < a.m) {
                             const T *from = (const T *)a.gh + (mw + row) * a.ld_gh + c;
-                            if (c + 8 <= a.n) v = Slot<T, 8>::load(from);
+                            if (c + 8 <= a.n) v = S8::load(from);
                             else
 #pragma unroll
                                 for (int e = 0; e < 8; ++e) v[e] = c + e < a.n ? from[e] : (T)0.f;
                         }
-                        *(typename Slot<T, 8>::vec *)place(row, lane & 3) = v;
+                        *(typename S8::vec *)place(row, lane & 3) = v;
                     }
                 }
 #pragma unroll
                 for (int j = 0; j < MB; ++j) {
                     __builtin_amdgcn_sched_barrier(0);  // one block at a time, for the registers' sake
-                    const int64_t m = mw + j * 32 + (lane & 31);
+                    const int64_t m = mw + j * 16 + lm;
                     if constexpr (END == kGate) {
-                        f32x16 h;
+                        f32x4 h[2];
+                        auto both = [&](int act) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                h[e / 4][e % 4] = act_of<FAST>(act, acc[i + e / 4][j][e % 4]) * acc[i + 2 + e / 4][j][e % 4];
+                        };
                         switch (a.act) {
-                        case 0:
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) h[e] = act_of<FAST>(0, acc[i][j][e]) * acc[i + 1][j][e];
-                            break;
-                        case 1:
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) h[e] = act_of<FAST>(1, acc[i][j][e]) * acc[i + 1][j][e];
-                            break;
-                        default:
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) h[e] = act_of<FAST>(2, acc[i][j][e]) * acc[i + 1][j][e];
+                        case 0: both(0); break;
+                        case 1: both(1); break;
+                        default: both(2);
                         }
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const f32x4 v = quad(h, g);
-                            if constexpr (sizeof(O) == 2) {
-                                put(j, g, __builtin_convertvector(v, typename Slot<T, 4>::vec));
-                            } else if (m < a.m) {
-                                const int n = col + g * 8 + ln;
-                                float *out = (float *)a.out[0] + m * a.ld_out[0];
-                                if (n + 3 < a.n) Slot<float, 4>::store(out + n, v);
-                                else
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        if (n + e < a.n) out[n + e] = v[e];
-                            }
+                        for (int half = 0; half < 2; ++half) {
+                            if constexpr (sizeof(O) == 2) put(j, half, h[half]);
+                            else store32((float *)a.out[0], a.ld_out[0], j, col + half * 16 + ln, h[half]);
                         }
                     } else {
                         // g and u give way to dg and du
-                        f32x16 d;
+                        f32x4 d[2];
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            f32x4 v = (f32x4)0.f;
+                        for (int half = 0; half < 2; ++half) {
                             if constexpr (sizeof(O) == 2) {
-                                v = __builtin_convertvector(*(const typename Slot<T, 4>::vec *)(
-                                        place(j * 32 + (lane & 31), g) + (lane >> 5) * 8), f32x4);
+                                d[half] = __builtin_convertvector(*mine(j, half), f32x4);
                             } else {
-                                const int n = col + g * 8 + ln;
+                                const int n = col + half * 16 + ln;
                                 const float *gh = (const float *)a.gh + m * a.ld_gh;
-                                if (m < a.m && n + 3 < a.n) v = Slot<float, 4>::load(gh + n);
+                                if (m < a.m && n + 3 < a.n) d[half] = Slot<float, 4>::load(gh + n);
                                 else
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e) v[e] = m < a.m && n + e < a.n ? gh[n + e] : 0.f;
+                                    for (int e = 0; e < 4; ++e) d[half][e] = m < a.m && n + e < a.n ? gh[n + e] : 0.f;
                             }
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) d[4 * g + e] = v[e];
                         }
                         auto both = [&](int act) {
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
+                            for (int e = 0; e < 8; ++e) {
                                 float value;
-                                const float s = slope_of<FAST>(act, acc[i][j][e], value);
-                                acc[i][j][e] = d[e] * acc[i + 1][j][e] * s;
-                                acc[i + 1][j][e] = d[e] * value;
+                                const float s = slope_of<FAST>(act, acc[i + e / 4][j][e % 4], value), dh = d[e / 4][e % 4];
+                                acc[i + e / 4][j][e % 4] = dh * acc[i + 2 + e / 4][j][e % 4] * s;
+                                acc[i + 2 + e / 4][j][e % 4] = dh * value;
                             }
                         };
                         switch (a.act) {
@@ -593,40 +607,37 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
                     if constexpr (END == kGateGrad) {
                         // zeros behind the block's columns come from the zeros in the place of grad_h
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
+                        for (int of = 0; of < 2; ++of) {
 #pragma unroll
-                            for (int j = 0; j < MB; ++j)
-#pragma unroll
-                                for (int g = 0; g < 4; ++g)
-                                    put(j, g, __builtin_convertvector(quad(acc[i + half][j], g), typename Slot<T, 4>::vec));
-                            store((T *)(half ? a.du : a.dg), a.ld_d, col, a.n_pad);
+                            for (int j = 0; j < MB; ++j) {
+                                put(j, 0, acc[i + 2 * of][j]);
+                                put(j, 1, acc[i + 2 * of + 1][j]);
+                            }
+                            store((T *)(of ? a.du : a.dg), a.ld_d, col, a.n_pad);
                         }
                     } else {
                         store((T *)a.out[0], a.ld_out[0], col, a.n);
                     }
                 } else if constexpr (END == kGateGrad) {
 #pragma unroll
-                    for (int half = 0; half < 2; ++half)
+                    for (int of = 0; of < 4; ++of)
 #pragma unroll
                         for (int j = 0; j < MB; ++j) {
-                            const int64_t m = mw + j * 32 + (lane & 31);
+                            const int64_t m = mw + j * 16 + lm;
+                            const int n = col + (of & 1) * 16 + ln;
+                            f32x4 v = acc[i + of][j];
+                            if (m >= a.m || n >= a.n_pad) continue;
+                            uint16_t *to = (of & 2 ? a.du : a.dg) + m * a.ld_d + n;
 #pragma unroll
-                            for (int g = 0; g < 4; ++g) {
-                                const int n = col + g * 8 + ln;
-                                f32x4 v = quad(acc[i + half][j], g);
-                                if (m >= a.m || n >= a.n_pad) continue;
-                                uint16_t *to = (half ? a.du : a.dg) + m * a.ld_d + n;
+                            for (int k = 0; k < 3; ++k) {
+                                s16x4 x;
 #pragma unroll
-                                for (int k = 0; k < 3; ++k) {
-                                    s16x4 x;
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
-                                        float f = v[e];
-                                        x[e] = (short)part_of(f);
-                                        v[e] = f;
-                                    }
-                                    *(s16x4 *)(to + k * a.d_plane) = x;
+                                for (int e = 0; e < 4; ++e) {
+                                    float f = v[e];
+                                    x[e] = (short)part_of(f);
+                                    v[e] = f;
                                 }
+                                *(s16x4 *)(to + k * a.d_plane) = x;
                             }
                         }
                 }
@@ -635,7 +646,7 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
 #pragma unroll
         for (int i = 0; i < NB; ++i)
 #pragma unroll
-            for (int j = 0; j < MB; ++j) acc[i][j] = (f32x16)0.f;
+            for (int j = 0; j < MB; ++j) acc[i][j] = (f32x4)0.f;
     }
 }
 
@@ -866,7 +877,7 @@ GradPlan plan(const GatedGradArgs &a)
     f.dg = (uint16_t *)room.take((uint64_t)f.d_plane * 2 * planes);
     f.du = (uint16_t *)room.take((uint64_t)f.d_plane * 2 * planes);
     f.outs = (a.ggate != nullptr) + (a.gup != nullptr);
-    const int64_t m = (int64_t)f.outs * a.hidden, slabs_x = (f.n_pad + 63) / 64, slabs_w = (a.n + 63) / 64;
+    const int64_t m = (int64_t)f.outs * a.hidden, slabs_x = (f.n_pad + kSlab - 1) / kSlab, slabs_w = (a.n + kSlab - 1) / kSlab;
     const int64_t all_x = slabs_x * 2 * (planes == 3 ? 6 : 1), all_w = slabs_w * (planes == 1 ? 1 : a.x ? 6 : 3);
     f.x_large = large_tiles(a.n, a.dim, all_x);
     f.w_large = large_tiles(m, a.dim, all_w);
@@ -937,7 +948,7 @@ hipError_t launch_gated(const GatedArgs &a, hipStream_t s)
     ProductArgs p = projections(f.gate, f.up, f.x, a.type, false, a.n, a.dim, a.hidden, a.act);
     p.out[0] = a.h;
     p.ld_out[0] = a.ld_h;
-    return product<false, false, kGate>(p, a.type, large_tiles(a.n, 2 * (int64_t)a.hidden, (int64_t)p.products * ((p.k + 63) / 64)), s);
+    return product<false, false, kGate>(p, a.type, large_tiles(a.n, 2 * (int64_t)a.hidden, (int64_t)p.products * ((p.k + kSlab - 1) / kSlab)), s);
 }
 
 uint64_t gated_grad_work(const GatedGradArgs &a) { return plan(a).bytes; }
@@ -964,7 +975,7 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s)
         p.d_plane = f.d_plane;
         p.ld_d = f.n_pad;
         p.n_pad = f.n_pad;
-        TRY_HIP((product<false, false, kGateGrad>(p, a.type, large_tiles(a.n, 2 * (int64_t)a.hidden, (int64_t)p.products * ((p.k + 63) / 64)), s)));
+        TRY_HIP((product<false, false, kGateGrad>(p, a.type, large_tiles(a.n, 2 * (int64_t)a.hidden, (int64_t)p.products * ((p.k + kSlab - 1) / kSlab)), s)));
     }
     if (a.gx && a.n) {
         ProductArgs x{};
