@@ -465,8 +465,12 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
         }
 
         // A lane's place: row j * 16 + lane % 16 of the wave's and, in register e
-        // of block i, column i * 16 + 4 (lane / 16) + e.
-        const int ln = (lane >> 4) * 4, lm = lane & 15;
+        // of block i, column i * 16 + 4 (el / 16) + e.
+        // (The lane is hidden from the compiler, which would keep all addresses of
+        // the end in registers during the products.)
+        int el = lane;
+        asm volatile("" : "+v"(el));
+        const int ln = (el >> 4) * 4, lm = el & 15;
         const int64_t mw = u.m0 + wm;
         const int nw = u.n0 + (kPair ? wn / 2 : wn);
         // Rows of 32 columns of 16 bits, turned through LDS so that a lane moves
@@ -476,14 +480,14 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
         typedef Slot<T, 8> S8;
         auto place = [&](int row, int piece) { return turn + row * 64 + ((piece ^ ((row >> 2) & 3)) << 4); };
         auto mine = [&](int j, int half) {  // this lane's four of a block's half of 16 columns
-            return (typename S4::vec *)(place(j * 16 + lm, half * 2 + (lane >> 5)) + ((lane >> 4) & 1) * 8);
+            return (typename S4::vec *)(place(j * 16 + lm, half * 2 + (el >> 5)) + ((el >> 4) & 1) * 8);
         };
         auto put = [&](int j, int half, f32x4 v) { *mine(j, half) = __builtin_convertvector(v, typename S4::vec); };
         auto store = [&](T *out, int64_t ld, int col, int64_t width) {  // the wave's rows, columns from col on
 #pragma unroll
             for (int r = 0; r < WM / 16; ++r) {
-                const int row = r * 16 + (lane >> 2), c = col + (lane & 3) * 8;
-                const typename S8::vec v = *(const typename S8::vec *)place(row, lane & 3);
+                const int row = r * 16 + (el >> 2), c = col + (el & 3) * 8;
+                const typename S8::vec v = *(const typename S8::vec *)place(row, el & 3);
                 if (mw + row >= a.m) continue;
                 T *to = out + (mw + row) * ld + c;
                 if (c + 8 <= width) S8::store(to, v);
@@ -503,20 +507,20 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
                     if (n + e < a.n) out[m * ld + n + e] = v[e];
         };
         if constexpr (END == kStore) {
-            if (a.parts > 1 || sizeof(O) == 4) {
-                float *out;
-                int64_t ld;
-                if (a.parts > 1) {
-                    out = a.part + ((int64_t)u.part * a.outs + u.which) * a.m * a.n;
-                    ld = a.n;
-                } else {
-                    out = (float *)a.out[u.which];
-                    ld = a.ld_out[u.which];
-                }
+            // 32 bits: a lane's four neighbours as they are
+            auto plain = [&](float *out, int64_t ld) {
 #pragma unroll
                 for (int i = 0; i < NB; ++i)
 #pragma unroll
-                    for (int j = 0; j < MB; ++j) store32(out, ld, j, nw + i * 16 + ln, acc[i][j]);
+                    for (int j = 0; j < MB; ++j) {
+                        store32(out, ld, j, nw + i * 16 + ln, acc[i][j]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+            };
+            if (a.parts > 1) {
+                plain(a.part + ((int64_t)u.part * a.outs + u.which) * a.m * a.n, a.n);
+            } else if constexpr (sizeof(O) == 4) {
+                plain((float *)a.out[u.which], a.ld_out[u.which]);
             } else if constexpr (sizeof(O) == 2) {
 #pragma unroll
                 for (int i = 0; i < NB; i += 2) {
@@ -537,7 +541,7 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
                     // grad_h to the lanes that hold g and u
 #pragma unroll
                     for (int r = 0; r < WM / 16; ++r) {
-                        const int row = r * 16 + (lane >> 2), c = col + (lane & 3) * 8;
+                        const int row = r * 16 + (el >> 2), c = col + (el & 3) * 8;
                         typename S8::vec v = (typename S8::vec)(T)0.f;
                         if (mw + row < a.m) {
                             const T *from = (const T *)a.gh + (mw + row) * a.ld_gh + c;
@@ -546,7 +550,7 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
 #pragma unroll
                                 for (int e = 0; e < 8; ++e) v[e] = c + e < a.n ? from[e] : (T)0.f;
                         }
-                        *(typename S8::vec *)place(row, lane & 3) = v;
+                        *(typename S8::vec *)place(row, el & 3) = v;
                     }
                 }
 #pragma unroll
