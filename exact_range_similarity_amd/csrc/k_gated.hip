@@ -86,17 +86,12 @@ struct ProductArgs {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-// A buffer at `base` whose last bytes lie behind all offsets in use: kOutside
-// is outside of it, and a load from there gives zeros.
-constexpr uint32_t kOutside = 0xffffffffu;
-__device__ __forceinline__ u32x4 buffer_at(const void *base)
-{
-    const uint64_t b = (uint64_t)base;
-    return (u32x4){(uint32_t)b, (uint32_t)(b >> 32) & 0xffffu, 0xfffffff0u, 0x00020000u};
-}
+// An offset that lies outside of every buffer here, also with what is added to
+// it (both below 2^31): a load from outside gives zeros.
+constexpr uint32_t kOutside = 0x80000000u;
 
-// 16 bytes from each lane's offset to LDS, lane by lane from `lds`.
-__device__ __forceinline__ void dma16(uint32_t lds, uint32_t off, u32x4 buffer)
+// 16 bytes from each lane's place in a buffer to LDS, lane by lane from `lds`.
+__device__ __forceinline__ void dma16(uint32_t lds, u32x4 buffer, uint32_t off)
 {
     // the wait state that a write of m0 needs before it is used
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
@@ -152,44 +147,71 @@ __device__ __forceinline__ uint16_t part_of(float &v)
 // 16-byte pieces exchanged by the row so that 16 neighbouring rows cover all
 // banks; across k it holds the tile's ROWS values at one k, its pieces exchanged
 // in pairs by bits 0, 1 and 3 of k.  Either way a wave's reads fall on all banks.
-template <int ROWS, int WAVES, bool ACROSS>
+// PAIR: rows of the slab are 32 of one matrix and 32 of another in turn.
+//
+// A slab is a buffer that begins with its first value, and a lane's loads lie a
+// fixed distance apart.  What is outside the matrix is outside the buffer: rows
+// behind the last of an operand along k and values of k of one across it by the
+// buffer's length, values of k of one along it by the lane's offset.  (Columns
+// of one across k that lie behind the tile's edge are the next row's first: they
+// only meet results that are not written.)
+template <int ROWS, bool ACROSS, bool PAIR>
 struct Side {
     static constexpr int kBytes = ROWS * kSlab * 2;
-    static constexpr int kLoads = kBytes / (WAVES * 64 * 16);
+    static constexpr int kLoads = kBytes / 4096;                   // of each of four waves
     static constexpr int kPieces = ACROSS ? ROWS / 8 : kSlab / 8;  // of a row of LDS
     static constexpr int kLoadRows = 64 / kPieces;                 // rows of LDS that a wave's load fills
-    uint32_t off[kLoads];
-    int piece;  // along k: the lane's piece
+    uint32_t off[2];  // of even and odd loads
+    int piece;
 
     static __device__ __forceinline__ int exchange(int row)
     {
         return ACROSS ? (row & 3) << 1 | (row & 8) : (row >> 1) & 7;
     }
 
-    // `room`: rows (along k) or columns (across k) from the tile's first that may be read
-    __device__ __forceinline__ void init(int wave, int64_t ld, int room)
+    __device__ __forceinline__ void init(int wave, int64_t ld)
     {
-        const int lane = threadIdx.x & 63, r = lane / kPieces;
+        const int lane = threadIdx.x & 63;
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            const int row = (j * WAVES + wave) * kLoadRows + r;
-            if constexpr (ACROSS) {
-                int c = (lane % kPieces) ^ exchange(row);
-                c = c * 8 < room ? c : 0;
-                off[j] = (uint32_t)(row * (int)ld + c * 8) * 2;
-            } else {
-                piece = (lane % kPieces) ^ exchange(row);
-                off[j] = (uint32_t)((row < room ? row : room - 1) * (int)ld + piece * 8) * 2;
-            }
+        for (int odd = 0; odd < 2; ++odd) {
+            // a wave's first load, but exchanged like its second
+            const int row = wave * kLoadRows + lane / kPieces;
+            piece = (lane % kPieces) ^ exchange(row + odd * 4 * kLoadRows);
+            off[odd] = (uint32_t)(row * (int)ld + piece * 8) * 2;
         }
     }
 
-    // Load j of a slab, of which the first `left` values of k exist.  (Without a
-    // branch, so that a slab's loads fit between the products.)
-    __device__ __forceinline__ void load(int j, int wave, uint32_t lds, int left, u32x4 buffer) const
+    // Bytes from one load of a lane to the next but `PAIR`'s, which come in twos.
+    static __device__ __forceinline__ uint32_t distance(int j, int64_t ld)
     {
-        const int k = ACROSS ? (j * WAVES + wave) * kLoadRows + (int)(threadIdx.x & 63) / kPieces : piece * 8;
-        dma16(lds + (j * WAVES + wave) * 1024, k < left ? off[j] : kOutside, buffer);
+        return (uint32_t)((PAIR ? j >> 1 : j) * 4 * kLoadRows * (int)ld) * 2;
+    }
+
+    // The buffer of a slab at `base`: `room` rows (along k) or columns (across
+    // it) from the tile's first on and `left` values of k exist.
+    static __device__ __forceinline__ u32x4 buffer(const uint16_t *base, int64_t ld, int room, int left)
+    {
+        const uint64_t b = (uint64_t)base;
+        return (u32x4){(uint32_t)b, (uint32_t)(b >> 32) & 0xffffu, length(ld, room, left), 0x00020000u};
+    }
+    static __device__ __forceinline__ uint32_t length(int64_t ld, int room, int left)
+    {
+        if (!ACROSS) return (uint32_t)((room < ROWS ? room : ROWS) * (int)ld) * 2;
+        return (uint32_t)(((left < kSlab + 1 ? left : kSlab + 1) - 1) * (int)ld + room) * 2;
+    }
+    // To the next slab; `left`: of that.
+    static __device__ __forceinline__ void move(u32x4 &b, int64_t ld, int room, int left)
+    {
+        const uint64_t to = ((uint64_t)b[1] << 32 | b[0]) + kSlab * 2 * (ACROSS ? (uint32_t)ld : 1u);
+        b[0] = (uint32_t)to;
+        b[1] = (uint32_t)(to >> 32);
+        if (ACROSS) b[2] = length(ld, room, left);
+    }
+
+    // A lane's offset in load j of a slab.
+    __device__ __forceinline__ uint32_t offset(int j, int64_t ld, int left) const
+    {
+        return (ACROSS || piece * 8 < left ? off[j & 1] : kOutside) + distance(j, ld);
     }
 
     // Values of 8 consecutive k for 16 consecutive rows from `row` (a multiple
@@ -292,8 +314,8 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
     constexpr bool kPair = END != kStore;  // P's rows alternate between the two weights
     constexpr int CN = kPair ? BN / 2 : BN;
     constexpr bool FAST = sizeof(O) == 2;
-    typedef Side<BN, WAVES, PA> P;
-    typedef Side<BM, WAVES, QA> Q;
+    typedef Side<BN, PA, kPair> P;
+    typedef Side<BM, QA, false> Q;
     constexpr int STAGE = P::kBytes + Q::kBytes;
     constexpr int kTurn = sizeof(O) == 2 ? WM * 64 : 0;  // a wave's room to turn 32 columns of its results
     __shared__ __align__(1024) char lds[kStages * STAGE + WAVES * kTurn];
@@ -326,76 +348,54 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
         return u;
     };
 
-    // The loads run up to two slabs ahead of the products, across units.
+    // The loads run up to two slabs ahead of the products, across units: where
+    // the next slab lies, how much of k it has, and how many more slabs follow it
+    // side by side.  Most turns only move on.
     P p;
     Q q;
+    p.init(wave, a.ld_p);
+    q.init(wave, a.ld_q);
     Unit lu = decode(unit);
-    int lunit = unit, pos = lu.first, left = 0;
-    bool edge = false;  // the offsets are those of a tile at the block's edge
-    auto offsets = [&]() {
-        p.init(wave, a.ld_p, PA ? a.n_room - lu.n0 : a.n - lu.n0);
-        if constexpr (kPair) {
-            // row r of the slab is row n0 + (r / 64) * 32 + r % 32 of Wg (r / 32 even) or Wu
-            const int r = lane / P::kPieces;
-#pragma unroll
-            for (int j = 0; j < P::kLoads; ++j) {
-                const int row = (j * WAVES + wave) * P::kLoadRows + r;
-                const int of = (row >> 6) * 32 + (row & 31);
-                p.off[j] = (uint32_t)((of < a.n - lu.n0 ? of : a.n - lu.n0 - 1) * (int)a.ld_p + p.piece * 8) * 2;
-            }
-        }
-        const int64_t room = (QA ? a.m_room : a.m) - lu.m0;
-        q.init(wave, a.ld_q, room < BM ? (int)room : BM);
-        edge = lu.n0 + CN > a.n || lu.m0 + BM > a.m;
-    };
-    offsets();
-    // Where the next slab lies, how much of k it has, and how many more slabs
-    // follow it side by side: most turns only move on.
+    int lunit = unit, pos = lu.first, left = 0, run = 0, p_room = 0, q_room = 0;
     u32x4 pb0 = (u32x4)0u, pb1 = (u32x4)0u, qb = (u32x4)0u;
-    int run = 0;
-    auto move = [](u32x4 &b, uint32_t by) {
-        const uint64_t to = ((uint64_t)b[1] << 32 | b[0]) + by;
-        b[0] = (uint32_t)to;
-        b[1] = (uint32_t)(to >> 32);
-    };
-    const uint32_t p_step = kSlab * 2 * (PA ? (uint32_t)a.ld_p : 1u), q_step = kSlab * 2 * (QA ? (uint32_t)a.ld_q : 1u);
     auto next_slab = [&]() {
         if (--run > 0) {
-            move(pb0, p_step);
-            if constexpr (kPair) move(pb1, p_step);
-            move(qb, q_step);
             left -= kSlab;
+            P::move(pb0, a.ld_p, p_room, left);
+            if constexpr (kPair) P::move(pb1, a.ld_p, p_room, left);
+            Q::move(qb, a.ld_q, q_room, left);
             return;
         }
         if (pos == lu.last) {
             lunit += stride;
-            if (lunit >= end) {  // there is none: zeros are loaded and not read
+            if (lunit >= end) {  // there is none: what is loaded now is not read
                 lunit = end;
-                left = 0;
+                pb0[2] = pb1[2] = qb[2] = 0;
                 return;
             }
             lu = decode(lunit);
             pos = lu.first;
-            if (edge || lu.n0 + CN > a.n || lu.m0 + BM > a.m) offsets();
         }
         const int seg = a.by_slabs(pos), at = pos - seg * a.slabs, k0 = at * kSlab;
         const int src = seg >= a.products, prod = seg - src * a.products;
         const int64_t po = ((a.p_planes >> (4 * prod)) & 15) * a.p_plane +
                            (PA ? (int64_t)k0 * a.ld_p + lu.n0 : (int64_t)lu.n0 * a.ld_p + k0);
-        pb0 = buffer_at(a.p[kPair ? 0 : src] + po);
-        if constexpr (kPair) pb1 = buffer_at(a.p[1] + po);
-        qb = buffer_at(a.q[a.outs == 2 ? lu.which : src] + ((a.q_planes >> (4 * prod)) & 15) * a.q_plane +
-                       (QA ? (int64_t)k0 * a.ld_q + lu.m0 : lu.m0 * a.ld_q + k0));
+        const int64_t qo = ((a.q_planes >> (4 * prod)) & 15) * a.q_plane +
+                           (QA ? (int64_t)k0 * a.ld_q + lu.m0 : lu.m0 * a.ld_q + k0);
         left = a.k - k0;
+        p_room = (PA ? a.n_room : a.n) - lu.n0;
+        q_room = (int)((QA ? a.m_room : a.m) - lu.m0);
+        pb0 = P::buffer(a.p[kPair ? 0 : src] + po, a.ld_p, p_room, left);
+        if constexpr (kPair) pb1 = P::buffer(a.p[1] + po, a.ld_p, p_room, left);
+        qb = Q::buffer(a.q[a.outs == 2 ? lu.which : src] + qo, a.ld_q, q_room, left);
         run = a.slabs - at < lu.last - pos ? a.slabs - at : lu.last - pos;
         pos += run;
     };
     constexpr int kLoads = P::kLoads + Q::kLoads;
     auto load = [&](int l, uint32_t at) {  // load l of the slab
-        if (l < P::kLoads)
-            p.load(l, wave, at, left, kPair && (((l * WAVES + wave) * P::kLoadRows) & 32) ? pb1 : pb0);
-        else
-            q.load(l - P::kLoads, wave, at + P::kBytes, left, qb);
+        const uint32_t to = at + wave * 1024 + l * 4096;
+        if (l < P::kLoads) dma16(to, kPair && (l & 1) ? pb1 : pb0, p.offset(l, a.ld_p, left));
+        else dma16(to, qb, q.offset(l - P::kLoads, a.ld_q, left));
     };
 
     const int wn = (wave & 1) * WN, wm = (wave >> 1) * WM;
@@ -744,7 +744,8 @@ struct Room {
 };
 
 // In place where the loads can take it: 16-bit values, rows that begin at 16
-// bytes and hold whole pieces of 16 bytes, spaced so that a tile's offsets fit 32 bits.
+// bytes and hold whole pieces of 16 bytes, spaced so that a tile's offsets stay
+// below 2^31 bytes.
 Operand operand(Room &room, const void *p, int type, int64_t n, int dim, int64_t ld)
 {
     Operand o;
