@@ -140,6 +140,15 @@ int check_norm_grad(const void *d_grad_y, int64_t ld_grad_y, int32_t type, int64
 
 constexpr int64_t kMaxGatedRows = (int64_t)1 << 30;
 
+// A result of the gated block's kernels: a tile's offsets stay below 2^31 bytes.
+int check_gated_out(const void *p, int32_t type, int64_t ld, int32_t dim, bool used, const char *what)
+{
+    const int r = check_tensor(p, type, ld, dim, used, what);
+    if (r != ERSJ_OK) return r;
+    if (ld >= (int64_t)1 << 21) return refuse("%s: row spacing %lld must be below 2^21", what, (long long)ld);
+    return ERSJ_OK;
+}
+
 int check_gated(int32_t type, int64_t n, int32_t dim, const void *d_gate, int64_t ld_gate, const void *d_up,
                 int64_t ld_up, int32_t hidden, int32_t act)
 {
@@ -422,7 +431,7 @@ int ersj_gated(const void *d_x, int32_t type, int64_t n, int32_t dim, int64_t ld
 {
     TRY(check_gated(type, n, dim, d_gate, ld_gate, d_up, ld_up, hidden, activation));
     TRY(check_tensor(d_x, type, ld_x, dim, n > 0, "x"));
-    TRY(check_tensor(d_h, type, ld_h, hidden, n > 0, "h"));
+    TRY(check_gated_out(d_h, type, ld_h, hidden, n > 0, "h"));
     const GatedArgs a{d_x, type, n, dim, ld_x, d_gate, ld_gate, d_up, ld_up, hidden, activation, d_h, ld_h, d_work};
     TRY(check_work(d_work, d_work_bytes, gated_work(a), 256));
     return done(launch_gated(a, (hipStream_t)stream), "gated block kernels");
@@ -465,9 +474,9 @@ int ersj_gated_grad(const void *d_grad_h, int64_t ld_grad_h, const void *d_x, in
     if (d_x && (d_codes || d_scales)) return refuse("x and rows held in 8 bits are both given");
     if (d_x || !(d_codes || d_scales)) TRY(check_tensor(d_x, type, ld_x, dim, n > 0, "x"));
     else TRY(check_packed(d_codes, d_scales, n, dim));
-    TRY(check_tensor(d_grad_x, type, ld_grad_x, dim, false, "grad_x"));
-    TRY(check_tensor(d_grad_gate, type, ld_grad_gate, dim, false, "grad_gate"));
-    TRY(check_tensor(d_grad_up, type, ld_grad_up, dim, false, "grad_up"));
+    TRY(check_gated_out(d_grad_x, type, ld_grad_x, dim, false, "grad_x"));
+    TRY(check_gated_out(d_grad_gate, type, ld_grad_gate, dim, false, "grad_gate"));
+    TRY(check_gated_out(d_grad_up, type, ld_grad_up, dim, false, "grad_up"));
     const GatedGradArgs a{d_grad_h, ld_grad_h, d_x, d_codes, d_scales, type, n, dim, ld_x, d_gate, ld_gate, d_up,
                           ld_up, hidden, activation, d_grad_x, ld_grad_x, d_grad_gate, d_grad_up, ld_grad_gate,
                           ld_grad_up, d_work};

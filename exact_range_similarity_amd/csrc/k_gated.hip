@@ -399,12 +399,6 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
     };
 
     const int wn = (wave & 1) * WN, wm = (wave >> 1) * WM;
-    f32x4 acc[NB][MB];
-#pragma unroll
-    for (int i = 0; i < NB; ++i)
-#pragma unroll
-        for (int j = 0; j < MB; ++j) acc[i][j] = (f32x4)0.f;
-
     // kStages slabs are in LDS or on their way.  A slab's steps each multiply
     // what the step before read from LDS and read what the next one multiplies;
     // the last step begins with the slab's only barrier, behind which the next
@@ -434,6 +428,11 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
     int buf = 0;
     for (; unit < end; unit += stride) {
         const Unit u = decode(unit);
+        f32x4 acc[NB][MB];
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int j = 0; j < MB; ++j) acc[i][j] = (f32x4)0.f;
         for (int t = u.first; t < u.last; ++t) {
             const char *at = lds + buf * STAGE;
             const uint32_t free = lds0 + buf * STAGE;
@@ -497,30 +496,43 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
                         if (c + e < width) to[e] = v[e];
             }
         };
-        auto store32 = [&](float *out, int64_t ld, int j, int n, f32x4 v) {  // a lane's four of 32 bits as they are
-            const int64_t m = mw + j * 16 + lm;
-            if (m >= a.m) return;
-            if (n + 3 < a.n) Slot<float, 4>::store(out + m * ld + n, v);
+        // 32 bits: a lane's four neighbours as they are, at offsets in a buffer that
+        // ends with the tile's last row (few registers for addresses, unlike pointers)
+        const bool whole = u.n0 + CN <= a.n;
+        __amdgpu_buffer_rsrc_t out32;
+        uint32_t at32 = 0, step32 = 0;
+        auto open32 = [&](float *out, int64_t ld) {
+            const int rows = a.m - u.m0 < BM ? (int)(a.m - u.m0) : BM;
+            out32 = __builtin_amdgcn_make_buffer_rsrc(out + u.m0 * ld + u.n0, 0, rows * (int)ld * 4, 0x00020000);
+            step32 = (uint32_t)(int)ld * 64;  // 16 rows
+            at32 = (uint32_t)((wm + lm) * (int)ld + (nw - u.n0) + ln) * 4;
+        };
+        auto store32 = [&](int j, int col, f32x4 v) {
+            const uint32_t off = at32 + j * step32 + col * 4;
+            const auto words = __builtin_bit_cast(u32x4, v);
+            if (whole) __builtin_amdgcn_raw_buffer_store_b128(words, out32, off, 0, 0);
             else
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (n + e < a.n) out[m * ld + n + e] = v[e];
+                    __builtin_amdgcn_raw_buffer_store_b32(words[e], out32,
+                                                          nw + ln + col + e < a.n ? off + 4 * e : kOutside, 0, 0);
+        };
+        // 32 bits: a sum leaves its accumulation register where it is stored, and not before
+        auto take = [](f32x4 v) {
+            if constexpr (sizeof(O) == 4) asm volatile("" : "+v"(v));
+            return v;
         };
         if constexpr (END == kStore) {
-            // 32 bits: a lane's four neighbours as they are
-            auto plain = [&](float *out, int64_t ld) {
+            if (a.parts > 1 || sizeof(O) == 4) {
+                if (a.parts > 1) open32(a.part + ((int64_t)u.part * a.outs + u.which) * a.m * a.n, a.n);
+                else open32((float *)a.out[u.which], a.ld_out[u.which]);
 #pragma unroll
                 for (int i = 0; i < NB; ++i)
 #pragma unroll
                     for (int j = 0; j < MB; ++j) {
-                        store32(out, ld, j, nw + i * 16 + ln, acc[i][j]);
+                        store32(j, i * 16, take(acc[i][j]));
                         __builtin_amdgcn_sched_barrier(0);
                     }
-            };
-            if (a.parts > 1) {
-                plain(a.part + ((int64_t)u.part * a.outs + u.which) * a.m * a.n, a.n);
-            } else if constexpr (sizeof(O) == 4) {
-                plain((float *)a.out[u.which], a.ld_out[u.which]);
             } else if constexpr (sizeof(O) == 2) {
 #pragma unroll
                 for (int i = 0; i < NB; i += 2) {
@@ -534,6 +546,7 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
             }
         } else {
             // blocks i and i + 1 hold g, the two after them u
+            if constexpr (END == kGate && sizeof(O) == 4) open32((float *)a.out[0], a.ld_out[0]);
 #pragma unroll
             for (int i = 0; i < NB; i += 4) {
                 const int col = nw + i * 8;
@@ -572,7 +585,7 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             if constexpr (sizeof(O) == 2) put(j, half, h[half]);
-                            else store32((float *)a.out[0], a.ld_out[0], j, col + half * 16 + ln, h[half]);
+                            else store32(j, i * 8 + half * 16, h[half]);
                         }
                     } else {
                         // g and u give way to dg and du
@@ -647,10 +660,6 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
                 }
             }
         }
-#pragma unroll
-        for (int i = 0; i < NB; ++i)
-#pragma unroll
-            for (int j = 0; j < MB; ++j) acc[i][j] = (f32x4)0.f;
     }
 }
 

@@ -174,7 +174,7 @@ uint64_t ersj_layer_norm_grad_packed_work(int32_t type, int64_t n, int32_t dim);
  *  activation     : ERSJ_SILU: g / (1 + exp(-g)); ERSJ_GELU: g Phi(g), Phi the
  *                   normal distribution; ERSJ_GELU_TANH: g / 2 * (1 +
  *                   tanh(sqrt(2 / pi) * (g + 0.044715 g^3))).
- *  d_h            : device [n][ld_h] of type.
+ *  d_h            : device [n][ld_h] of type, ld_h < 2^21.
  *  d_work         : at least ersj_gated_work(...) bytes, aligned to 256; it
  *                   takes the arguments of the call, looks at the addresses'
  *                   alignment alone, and gives 0 where none is needed.
@@ -198,6 +198,7 @@ uint64_t ersj_gated_work(const void *d_x, int32_t type, int64_t n, int32_t dim, 
  *  d_codes, d_scales : its rows held in 8 bits.
  *  d_grad_x          : device [n][ld_grad_x] of type; NULL: not wanted.
  *  d_grad_gate, d_grad_up : device [hidden][ld_*] of type; NULL: not wanted.
+ *                      The three's spacings are below 2^21.
  *  d_work            : at least ersj_gated_grad_work(...) bytes, aligned to
  *                      256; want_*: whether that gradient is wanted.
  * dg and du are rounded to the 16-bit type that they are multiplied in (32-bit
