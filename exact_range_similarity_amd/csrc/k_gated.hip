@@ -36,7 +36,7 @@ typedef bf16_t bf16x8 __attribute__((ext_vector_type(8)));
 // one plane, three of both operands, three of one of them.
 constexpr uint32_t kPlanes6P = 0x010201, kPlanes6Q = 0x001021, kPlanes3 = 0x012;
 
-constexpr int kSlab = 64, kSteps = kSlab / 32, kStages = 2;
+constexpr int kSlab = 64, kSteps = kSlab / 32;
 
 enum { kStore, kGate, kGateGrad };
 
@@ -166,7 +166,8 @@ struct Side {
 
     static __device__ __forceinline__ int exchange(int row)
     {
-        return ACROSS ? (row & 3) << 1 | (row & 8) : (row >> 1) & 7;
+        if (!ACROSS) return (row >> 1) & 7;
+        return ROWS == 64 ? (row & 2) | (row & 8) >> 1 : (row & 3) << 1 | (row & 8);
     }
 
     __device__ __forceinline__ void init(int wave, int64_t ld)
@@ -307,10 +308,12 @@ struct Unit {
 };
 
 // T: the 16-bit type multiplied; O: the tensors' type.
-template <typename T, typename O, int BM, int BN, bool PA, bool QA, int END>
-__global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs a)
+template <typename T, typename O, int BM, int kStages, bool PA, bool QA, int END>
+__global__ __launch_bounds__(256, BM == 256 || kStages * BM > 256 ? 1 : 2) void k_product(ProductArgs a)
 {
-    constexpr int WAVES = 4, WM = BM / 2, WN = BN / 2, MB = WM / 16, NB = WN / 16;
+    constexpr int BN = BM, WAVES = 4;
+    // waves two by two; in the smallest tile one above the other, so that each has g and u of its places
+    constexpr int WM = BM == 64 ? 16 : BM / 2, WN = BM == 64 ? 64 : BN / 2, MB = WM / 16, NB = WN / 16;
     constexpr bool kPair = END != kStore;  // P's rows alternate between the two weights
     constexpr int CN = kPair ? BN / 2 : BN;
     constexpr bool FAST = sizeof(O) == 2;
@@ -398,7 +401,7 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
         else dma16(to, qb, q.offset(l - P::kLoads, a.ld_q, left));
     };
 
-    const int wn = (wave & 1) * WN, wm = (wave >> 1) * WM;
+    const int wn = BM == 64 ? 0 : (wave & 1) * WN, wm = (BM == 64 ? wave : wave >> 1) * WM;
     // kStages slabs are in LDS or on their way.  A slab's steps each multiply
     // what the step before read from LDS and read what the next one multiplies;
     // the last step begins with the slab's only barrier, behind which the next
@@ -419,10 +422,34 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
 #pragma unroll
         for (int l = 0; l < kLoads; ++l) load(l, lds0 + b * STAGE);
     }
-    wait_loads<kLoads>();
+    wait_loads<(kStages - 1) * kLoads>();
     barrier();
 #pragma unroll
     for (int r = 0; r < kReads; ++r) read(0, r, lds, 0);
+
+    typedef Slot<T, 4> S4;
+    typedef Slot<T, 8> S8;
+    auto grad_row = [&](int64_t m, int c) {  // eight values of grad_h, zeros outside
+        typename S8::vec v = (typename S8::vec)(T)0.f;
+        if (m < a.m) {
+            const T *from = (const T *)a.gh + m * a.ld_gh + c;
+            if (c + 8 <= a.n) v = S8::load(from);
+            else
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = c + e < a.n ? from[e] : (T)0.f;
+        }
+        return v;
+    };
+    // loads of grad_h ahead of a unit's products, and a lower bound on what a
+    // tile inside the block issues after the loads of its last slabs: its results'
+    // stores and the next unit's loads of grad_h (at most what the counter holds)
+    constexpr int kAhead = END == kGateGrad && sizeof(O) == 2 && BM < 256 ? WM / 16 : 0;
+    constexpr int kStores = sizeof(O) == 4 ? (END == kStore ? kCells : END == kGate ? kCells / 2 : 0)
+                            : END == kGate ? NB / 4 * (WM / 16) : NB / 2 * (WM / 16);
+    // (not in the large tile, whose long sums hide that wait: forward of 8192 x
+    // 4096 x 11008 1220 us, 1240 with it, for the registers that it takes)
+    constexpr int kSince = BM == 256 ? 0 : kStores + kAhead < 40 ? kStores + kAhead : 40;
+    bool before = false;  // the unit before lay inside the block
 
     char *turn = lds + kStages * STAGE + wave * kTurn;
     int buf = 0;
@@ -433,6 +460,19 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
         for (int i = 0; i < NB; ++i)
 #pragma unroll
             for (int j = 0; j < MB; ++j) acc[i][j] = (f32x4)0.f;
+        const int64_t mw = u.m0 + wm;
+        const int nw = u.n0 + (kPair ? wn / 2 : wn);
+        // grad_h comes while the products are formed, a row's 32 columns over four
+        // lanes; the large tile has no registers for it, and less need
+        const bool inner = u.m0 + BM <= a.m && u.n0 + CN <= a.n;
+        typename S8::vec dh[kAhead ? kAhead : 1];
+        if constexpr (kAhead > 0) {
+#pragma unroll
+            for (int r = 0; r < kAhead; ++r) dh[r] = grad_row(mw + r * 16 + (lane >> 2), nw + (lane & 3) * 8);
+        }
+        // What was issued after the first slab's loads, in order, need not be waited for with them.
+        const bool calm = inner && before;
+        before = inner;
         for (int t = u.first; t < u.last; ++t) {
             const char *at = lds + buf * STAGE;
             const uint32_t free = lds0 + buf * STAGE;
@@ -443,7 +483,10 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
                 if (kk == kSteps - 1) {
                     next_slab();
                     // this wave's loads of the next slab, and its reads of this one
-                    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+                    if (kSince > 0 && calm && t == u.first)
+                        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kStages - 2) * kLoads + kSince) : "memory");
+                    else
+                        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kStages - 2) * kLoads) : "memory");
                     barrier();
                 }
                 __builtin_amdgcn_sched_barrier(0);
@@ -470,19 +513,19 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
         int el = lane;
         asm volatile("" : "+v"(el));
         const int ln = (el >> 4) * 4, lm = el & 15;
-        const int64_t mw = u.m0 + wm;
-        const int nw = u.n0 + (kPair ? wn / 2 : wn);
         // Rows of 32 columns of 16 bits, turned through LDS so that a lane moves
         // 16 bytes and four lanes a row; pieces of 16 bytes are exchanged by the
         // row, so that all banks take part.
-        typedef Slot<T, 4> S4;
-        typedef Slot<T, 8> S8;
         auto place = [&](int row, int piece) { return turn + row * 64 + ((piece ^ ((row >> 2) & 3)) << 4); };
         auto mine = [&](int j, int half) {  // this lane's four of a block's half of 16 columns
             return (typename S4::vec *)(place(j * 16 + lm, half * 2 + (el >> 5)) + ((el >> 4) & 1) * 8);
         };
         auto put = [&](int j, int half, f32x4 v) { *mine(j, half) = __builtin_convertvector(v, typename S4::vec); };
+        // What a lane writes there another reads, within a wave and in vectors of
+        // another length: nothing is moved across these places.
+        auto turned = []() { asm volatile("" ::: "memory"); };
         auto store = [&](T *out, int64_t ld, int col, int64_t width) {  // the wave's rows, columns from col on
+            turned();
 #pragma unroll
             for (int r = 0; r < WM / 16; ++r) {
                 const int row = r * 16 + (el >> 2), c = col + (el & 3) * 8;
@@ -495,6 +538,7 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
                     for (int e = 0; e < 8; ++e)
                         if (c + e < width) to[e] = v[e];
             }
+            turned();
         };
         // 32 bits: a lane's four neighbours as they are, at offsets in a buffer that
         // ends with the tile's last row (few registers for addresses, unlike pointers)
@@ -553,18 +597,10 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
                 if constexpr (END == kGateGrad && sizeof(O) == 2) {
                     // grad_h to the lanes that hold g and u
 #pragma unroll
-                    for (int r = 0; r < WM / 16; ++r) {
-                        const int row = r * 16 + (el >> 2), c = col + (el & 3) * 8;
-                        typename S8::vec v = (typename S8::vec)(T)0.f;
-                        if (mw + row < a.m) {
-                            const T *from = (const T *)a.gh + (mw + row) * a.ld_gh + c;
-                            if (c + 8 <= a.n) v = S8::load(from);
-                            else
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) v[e] = c + e < a.n ? from[e] : (T)0.f;
-                        }
-                        *(typename S8::vec *)place(row, el & 3) = v;
-                    }
+                    for (int r = 0; r < WM / 16; ++r)
+                        *(typename S8::vec *)place(r * 16 + (el >> 2), el & 3) =
+                            kAhead ? dh[kAhead ? r : 0] : grad_row(mw + r * 16 + (el >> 2), col + (el & 3) * 8);
+                    turned();
                 }
 #pragma unroll
                 for (int j = 0; j < MB; ++j) {
@@ -622,6 +658,7 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_product(ProductArgs 
                 __builtin_amdgcn_sched_barrier(0);
                 if constexpr (sizeof(O) == 2) {
                     if constexpr (END == kGateGrad) {
+                        turned();
                         // zeros behind the block's columns come from the zeros in the place of grad_h
 #pragma unroll
                         for (int of = 0; of < 2; ++of) {
@@ -671,43 +708,71 @@ __global__ __launch_bounds__(256) void k_zero(O *out, int64_t ld, int m, int n)
         for (int c = threadIdx.x; c < n; c += 256) out[r * ld + c] = (O)0.f;
 }
 
-// Sums of the parts of a product, in order.
+// Sums of the parts of a product, in order, eight of them on their way at a
+// time.  (Only products of few tiles have parts: m n is below 2^23.)
 template <typename O>
-__global__ __launch_bounds__(256) void k_product_join(const float *part, int parts, int outs, int m, int n, O *out0,
-                                                      O *out1, int64_t ld0, int64_t ld1)
+__global__ __launch_bounds__(256) void k_product_join(const float *part, int parts, int m, int n, int all, Divide by_n,
+                                                      O *out0, O *out1, int64_t ld0, int64_t ld1)
 {
-    const int64_t size = (int64_t)m * n, all = size * outs;
-    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < all; i += (int64_t)gridDim.x * 1024) {
-        const int len = all - i < 4 ? (int)(all - i) : 4;
-        f32x4 v = (f32x4)0.f;
-        for (int p = 0; p < parts; ++p) {
-            const float *at = part + p * all + i;
-            if (len == 4) v += Slot<float, 4>::load(at);
-            else
-                for (int e = 0; e < len; ++e) v[e] += at[e];
+    const int i = (blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= all) return;
+    f32x4 v = (f32x4)0.f;
+    if (i + 4 <= all) {
+        for (int p = 0; p < parts; p += 8) {
+            f32x4 x[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                x[u] = Slot<float, 4>::load(part + (int64_t)(p + u < parts ? p + u : parts - 1) * all + i);
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (p + u < parts) v += x[u];
         }
-        for (int e = 0; e < len; ++e) {
-            const int64_t w = i + e >= size, r = i + e - w * size, row = r / n;
-            (w ? out1 : out0)[row * (w ? ld1 : ld0) + r - row * n] = (O)v[e];
+    } else {
+        for (int p = 0; p < parts; ++p)
+            for (int e = 0; e < all - i; ++e) v[e] += part[(int64_t)p * all + i + e];
+    }
+    int row = by_n(i), col = i - row * n;
+    if (col + 4 <= n) {
+        O *to = row < m ? out0 + row * ld0 : out1 + (row - m) * ld1;
+        Slot<O, 4>::store(to + col, __builtin_convertvector(v, typename Slot<O, 4>::vec));
+        return;
+    }
+    for (int e = 0; e < 4 && i + e < all; ++e, ++col) {
+        while (col >= n) {
+            col -= n;
+            ++row;
         }
+        (row < m ? out0 + row * ld0 : out1 + (row - m) * ld1)[col] = (O)v[e];
     }
 }
 
-// A matrix [n][dim] as the products read it: 16-bit values with rows of `pad`
+// Matrices [n][dim] as the products read them: 16-bit values with rows of `pad`
 // (a multiple of 8) and zeros behind the row's end; three planes for 32 bits.
+struct Lay {
+    const void *src;
+    int64_t ld, n;
+    int dim, pad;
+    uint16_t *out;
+};
+struct Lays {
+    Lay m[3];
+};
 template <typename S>
-__global__ __launch_bounds__(256) void k_lay(const S *src, int64_t ld, int64_t n, int dim, int pad, uint16_t *out)
+__global__ __launch_bounds__(256) void k_lay(Lays l)
 {
-    const int per = pad / 8;
-    const int64_t all = n * per;
+    const Lay a = l.m[blockIdx.y];
+    const int per = a.pad / 8;
+    const int64_t all = a.n * per;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / per;
+        const int64_t r = all < (int64_t)1 << 32 ? (int64_t)((uint32_t)i / (uint32_t)per) : i / per;
         const int c = (int)(i - r * per) * 8;
+        const S *src = (const S *)a.src + r * a.ld + c;
         typename Slot<S, 8>::vec v;
-        if (c + 8 <= dim) v = Slot<S, 8>::load(src + r * ld + c);
+        if (c + 8 <= a.dim) v = Slot<S, 8>::load(src);
         else
-            for (int e = 0; e < 8; ++e) v[e] = c + e < dim ? src[r * ld + c + e] : (S)0.f;
-        uint16_t *to = out + r * pad + c;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = c + e < a.dim ? src[e] : (S)0.f;
+        uint16_t *to = a.out + r * a.pad + c;
         if constexpr (sizeof(S) == 2) {
             *(typename Slot<S, 8>::vec *)to = v;
         } else {
@@ -720,7 +785,7 @@ __global__ __launch_bounds__(256) void k_lay(const S *src, int64_t ld, int64_t n
                     x[e] = (short)part_of(f);
                     v[e] = f;
                 }
-                *(s16x8 *)(to + k * n * pad) = x;
+                *(s16x8 *)(to + k * a.n * a.pad) = x;
             }
         }
     }
@@ -746,7 +811,7 @@ struct Room {
     uint64_t used = 0;
     void *take(uint64_t bytes)
     {
-        char *at = base + used;
+        void *at = (void *)((uintptr_t)base + used);
         used += (bytes + 255) & ~(uint64_t)255;
         return at;
     }
@@ -771,23 +836,38 @@ Operand operand(Room &room, const void *p, int type, int64_t n, int dim, int64_t
     return o;
 }
 
-hipError_t lay(const Operand &o, const void *src, int type, int64_t n, int dim, int64_t ld, hipStream_t s)
-{
-    if (!o.laid || n == 0) return hipSuccess;
-    const unsigned blocks = blocks_for(n * (o.ld / 8));
-    uint16_t *out = const_cast<uint16_t *>(o.p);
-    if (type == kF32) k_lay<float><<<blocks, 256, 0, s>>>((const float *)src, ld, n, dim, (int)o.ld, out);
-    else k_lay<f16_t><<<blocks, 256, 0, s>>>((const f16_t *)src, ld, n, dim, (int)o.ld, out);
-    return hipGetLastError();
-}
+// Lays out those of the matrices that are not read in place.
+struct Layer {
+    Lays l;
+    int count = 0;
+    int64_t most = 0;
+    void add(const Operand &o, const void *src, int64_t n, int dim, int64_t ld)
+    {
+        if (!o.laid || !src) return;
+        l.m[count++] = Lay{src, ld, n, dim, (int)o.ld, const_cast<uint16_t *>(o.p)};
+        if (n * (o.ld / 8) > most) most = n * (o.ld / 8);
+    }
+    hipError_t run(int type, hipStream_t s) const
+    {
+        if (!count) return hipSuccess;
+        const dim3 blocks(blocks_for(most), count);
+        if (type == kF32) k_lay<float><<<blocks, 256, 0, s>>>(l);
+        else k_lay<f16_t><<<blocks, 256, 0, s>>>(l);
+        return hipGetLastError();
+    }
+};
+
+// Tiles of a product, by their edge and the slabs that are in LDS or on their way.
+enum Tile { kTile64, kTile128, kTile128Deep, kTile256 };
+constexpr int edge_of(Tile t) { return t == kTile64 ? 64 : t == kTile256 ? 256 : 128; }
 
 template <typename T, typename O, bool PA, bool QA, int END>
-hipError_t run_product(ProductArgs &a, bool large, hipStream_t s)
+hipError_t run_product(ProductArgs &a, Tile tile, hipStream_t s)
 {
-    // that end's code for 32 bits is too long for the large tile
-    constexpr bool kLarge = !(END == kGateGrad && sizeof(O) == 4);
-    large = large && kLarge;
-    const int bm = large ? 256 : 128, bn = (large ? 256 : 128) / (END == kStore ? 1 : 2);
+    // that end's code for 32 bits is too long for the large tile; only projections take the deep one
+    constexpr bool kLarge = !(END == kGateGrad && sizeof(O) == 4), kDeep = END != kStore;
+    if (tile == kTile256 && !kLarge) tile = kTile128;
+    const int bm = edge_of(tile), bn = bm / (END == kStore ? 1 : 2);
     a.mt = (a.m + bm - 1) / bm;
     a.nt = (a.n + bn - 1) / bn;
     a.slabs = (a.k + kSlab - 1) / kSlab;
@@ -802,40 +882,62 @@ hipError_t run_product(ProductArgs &a, bool large, hipStream_t s)
     a.by_column.set(8 * a.nt);
     a.by_rest.set(a.mt % 8 ? a.mt % 8 : 8);
     // as many workgroups as run at once, a multiple of the dies
-    const int64_t most = large ? 256 : 512;
+    const int64_t most = tile == kTile256 || tile == kTile128Deep ? 256 : 512;
     const unsigned blocks = (unsigned)(count < most ? (count + 7) & ~(int64_t)7 : most);
-    if constexpr (kLarge)
-        if (large) {
-            k_product<T, O, 256, 256, PA, QA, END><<<blocks, 256, 0, s>>>(a);
-            return hipGetLastError();
-        }
-    k_product<T, O, 128, 128, PA, QA, END><<<blocks, 256, 0, s>>>(a);
+    switch (tile) {
+    case kTile64: k_product<T, O, 64, 4, PA, QA, END><<<blocks, 256, 0, s>>>(a); break;
+    case kTile128: k_product<T, O, 128, 2, PA, QA, END><<<blocks, 256, 0, s>>>(a); break;
+    case kTile128Deep:
+        if constexpr (kDeep) k_product<T, O, 128, 4, PA, QA, END><<<blocks, 256, 0, s>>>(a);
+        break;
+    default:
+        if constexpr (kLarge) k_product<T, O, 256, 2, PA, QA, END><<<blocks, 256, 0, s>>>(a);
+    }
     return hipGetLastError();
 }
 
 template <bool PA, bool QA, int END>
-hipError_t product(ProductArgs &a, int type, bool large, hipStream_t s)
+hipError_t product(ProductArgs &a, int type, Tile tile, hipStream_t s)
 {
-    if (type == kF32) return run_product<bf16_t, float, PA, QA, END>(a, large, s);
-    if (type == kF16) return run_product<f16_t, f16_t, PA, QA, END>(a, large, s);
-    return run_product<bf16_t, bf16_t, PA, QA, END>(a, large, s);
+    if (type == kF32) return run_product<bf16_t, float, PA, QA, END>(a, tile, s);
+    if (type == kF16) return run_product<f16_t, f16_t, PA, QA, END>(a, tile, s);
+    return run_product<bf16_t, bf16_t, PA, QA, END>(a, tile, s);
 }
 
-// Whether tiles of 256 x 256 are taken: where every compute unit gets one and
-// the sum is long enough.  Two workgroups of 128 x 128 overlap one's end with the
-// other's products; one of 256 x 256 reads less (`slabs` of k; 65,536 x 384 x
-// 1024 bf16, 6 slabs: 130 us with 128, 204 with 256; 8192 x 4096 x 11008, 64
-// slabs: 1702 and 1440).
-bool large_tiles(int64_t m, int64_t n, int64_t slabs)
+int64_t tiles_of(int64_t m, int64_t n, Tile t) { return ((m + edge_of(t) - 1) / edge_of(t)) * ((n + edge_of(t) - 1) / edge_of(t)); }
+
+// The tile for m x n results of `slabs` slabs each.  256 x 256 where every
+// compute unit gets one and the sum is long enough: it reads less, but two
+// workgroups of 128 x 128 overlap one's end with the other's products (65,536 x
+// 384 x 1024 bf16, 6 slabs: 130 us with 128, 204 with 256; 8192 x 4096 x 11008,
+// 64 slabs: 1494 and 1261).  Below, for the projections, whose sums cannot be
+// cut: 128 x 128 with four slabs on their way where there is one for a compute
+// unit (1999 x 385 x 1001 f32, 42 slabs: 42 us, two slabs 48), 64 x 64 where
+// there are fewer (300 x 1000 x 1000 f32: 41 us, 63 with the larger; 9 x 4096 x
+// 11008 bf16: 34 us, 5.3 TB/s of weights, and 45).
+Tile projection_tile(int64_t m, int64_t n, int64_t slabs)
 {
-    return slabs >= 24 && ((m + 255) / 256) * ((n + 255) / 256) >= 256;
+    if (slabs >= 24 && tiles_of(m, n, kTile256) >= 256) return kTile256;
+    const int64_t tiles = tiles_of(m, n, kTile128);
+    return tiles > 256 ? kTile128 : tiles > 100 && slabs >= 16 ? kTile128Deep : kTile64;
 }
 
-// Into how many parts the sum over k is cut so that the device is filled.
-int parts_of(int64_t m, int64_t n, int64_t slabs)
+// Other sums are cut into parts; small products do better in small tiles (dx of
+// 2000 x 384 x 1024 bf16, 1536 tiles times slabs: 18 us, 23 in tiles of 128; of
+// 1999 x 385 x 1001 f32, 12,288: 54 and 40).
+Tile sum_tile(int64_t m, int64_t n, int64_t slabs)
 {
-    const int64_t tiles = ((m + 127) / 128) * ((n + 127) / 128);
-    int64_t parts = 512 / tiles;
+    if (slabs >= 24 && tiles_of(m, n, kTile256) >= 256) return kTile256;
+    const int64_t tiles = tiles_of(m, n, kTile128);
+    return tiles <= 256 && tiles * slabs <= 5000 ? kTile64 : kTile128;
+}
+
+// Into how many parts a sum is cut so that the device is filled, each of four
+// slabs at least.
+int parts_of(int64_t m, int64_t n, int64_t slabs, Tile t)
+{
+    if (t == kTile256) return 1;
+    int64_t parts = 512 / tiles_of(m, n, t);
     if (parts > slabs / 4) parts = slabs / 4;
     return parts < 1 ? 1 : (int)parts;
 }
@@ -875,7 +977,7 @@ struct GradPlan {
     int n_pad, outs;
     float *part;
     int x_parts, w_parts;
-    bool x_large, w_large;
+    Tile x_tile, w_tile;
     uint64_t bytes;
 };
 
@@ -893,10 +995,10 @@ GradPlan plan(const GatedGradArgs &a)
     f.outs = (a.ggate != nullptr) + (a.gup != nullptr);
     const int64_t m = (int64_t)f.outs * a.hidden, slabs_x = (f.n_pad + kSlab - 1) / kSlab, slabs_w = (a.n + kSlab - 1) / kSlab;
     const int64_t all_x = slabs_x * 2 * (planes == 3 ? 6 : 1), all_w = slabs_w * (planes == 1 ? 1 : a.x ? 6 : 3);
-    f.x_large = large_tiles(a.n, a.dim, all_x);
-    f.w_large = large_tiles(m, a.dim, all_w);
-    f.x_parts = a.gx && a.n && !f.x_large ? parts_of(a.n, a.dim, all_x) : 1;
-    f.w_parts = f.outs && !f.w_large ? parts_of(m, a.dim, all_w) : 1;
+    f.x_tile = sum_tile(a.n, a.dim, all_x);
+    f.w_tile = sum_tile(m, a.dim, all_w);
+    f.x_parts = a.gx && a.n ? parts_of(a.n, a.dim, all_x, f.x_tile) : 1;
+    f.w_parts = f.outs && a.n ? parts_of(m, a.dim, all_w, f.w_tile) : 1;
     uint64_t part = 0;
     if (f.x_parts > 1) part = (uint64_t)f.x_parts * a.n * a.dim * 4;
     if (f.w_parts > 1) {
@@ -911,11 +1013,12 @@ GradPlan plan(const GatedGradArgs &a)
 hipError_t join(const ProductArgs &p, int type, hipStream_t s)
 {
     if (p.parts == 1) return hipSuccess;
-    const int64_t all = (int64_t)p.m * p.n * p.outs;
-    const unsigned blocks = blocks_for((all + 3) / 4);
+    const int all = p.m * p.n * p.outs;
+    Divide by_n;
+    by_n.set(p.n);
     ERSJ_ELEM_SWITCH(type, O,
-        k_product_join<O><<<blocks, 256, 0, s>>>(p.part, p.parts, p.outs, p.m, p.n, (O *)p.out[0], (O *)p.out[1],
-                                                 p.ld_out[0], p.ld_out[1]));
+        k_product_join<O><<<blocks_for((all + 3) / 4), 256, 0, s>>>(p.part, p.parts, p.m, p.n, all, by_n, (O *)p.out[0],
+                                                                    (O *)p.out[1], p.ld_out[0], p.ld_out[1]));
     return hipGetLastError();
 }
 
@@ -956,13 +1059,15 @@ hipError_t launch_gated(const GatedArgs &a, hipStream_t s)
 {
     if (a.n == 0) return hipSuccess;
     const ForwardPlan f = plan(a);
-    TRY_HIP(lay(f.x, a.x, a.type, a.n, a.dim, a.ld_x, s));
-    TRY_HIP(lay(f.gate, a.gate, a.type, a.hidden, a.dim, a.ld_gate, s));
-    TRY_HIP(lay(f.up, a.up, a.type, a.hidden, a.dim, a.ld_up, s));
+    Layer layer;
+    layer.add(f.x, a.x, a.n, a.dim, a.ld_x);
+    layer.add(f.gate, a.gate, a.hidden, a.dim, a.ld_gate);
+    layer.add(f.up, a.up, a.hidden, a.dim, a.ld_up);
+    TRY_HIP(layer.run(a.type, s));
     ProductArgs p = projections(f.gate, f.up, f.x, a.type, false, a.n, a.dim, a.hidden, a.act);
     p.out[0] = a.h;
     p.ld_out[0] = a.ld_h;
-    return product<false, false, kGate>(p, a.type, large_tiles(a.n, 2 * (int64_t)a.hidden, (int64_t)p.products * ((p.k + kSlab - 1) / kSlab)), s);
+    return product<false, false, kGate>(p, a.type, projection_tile(a.n, 2 * (int64_t)a.hidden, (int64_t)p.products * ((p.k + kSlab - 1) / kSlab)), s);
 }
 
 uint64_t gated_grad_work(const GatedGradArgs &a) { return plan(a).bytes; }
@@ -972,15 +1077,17 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s)
     const GradPlan f = plan(a);
     if (!f.outs && (!a.gx || a.n == 0)) return hipSuccess;
     if (a.n) {
-        if (a.x) TRY_HIP(lay(f.x, a.x, a.type, a.n, a.dim, a.ld_x, s));
-        else {
+        Layer layer;
+        layer.add(f.x, a.x, a.n, a.dim, a.ld_x);
+        layer.add(f.gate, a.gate, a.hidden, a.dim, a.ld_gate);
+        layer.add(f.up, a.up, a.hidden, a.dim, a.ld_up);
+        TRY_HIP(layer.run(a.type, s));
+        if (!a.x) {
             // what a code stands for is a bf16 number: 32-bit rows have one plane
             const UnpackArgs u{a.codes, a.scales, a.n, a.dim, const_cast<uint16_t *>(f.x.p),
                                a.type == kF16 ? kF16 : kBF16, f.x.ld, (int)f.x.ld};
             TRY_HIP(launch_unpack(u, s));
         }
-        TRY_HIP(lay(f.gate, a.gate, a.type, a.hidden, a.dim, a.ld_gate, s));
-        TRY_HIP(lay(f.up, a.up, a.type, a.hidden, a.dim, a.ld_up, s));
         ProductArgs p = projections(f.gate, f.up, f.x, a.type, !a.x, a.n, a.dim, a.hidden, a.act);
         p.gh = a.gh;
         p.ld_gh = a.ld_gh;
@@ -989,7 +1096,7 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s)
         p.d_plane = f.d_plane;
         p.ld_d = f.n_pad;
         p.n_pad = f.n_pad;
-        TRY_HIP((product<false, false, kGateGrad>(p, a.type, large_tiles(a.n, 2 * (int64_t)a.hidden, (int64_t)p.products * ((p.k + kSlab - 1) / kSlab)), s)));
+        TRY_HIP((product<false, false, kGateGrad>(p, a.type, projection_tile(a.n, 2 * (int64_t)a.hidden, (int64_t)p.products * ((p.k + kSlab - 1) / kSlab)), s)));
     }
     if (a.gx && a.n) {
         ProductArgs x{};
@@ -1014,7 +1121,7 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s)
         x.n_room = pad8(a.dim);
         x.out[0] = a.gx;
         x.ld_out[0] = a.ld_gx;
-        TRY_HIP((product<true, false, kStore>(x, a.type, f.x_large, s)));
+        TRY_HIP((product<true, false, kStore>(x, a.type, f.x_tile, s)));
         TRY_HIP(join(x, a.type, s));
     }
     if (f.outs && a.n == 0) {
@@ -1050,7 +1157,7 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s)
         w.out[1] = a.gup;
         w.ld_out[0] = a.ggate ? a.ld_ggate : a.ld_gup;
         w.ld_out[1] = a.ld_gup;
-        TRY_HIP((product<true, true, kStore>(w, a.type, f.w_large, s)));
+        TRY_HIP((product<true, true, kStore>(w, a.type, f.w_tile, s)));
         TRY_HIP(join(w, a.type, s));
     }
     return hipSuccess;
