@@ -2,8 +2,8 @@
 // least of which 127 reach the largest of them, and each is held as the whole
 // number of them nearest to it.  A power of two makes every step exact (scaling,
 // the value that a code stands for, also as a 16-bit number), so nothing but
-// the one rounding to a whole number is lost: at most half of 2^e, between
-// 1/254 and 1/128 of the largest.  Both kernels are bound by memory.
+// the one rounding to a whole number is lost: at most half of 2^e, less than
+// 1/127 of the largest.  Both kernels are bound by memory.
 #include "feedforward_internal.h"
 
 namespace ersj {

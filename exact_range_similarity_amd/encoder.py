@@ -353,13 +353,20 @@ class PackedRows:
 def _empty_packed(shape, dtype, device):
     codes = torch.empty(shape, dtype=torch.int8, device=device)
     scales = torch.empty(shape[:-1] + (-(-shape[-1] // PACK_BLOCK),), dtype=torch.uint8, device=device)
-    return PackedRows(codes, scales, dtype)
+    return _packed(codes, scales, dtype)
+
+
+def _packed(codes, scales, dtype):
+    """PackedRows of tensors made here, which need no checks."""
+    kept = object.__new__(PackedRows)
+    kept.codes, kept.scales, kept.dtype = codes, scales, dtype
+    return kept
 
 
 def pack_rows(x, stream=None):
     """``ersj_pack_rows``: the rows of ``x`` in 8 bits, as ``PackedRows``: whole
-    multiples of a power of two for each run of 32 along a row, off by at most
-    1/128 of the largest of the run.  Not differentiable; ``layer_norm`` and
+    multiples of a power of two for each run of 32 along a row, off by less than
+    1/127 of the largest of the run.  Not differentiable; ``layer_norm`` and
     ``gated`` keep their input so with ``pack=True``."""
     xt = _type(x, "x")
     device = x.device
@@ -555,8 +562,8 @@ class _LayerNormPacked(torch.autograd.Function):
         need = ctx.needs_input_grad
         params = need[1] or need[2]
         dtype = ctx.dtypes[1] if weight is None else weight.dtype
-        gx, gw, gb = layer_norm_grad(_as_rows(grad), PackedRows(codes, scales, ctx.dtypes[0]), mean, rstd, weight,
-                                     dtype, need[0], params)
+        gx, gw, gb = layer_norm_grad(_as_rows(grad), _packed(codes, scales, ctx.dtypes[0]), mean, rstd, weight, dtype,
+                                     need[0], params)
         return gx, gw if need[1] else None, gb if need[2] else None, None
 
 

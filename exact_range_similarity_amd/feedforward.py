@@ -6,8 +6,8 @@ in the manner of ``encoder``: types, rows, ``out`` and ``stream`` are as there.
 """
 import torch
 
-from .encoder import (_TYPES, PackedRows, _apply, _as_rows, _check, _elsewhere, _given, _library, _on, _raw_stream,
-                      _rows, _run_elsewhere, _type, _written, pack_rows)
+from .encoder import (_TYPES, PackedRows, _apply, _as_rows, _check, _elsewhere, _given, _library, _on, _packed,
+                      _raw_stream, _rows, _run_elsewhere, _type, _written, pack_rows)
 
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}  # ERSJ_SILU, ERSJ_GELU, ERSJ_GELU_TANH
 
@@ -129,5 +129,5 @@ class _Gated(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
         *kept, w_gate, w_up = ctx.saved_tensors
-        x = kept[0] if ctx.packed is None else PackedRows(*kept, ctx.packed)
+        x = kept[0] if ctx.packed is None else _packed(*kept, ctx.packed)
         return *gated_grad(_as_rows(grad), x, w_gate, w_up, ctx.activation, *ctx.needs_input_grad[:3]), None, None

@@ -1,13 +1,15 @@
 """Train a token-table encoder and join the vectors it makes.
 
 A text's vector is the mean of its normalised token rows, scaled to unit
-length: embed -> layer_norm -> mean over the text -> unit length.  Training
+length: embed -> layer_norm -> mean over the text -> unit length.  With
+``--hidden`` a gated feed-forward block is added to the rows before the mean, and
+what the backward pass needs of the forward pass is kept in 8 bits.  Training
 draws pairs of texts of one topic together and apart from the other texts of
 the batch, clips the gradients by their global norm and takes a step; the
 exact epsilon self-join then finds all pairs of texts whose vectors lie within
 a given distance.  Synthetic topics stand in for a corpus.
 
-    python examples/train_encoder.py [--texts 20000] [--steps 200]
+    python examples/train_encoder.py [--texts 20000] [--steps 200] [--hidden 192]
 """
 import argparse
 import os
@@ -46,19 +48,27 @@ class Corpus:
 
 
 class Encoder:
-    def __init__(self, vocab, dim, padding, seed, device="cuda"):
+    def __init__(self, vocab, dim, padding, seed, hidden=0, device="cuda"):
         g = torch.Generator(device=device).manual_seed(seed)
         self.table = torch.randn((vocab, dim), generator=g, device=device).mul_(dim ** -0.5).requires_grad_()
         self.weight = torch.ones(dim, device=device, requires_grad=True)
         self.bias = torch.zeros(dim, device=device, requires_grad=True)
         self.padding, self.scale = padding, dim ** 0.5
+        self.block = None
+        if hidden:  # both projections up, one down that begins at zero
+            up = [torch.randn((hidden, dim), generator=g, device=device).mul_(dim ** -0.5) for _ in range(2)]
+            self.block = [w.to(torch.bfloat16).requires_grad_()
+                          for w in (*up, torch.zeros((dim, hidden), device=device))]
 
     def parameters(self):
-        return [self.table, self.weight, self.bias]
+        return [self.table, self.weight, self.bias] + (self.block or [])
 
     def __call__(self, ids):
         rows = ersj.embed(self.table, ids, self.scale, self.padding, torch.bfloat16)
-        rows, _, _ = ersj.layer_norm(rows, self.weight, self.bias)
+        rows, _, _ = ersj.layer_norm(rows, self.weight, self.bias, pack=self.block is not None)
+        if self.block:
+            gate, up, down = self.block
+            rows = rows + ersj.gated(rows, gate, up, "gelu", pack=True) @ down.t()
         kept = (ids != self.padding).unsqueeze(-1)
         total = (rows.float() * kept).sum(dim=1)
         return total / total.norm(dim=1, keepdim=True).clamp_min(1e-12)
@@ -83,9 +93,9 @@ def join_quality(x, topic, eps):
 
 
 def train(texts=20000, topics=500, vocab=32768, dim=64, length=48, batch=256, steps=200, rate=60.0, max_norm=0.5,
-          eps=0.9, seed=0, log=print):
+          eps=0.9, seed=0, hidden=0, log=print):
     corpus = Corpus(texts, topics, vocab, length, seed)
-    encoder = Encoder(vocab, dim, corpus.padding, seed + 1)
+    encoder = Encoder(vocab, dim, corpus.padding, seed + 1, hidden)
     g = torch.Generator(device="cuda").manual_seed(seed + 2)
     target = torch.arange(min(batch, topics), device="cuda")
     quality = [join_quality(vectors(encoder, corpus.ids), corpus.topic, eps)]
@@ -117,5 +127,6 @@ if __name__ == "__main__":
     ap.add_argument("--texts", type=int, default=20000)
     ap.add_argument("--steps", type=int, default=200)
     ap.add_argument("--dim", type=int, default=64)
+    ap.add_argument("--hidden", type=int, default=0)
     args = ap.parse_args()
-    train(texts=args.texts, steps=args.steps, dim=args.dim)
+    train(texts=args.texts, steps=args.steps, dim=args.dim, hidden=args.hidden)

@@ -125,7 +125,8 @@ def held_ref(x):
     most = wide.abs().amax(dim=2)
     bad = ~torch.isfinite(wide).all(dim=2)
     at, e = torch.frexp(torch.where(bad, torch.ones_like(most), most) / 127)
-    e = torch.where(at == 0.5, e - 1, e).clamp(min=-126).to(torch.int64)
+    # (zero has no exponent of its own: the least)
+    e = torch.where(at == 0, torch.full_like(e, -126), torch.where(at == 0.5, e - 1, e)).clamp(min=-126).to(torch.int64)
     top = 10 if x.dtype == torch.float16 else 122
     lim = torch.where(e == top, 63.0, 127.0).to(F64).unsqueeze(-1)
     step = ((e + 1023) << 52).view(F64).unsqueeze(-1)

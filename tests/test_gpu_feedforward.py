@@ -73,6 +73,16 @@ def test_gated_of_many_rows(n, dim, hidden, kind):
 
 
 @pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("n,dim,hidden", [(4200, 4104, 2100), (4300, 4099, 2111), (1500, 1100, 700), (1500, 1097, 704)])
+def test_gated_in_large_tiles(n, dim, hidden, kind):
+    # enough of them for tiles of 256 in every product, with edges in both directions;
+    # and just enough for one tile of 128 to a compute unit
+    x, wg, wu, dh = block(n, dim, hidden, TYPES[kind], 50)
+    check_gated(ersj.gated(x, wg, wu, "gelu"), x, wg, wu, "gelu")
+    check_gated_grad(ersj.gated_grad(dh, x, wg, wu, "gelu"), dh, x, wg, wu, "gelu")
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
 @pytest.mark.parametrize("dim", [1, 3, 7, 8, 15, 16, 31, 32, 33, 63, 64, 65, 100, 384, 385, 1001])
 def test_pack(dim, kind):
     for n, pad in ((1, 0), (7, 5), (300, 0), (333, 9)):
