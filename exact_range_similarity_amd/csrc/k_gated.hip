@@ -33,8 +33,8 @@ typedef f16_t f16x8 __attribute__((ext_vector_type(8)));
 typedef bf16_t bf16x8 __attribute__((ext_vector_type(8)));
 
 // Which planes are multiplied in turn, four bits each, smallest products first:
-// one plane, three of both operands, three of one of them.
-constexpr uint32_t kPlanes6P = 0x010201, kPlanes6Q = 0x001021, kPlanes3 = 0x012;
+// one plane, three of both operands, three of one of them, two of one.
+constexpr uint32_t kPlanes2 = 0x01, kPlanes6P = 0x010201, kPlanes6Q = 0x001021, kPlanes3 = 0x012;
 
 constexpr int kSlab = 64, kSteps = kSlab / 32;
 
@@ -80,6 +80,7 @@ struct ProductArgs {
     int64_t ld_gh;
     uint16_t *dg, *du;
     int64_t d_plane, ld_d;
+    int d_planes;         // of dg and du
     int n_pad;            // columns of dg and du that are written, zeros behind n
     int act;
 };
@@ -662,12 +663,26 @@ __global__ __launch_bounds__(256, BM == 256 || kStages * BM > 256 ? 1 : 2) void 
                         // zeros behind the block's columns come from the zeros in the place of grad_h
 #pragma unroll
                         for (int of = 0; of < 2; ++of) {
+                            T *to = (T *)(of ? a.du : a.dg);
+                            for (int plane = 0;; ++plane) {
 #pragma unroll
-                            for (int j = 0; j < MB; ++j) {
-                                put(j, 0, acc[i + 2 * of][j]);
-                                put(j, 1, acc[i + 2 * of + 1][j]);
+                                for (int j = 0; j < MB; ++j) {
+                                    put(j, 0, acc[i + 2 * of][j]);
+                                    put(j, 1, acc[i + 2 * of + 1][j]);
+                                }
+                                store(to, a.ld_d, col, a.n_pad);
+                                if (BM == 256 || plane + 1 == a.d_planes) break;
+                                to += a.d_plane;
+#pragma unroll
+                                for (int c = 0; c < 2 * MB; ++c) {
+                                    f32x4 &v = acc[i + 2 * of + c / MB][c % MB];
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        const float h = (float)(T)v[e];
+                                        v[e] = fabsf(h) < __builtin_inff() ? v[e] - h : 0.f;
+                                    }
+                                }
                             }
-                            store((T *)(of ? a.du : a.dg), a.ld_d, col, a.n_pad);
                         }
                     } else {
                         store((T *)a.out[0], a.ld_out[0], col, a.n);
@@ -974,7 +989,7 @@ struct GradPlan {
     Operand x, gate, up;
     uint16_t *dg, *du;
     int64_t d_plane;
-    int n_pad, outs;
+    int n_pad, outs, d_planes;
     float *part;
     int x_parts, w_parts;
     Tile x_tile, w_tile;
@@ -987,14 +1002,20 @@ GradPlan plan(const GatedGradArgs &a)
     GradPlan f;
     f.x = operand(room, a.x, a.type, a.n, a.dim, a.ld_x);
     weights(room, a.gate, a.ld_gate, a.up, a.ld_up, a.type, a.hidden, a.dim, f.gate, f.up);
-    const int planes = a.type == kF32 ? 3 : 1;
+    // dg and du as 16-bit values are a rounding more than the results' own, 1.4 times
+    // its error; in small products, which other things bound, they have a second
+    // plane for what the first leaves over (9 x 384 x 1024 bf16: 28 us either way;
+    // 1 x 4096 x 11008, where the weights are read twice for it: 117 us and 151)
+    const int64_t weight = (int64_t)a.dim * a.hidden;
+    f.d_planes = a.type == kF32 ? 3 : a.n * weight <= (int64_t)1 << 27 && weight <= 1 << 23 ? 2 : 1;
+    const int planes = f.d_planes;
     f.n_pad = pad8(a.hidden);
     f.d_plane = a.n * f.n_pad;
     f.dg = (uint16_t *)room.take((uint64_t)f.d_plane * 2 * planes);
     f.du = (uint16_t *)room.take((uint64_t)f.d_plane * 2 * planes);
     f.outs = (a.ggate != nullptr) + (a.gup != nullptr);
     const int64_t m = (int64_t)f.outs * a.hidden, slabs_x = (f.n_pad + kSlab - 1) / kSlab, slabs_w = (a.n + kSlab - 1) / kSlab;
-    const int64_t all_x = slabs_x * 2 * (planes == 3 ? 6 : 1), all_w = slabs_w * (planes == 1 ? 1 : a.x ? 6 : 3);
+    const int64_t all_x = slabs_x * 2 * (planes == 3 ? 6 : planes), all_w = slabs_w * (planes < 3 ? planes : a.x ? 6 : 3);
     f.x_tile = sum_tile(a.n, a.dim, all_x);
     f.w_tile = sum_tile(m, a.dim, all_w);
     f.x_parts = a.gx && a.n ? parts_of(a.n, a.dim, all_x, f.x_tile) : 1;
@@ -1095,6 +1116,7 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s)
         p.du = f.du;
         p.d_plane = f.d_plane;
         p.ld_d = f.n_pad;
+        p.d_planes = f.d_planes;
         p.n_pad = f.n_pad;
         TRY_HIP((product<false, false, kGateGrad>(p, a.type, projection_tile(a.n, 2 * (int64_t)a.hidden, (int64_t)p.products * ((p.k + kSlab - 1) / kSlab)), s)));
     }
@@ -1109,9 +1131,9 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s)
         x.p_plane = f.gate.plane;
         x.q_plane = f.d_plane;
         x.k = a.hidden;
-        x.products = a.type == kF32 ? 6 : 1;
+        x.products = a.type == kF32 ? 6 : f.d_planes;
         x.p_planes = a.type == kF32 ? kPlanes6P : 0;
-        x.q_planes = a.type == kF32 ? kPlanes6Q : 0;
+        x.q_planes = a.type == kF32 ? kPlanes6Q : f.d_planes == 2 ? kPlanes2 : 0;
         x.sources = 2;
         x.outs = 1;
         x.parts = f.x_parts;
@@ -1142,9 +1164,9 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s)
         w.p_plane = f.x.plane;
         w.q_plane = f.d_plane;
         w.k = (int)a.n;
-        w.products = a.type != kF32 ? 1 : a.x ? 6 : 3;
+        w.products = a.type != kF32 ? f.d_planes : a.x ? 6 : 3;
         w.p_planes = a.type != kF32 || !a.x ? 0 : kPlanes6P;
-        w.q_planes = a.type != kF32 ? 0 : a.x ? kPlanes6Q : kPlanes3;
+        w.q_planes = a.type != kF32 ? (f.d_planes == 2 ? kPlanes2 : 0) : a.x ? kPlanes6Q : kPlanes3;
         w.sources = 1;
         w.outs = f.outs;
         w.parts = f.w_parts;

@@ -201,8 +201,8 @@ uint64_t ersj_gated_work(const void *d_x, int32_t type, int64_t n, int32_t dim, 
  *                      The three's spacings are below 2^21.
  *  d_work            : at least ersj_gated_grad_work(...) bytes, aligned to
  *                      256; want_*: whether that gradient is wanted.
- * dg and du are rounded to the 16-bit type that they are multiplied in (32-bit
- * tensors: held in three parts).  Errors: INVALID_ARG, HIP.
+ * dg and du are rounded to the 16-bit type that they are multiplied in (small
+ * products: held in two parts of it, 32-bit tensors: in three).  Errors: INVALID_ARG, HIP.
  */
 int ersj_gated_grad(const void *d_grad_h, int64_t ld_grad_h, const void *d_x, int64_t ld_x, const int8_t *d_codes,
                     const uint8_t *d_scales, int32_t type, int64_t n, int32_t dim, const void *d_gate, int64_t ld_gate,
