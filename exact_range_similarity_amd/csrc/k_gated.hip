@@ -725,39 +725,53 @@ __global__ __launch_bounds__(256) void k_zero(O *out, int64_t ld, int m, int n)
 
 // Sums of the parts of a product, in order, eight of them on their way at a
 // time.  (Only products of few tiles have parts: m n is below 2^23.)
+struct Parts {
+    const float *part;
+    int parts, m, n, all;  // all: of one or two results [m][n]
+    Divide by_n;
+    void *out[2];
+    int64_t ld[2];
+};
+struct Joins {
+    Parts p[2];
+};
 template <typename O>
-__global__ __launch_bounds__(256) void k_product_join(const float *part, int parts, int m, int n, int all, Divide by_n,
-                                                      O *out0, O *out1, int64_t ld0, int64_t ld1)
+__global__ __launch_bounds__(256) void k_product_join(Joins joins)
 {
+    const Parts a = joins.p[blockIdx.y];
     const int i = (blockIdx.x * 256 + threadIdx.x) * 4;
-    if (i >= all) return;
+    if (i >= a.all) return;
     f32x4 v = (f32x4)0.f;
-    if (i + 4 <= all) {
-        for (int p = 0; p < parts; p += 8) {
+    if (i + 4 <= a.all) {
+        for (int p = 0; p < a.parts; p += 8) {
             f32x4 x[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-                x[u] = Slot<float, 4>::load(part + (int64_t)(p + u < parts ? p + u : parts - 1) * all + i);
+                x[u] = Slot<float, 4>::load(a.part + (int64_t)(p + u < a.parts ? p + u : a.parts - 1) * a.all + i);
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-                if (p + u < parts) v += x[u];
+                if (p + u < a.parts) v += x[u];
         }
     } else {
-        for (int p = 0; p < parts; ++p)
-            for (int e = 0; e < all - i; ++e) v[e] += part[(int64_t)p * all + i + e];
+        for (int p = 0; p < a.parts; ++p)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e < a.all) v[e] += a.part[(int64_t)p * a.all + i + e];
     }
-    int row = by_n(i), col = i - row * n;
-    if (col + 4 <= n) {
-        O *to = row < m ? out0 + row * ld0 : out1 + (row - m) * ld1;
-        Slot<O, 4>::store(to + col, __builtin_convertvector(v, typename Slot<O, 4>::vec));
+    int row = a.by_n(i), col = i - row * a.n;
+    auto at = [&](int r) { return row < a.m ? (O *)a.out[0] + r * a.ld[0] : (O *)a.out[1] + (r - a.m) * a.ld[1]; };
+    if (col + 4 <= a.n) {
+        Slot<O, 4>::store(at(row) + col, __builtin_convertvector(v, typename Slot<O, 4>::vec));
         return;
     }
-    for (int e = 0; e < 4 && i + e < all; ++e, ++col) {
-        while (col >= n) {
-            col -= n;
+#pragma unroll
+    for (int e = 0; e < 4; ++e, ++col) {
+        if (i + e >= a.all) return;
+        while (col >= a.n) {
+            col -= a.n;
             ++row;
         }
-        (row < m ? out0 + row * ld0 : out1 + (row - m) * ld1)[col] = (O)v[e];
+        at(row)[col] = (O)v[e];
     }
 }
 
@@ -990,7 +1004,7 @@ struct GradPlan {
     uint16_t *dg, *du;
     int64_t d_plane;
     int n_pad, outs, d_planes;
-    float *part;
+    float *x_part, *w_part;
     int x_parts, w_parts;
     Tile x_tile, w_tile;
     uint64_t bytes;
@@ -1020,28 +1034,40 @@ GradPlan plan(const GatedGradArgs &a)
     f.w_tile = sum_tile(m, a.dim, all_w);
     f.x_parts = a.gx && a.n ? parts_of(a.n, a.dim, all_x, f.x_tile) : 1;
     f.w_parts = f.outs && a.n ? parts_of(m, a.dim, all_w, f.w_tile) : 1;
-    uint64_t part = 0;
-    if (f.x_parts > 1) part = (uint64_t)f.x_parts * a.n * a.dim * 4;
-    if (f.w_parts > 1) {
-        const uint64_t b = (uint64_t)f.w_parts * m * a.dim * 4;
-        if (b > part) part = b;
-    }
-    f.part = (float *)room.take(part);
+    f.x_part = (float *)room.take(f.x_parts > 1 ? (uint64_t)f.x_parts * a.n * a.dim * 4 : 0);
+    f.w_part = (float *)room.take(f.w_parts > 1 ? (uint64_t)f.w_parts * m * a.dim * 4 : 0);
     f.bytes = room.used;
     return f;
 }
 
-hipError_t join(const ProductArgs &p, int type, hipStream_t s)
-{
-    if (p.parts == 1) return hipSuccess;
-    const int all = p.m * p.n * p.outs;
-    Divide by_n;
-    by_n.set(p.n);
-    ERSJ_ELEM_SWITCH(type, O,
-        k_product_join<O><<<blocks_for((all + 3) / 4), 256, 0, s>>>(p.part, p.parts, p.m, p.n, all, by_n, (O *)p.out[0],
-                                                                    (O *)p.out[1], p.ld_out[0], p.ld_out[1]));
-    return hipGetLastError();
-}
+// The parts of one product or two, added in one launch.
+struct Joiner {
+    Joins j;
+    int count = 0, most = 0;
+    void add(const ProductArgs &p)
+    {
+        if (p.parts == 1) return;
+        Parts &a = j.p[count++];
+        a.part = p.part;
+        a.parts = p.parts;
+        a.m = p.m;
+        a.n = p.n;
+        a.all = p.m * p.n * p.outs;
+        a.by_n.set(p.n);
+        for (int i = 0; i < 2; ++i) {
+            a.out[i] = p.out[i];
+            a.ld[i] = p.ld_out[i];
+        }
+        if (a.all > most) most = a.all;
+    }
+    hipError_t run(int type, hipStream_t s) const
+    {
+        if (!count) return hipSuccess;
+        const dim3 blocks(blocks_for((most + 3) / 4), count);
+        ERSJ_ELEM_SWITCH(type, O, k_product_join<O><<<blocks, 256, 0, s>>>(j));
+        return hipGetLastError();
+    }
+};
 
 // P = the weights, Q = the rows: both projections.
 ProductArgs projections(const Operand &gate, const Operand &up, const Operand &x, int type, bool held, int64_t n,
@@ -1120,6 +1146,7 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s)
         p.n_pad = f.n_pad;
         TRY_HIP((product<false, false, kGateGrad>(p, a.type, projection_tile(a.n, 2 * (int64_t)a.hidden, (int64_t)p.products * ((p.k + kSlab - 1) / kSlab)), s)));
     }
+    Joiner joiner;
     if (a.gx && a.n) {
         ProductArgs x{};
         x.p[0] = f.gate.p;
@@ -1137,14 +1164,14 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s)
         x.sources = 2;
         x.outs = 1;
         x.parts = f.x_parts;
-        x.part = f.part;
+        x.part = f.x_part;
         x.m = (int)a.n;
         x.n = a.dim;
         x.n_room = pad8(a.dim);
         x.out[0] = a.gx;
         x.ld_out[0] = a.ld_gx;
         TRY_HIP((product<true, false, kStore>(x, a.type, f.x_tile, s)));
-        TRY_HIP(join(x, a.type, s));
+        joiner.add(x);
     }
     if (f.outs && a.n == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -1170,7 +1197,7 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s)
         w.sources = 1;
         w.outs = f.outs;
         w.parts = f.w_parts;
-        w.part = f.part;
+        w.part = f.w_part;
         w.m = a.hidden;
         w.n = a.dim;
         w.n_room = pad8(a.dim);
@@ -1180,9 +1207,9 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s)
         w.ld_out[0] = a.ggate ? a.ld_ggate : a.ld_gup;
         w.ld_out[1] = a.ld_gup;
         TRY_HIP((product<true, true, kStore>(w, a.type, f.w_tile, s)));
-        TRY_HIP(join(w, a.type, s));
+        joiner.add(w);
     }
-    return hipSuccess;
+    return joiner.run(a.type, s);
 }
 
 }  // namespace ersj
