@@ -5,20 +5,32 @@
 //   dx = dg Wg + du Wu, dWg = dg^T x, dWu = du^T x  (a product each, the first over both pairs)
 //
 // All of it is one tiled matrix product with different ends.  A workgroup owns
-// BM x BN results; the two operands' slabs of 64 along k are copied to LDS by
-// loads that write it directly, one slab ahead, and feed 32x32x16 matrix
-// instructions.  An operand whose rows run along k is read from LDS 16 bytes a
-// lane; one whose rows run across k (the weights for dx, all operands of dW)
-// is staged as it lies in memory and transposed by the LDS read itself, so no
-// transposed copy of anything is made.  For the projections the rows of the
-// weights' slab alternate 32 of Wg and 32 of Wu, so a lane holds g and u of the
-// same place.  The matrix instruction's first operand is the one along the
-// results' rows in memory: a lane then holds four neighbours of a row.
+// tiles of BM x BM results in turn; the two operands' slabs of 64 along k are
+// copied to LDS by loads that write it directly, up to two (small tiles: four)
+// slabs ahead and into the next tile, and feed 16x16x32 matrix instructions
+// (32x32x16 ones, which move more sums through the registers, took 1440 us where
+// these take 1283, forward of 8192 x 4096 x 11008 bf16).  An operand whose rows run
+// along k is read from LDS 16 bytes a lane; one whose rows run across k (the
+// weights for dx, all operands of dW) is staged as it lies in memory and
+// transposed by the LDS read itself, so no transposed copy of anything is made.
+// For the projections the rows of the weights' slab alternate 32 of Wg and 32 of
+// Wu, so a lane holds g and u of the same place.  The matrix instruction's first
+// operand is the one along the results' rows in memory: a lane then holds four
+// neighbours of a row.
+//
+// 8192 x 4096 x 11008 bf16: forward 1.16 ms (1.27 PFLOP/s), gradient 3.6 ms (1.22),
+// bound by the matrix units at the clock that the power allows (2.0 GHz, half of
+// their cycles busy, as in the library's product of this size, 1.25 PFLOP/s).
+// 65,536 x 384 x 1024: forward 143 us, where a tile's end (activation, 134 MB of
+// results) and the fetch of its six slabs weigh as much as its products.  Few rows
+// are bound by the weights: 1 x 4096 x 11008, 180 MB, 37 us, 4.9 TB/s.
 //
 // 32-bit tensors are split into three bf16 parts, x = x1 + x2 + x3, each the
-// rounded rest of those before, and the six products whose order is above 2^-27
-// of the whole are summed, smallest first: the same kernel with six times the
-// slabs.  What is dropped is at most 3 * 2^-27 of each product.
+// rounded rest of those before (8 bits each: nothing is left of 24), and the six
+// products of parts whose order is 2^-16 and above are summed, smallest first:
+// the same kernel with six times the slabs, 215 TFLOP/s for 4096 x 4096 x 4096
+// where the library's 32-bit product has 148.  What is dropped (x2 y3, x3 y2, x3
+// y3) is at most 2^-23 of each product.
 #include "feedforward_internal.h"
 
 namespace ersj {
@@ -474,6 +486,9 @@ __global__ __launch_bounds__(256, BM == 256 || kStages * BM > 256 ? 1 : 2) void 
         // What was issued after the first slab's loads, in order, need not be waited for with them.
         const bool calm = inner && before;
         before = inner;
+        // one workgroup's products go before the end of the other that shares the unit
+        // (65,536 x 384 x 1024 bf16: forward 167 us, 161 with it, on one card)
+        if constexpr (BM == 128) __builtin_amdgcn_s_setprio(1);
         for (int t = u.first; t < u.last; ++t) {
             const char *at = lds + buf * STAGE;
             const uint32_t free = lds0 + buf * STAGE;
@@ -506,6 +521,8 @@ __global__ __launch_bounds__(256, BM == 256 || kStages * BM > 256 ? 1 : 2) void 
                 }
             }
         }
+
+        if constexpr (BM == 128) __builtin_amdgcn_s_setprio(0);
 
         // A lane's place: row j * 16 + lane % 16 of the wave's and, in register e
         // of block i, column i * 16 + 4 (el / 16) + e.

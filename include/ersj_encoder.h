@@ -179,7 +179,7 @@ uint64_t ersj_layer_norm_grad_packed_work(int32_t type, int64_t n, int32_t dim);
  *                   takes the arguments of the call, looks at the addresses'
  *                   alignment alone, and gives 0 where none is needed.
  * g and u stay in 32 bits.  16-bit types are multiplied as they are; 32-bit
- * values as three bf16 parts each, with an error of at most 2^-25 of every
+ * values as three bf16 parts each, with an error of at most 2^-23 of every
  * product, and an infinity among them counts as NaN.  Errors: INVALID_ARG, HIP.
  */
 enum { ERSJ_SILU = 0, ERSJ_GELU = 1, ERSJ_GELU_TANH = 2 };

@@ -5,9 +5,10 @@ A matrix instruction adds 16 products and its accumulator, each of the 17 terms
 through at most 16 additions of error below 2u, so one instruction is off by
 less than 32.1u of its terms' magnitudes, and a sum over k of k / 16
 instructions by (k / 16) * 36u of the sum of all magnitudes (second-order terms
-included).  32-bit values are multiplied as three bf16 parts: six such sums,
-3 * 2^-27 of each product dropped and 2 * 2^-27 lost with what three parts do
-not hold.
+included).  32-bit values are multiplied as three bf16 parts: bf16 rounding is
+off by at most 2^-8, so the second part is at most 2^-8 and the third 2^-16 of
+the value, and 3 * 8 bits hold all 24.  Six of the nine products of parts are
+summed; the others, two of order 2^-24 and one of 2^-32, are dropped.
 """
 import math
 
@@ -52,7 +53,7 @@ def products(dtype, held=False):
 def sum_error(k, dtype, magnitudes, held=False):
     """Bound on a sum over k of products by matrix instructions."""
     k = -(-k // 16) * 16
-    split = 5 * 2.0 ** -27 if dtype == torch.float32 else 0.0
+    split = 2 * 2.0 ** -24 + 2.0 ** -32 if dtype == torch.float32 else 0.0
     return magnitudes * (k / 16 * 36 * U * products(dtype, held) + split)
 
 
@@ -85,8 +86,8 @@ def gated_grad_ref(grad, x, w_gate, w_up, act, held=False):
     # the slopes' slopes are below 1.2 as well
     edg = dh.abs() * (eu * slope.abs() + (u.abs() + eu) * (1.2 * eg + es)) + 3 * U * dg.abs()
     edu = dh.abs() * (1.2 * eg + ev) + 2 * U * du.abs()
-    # rounded to the type multiplied, three bf16 parts in 32 bits
-    part = 2.0 ** -26 if dtype == torch.float32 else unit(dtype)
+    # rounded to the type multiplied; three bf16 parts hold 32 bits whole
+    part = 0.0 if dtype == torch.float32 else unit(dtype)
     edg = edg * (1 + part) + part * dg.abs() + tiny(dtype)
     edu = edu * (1 + part) + part * du.abs() + tiny(dtype)
     n, hidden = grad.shape
