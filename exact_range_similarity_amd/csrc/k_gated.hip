@@ -806,32 +806,34 @@ struct Lays {
 template <typename S>
 __global__ __launch_bounds__(256) void k_lay(Lays l)
 {
+    constexpr int kLen = 16 / sizeof(S);  // a thread's values
+    typedef Slot<S, kLen> V;
     const Lay a = l.m[blockIdx.y];
-    const int per = a.pad / 8;
+    const uint32_t per = a.pad / kLen;
     const int64_t all = a.n * per;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = all < (int64_t)1 << 32 ? (int64_t)((uint32_t)i / (uint32_t)per) : i / per;
-        const int c = (int)(i - r * per) * 8;
+        const int64_t r = i >> 32 ? i / per : (int64_t)((uint32_t)i / per);
+        const int c = (int)(i - r * per) * kLen;
         const S *src = (const S *)a.src + r * a.ld + c;
-        typename Slot<S, 8>::vec v;
-        if (c + 8 <= a.dim) v = Slot<S, 8>::load(src);
+        typename V::vec v;
+        if (c + kLen <= a.dim) v = V::load(src);
         else
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = c + e < a.dim ? src[e] : (S)0.f;
+            for (int e = 0; e < kLen; ++e) v[e] = c + e < a.dim ? src[e] : (S)0.f;
         uint16_t *to = a.out + r * a.pad + c;
         if constexpr (sizeof(S) == 2) {
-            *(typename Slot<S, 8>::vec *)to = v;
+            *(typename V::vec *)to = v;
         } else {
 #pragma unroll
             for (int k = 0; k < 3; ++k) {
-                s16x8 x;
+                s16x4 x;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int e = 0; e < 4; ++e) {
                     float f = v[e];
                     x[e] = (short)part_of(f);
                     v[e] = f;
                 }
-                *(s16x8 *)(to + k * a.n * a.pad) = x;
+                *(s16x4 *)(to + k * a.n * a.pad) = x;
             }
         }
     }
@@ -891,12 +893,12 @@ struct Layer {
     {
         if (!o.laid || !src) return;
         l.m[count++] = Lay{src, ld, n, dim, (int)o.ld, const_cast<uint16_t *>(o.p)};
-        if (n * (o.ld / 8) > most) most = n * (o.ld / 8);
+        if (n * o.ld > most) most = n * o.ld;
     }
     hipError_t run(int type, hipStream_t s) const
     {
         if (!count) return hipSuccess;
-        const dim3 blocks(blocks_for(most), count);
+        const dim3 blocks(blocks_for(most / (type == kF32 ? 4 : 8)), count);
         if (type == kF32) k_lay<float><<<blocks, 256, 0, s>>>(l);
         else k_lay<f16_t><<<blocks, 256, 0, s>>>(l);
         return hipGetLastError();
