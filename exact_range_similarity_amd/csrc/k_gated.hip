@@ -730,6 +730,7 @@ __global__ __launch_bounds__(256, BM == 256 || kStages * BM > 256 ? 1 : 2) void 
             }
         }
     }
+    wait_loads<0>();  // no load is on its way to LDS when the workgroup ends
 }
 
 // Zeros, for the gradients of weights that no row meets.
@@ -954,18 +955,26 @@ hipError_t product(ProductArgs &a, int type, Tile tile, hipStream_t s)
 
 int64_t tiles_of(int64_t m, int64_t n, Tile t) { return ((m + edge_of(t) - 1) / edge_of(t)) * ((n + edge_of(t) - 1) / edge_of(t)); }
 
-// The tile for m x n results of `slabs` slabs each.  256 x 256 where every
-// compute unit gets one and the sum is long enough: it reads less, but two
-// workgroups of 128 x 128 overlap one's end with the other's products (65,536 x
-// 384 x 1024 bf16, 6 slabs: 130 us with 128, 204 with 256; 8192 x 4096 x 11008,
-// 64 slabs: 1494 and 1261).  Below, for the projections, whose sums cannot be
+// Whether m x n results of `slabs` slabs each are formed in tiles of 256 x 256:
+// where every compute unit gets one and the sum is long enough.  They read less,
+// but two workgroups of 128 x 128 overlap one's end with the other's products
+// (65,536 x 384 x 1024 bf16, 6 slabs: 130 us with 128, 204 with 256; 8192 x 4096 x
+// 11008, 64 slabs: 1494 and 1261), and wide tiles may lie half outside (dx of the
+// former, 384 columns, 32 slabs: 121 us with 128, 132 with 256).
+bool large_tiles(int64_t m, int64_t n, int64_t slabs)
+{
+    const int64_t large = tiles_of(m, n, kTile256);
+    return slabs >= 24 && large >= 256 && large * 20 <= tiles_of(m, n, kTile128) * 6;
+}
+
+// Otherwise, for the projections, whose sums cannot be
 // cut: 128 x 128 with four slabs on their way where there is one for a compute
 // unit (1999 x 385 x 1001 f32, 42 slabs: 42 us, two slabs 48), 64 x 64 where
 // there are fewer (300 x 1000 x 1000 f32: 41 us, 63 with the larger; 9 x 4096 x
 // 11008 bf16: 34 us, 5.3 TB/s of weights, and 45).
 Tile projection_tile(int64_t m, int64_t n, int64_t slabs)
 {
-    if (slabs >= 24 && tiles_of(m, n, kTile256) >= 256) return kTile256;
+    if (large_tiles(m, n, slabs)) return kTile256;
     const int64_t tiles = tiles_of(m, n, kTile128);
     return tiles > 256 ? kTile128 : tiles > 100 && slabs >= 16 ? kTile128Deep : kTile64;
 }
@@ -975,7 +984,7 @@ Tile projection_tile(int64_t m, int64_t n, int64_t slabs)
 // 1999 x 385 x 1001 f32, 12,288: 54 and 40).
 Tile sum_tile(int64_t m, int64_t n, int64_t slabs)
 {
-    if (slabs >= 24 && tiles_of(m, n, kTile256) >= 256) return kTile256;
+    if (large_tiles(m, n, slabs)) return kTile256;
     const int64_t tiles = tiles_of(m, n, kTile128);
     return tiles <= 256 && tiles * slabs <= 5000 ? kTile64 : kTile128;
 }
