@@ -467,20 +467,40 @@ def layer_norm_grad(grad, x, mean, rstd, weight=None, dtype=None, want_x=True, w
     ``PackedRows`` of them (``ersj_layer_norm_grad_packed``).  The last two have
     ``dtype``: the weight's type (the default; float32 without one), x's, or float32.
     What is not wanted comes back as None."""
-    packed = x if type(x) is PackedRows else None
-    xt = _type(x, "x") if packed is None else _TYPES[x.dtype]
+    if type(x) is PackedRows:
+        return _layer_norm_grad_packed(grad, x, mean, rstd, weight, dtype, want_x, want_params, stream)
+    xt = _type(x, "x")
     if _type(grad, "grad") != xt:
         raise TypeError("grad must have the type of x")
     device = x.device
     if _elsewhere(device, stream):
-        kept = (x,) if packed is None else (x.codes, x.scales)
-        return _run_elsewhere(device, stream, (grad, *kept, mean, rstd, weight),
+        return _run_elsewhere(device, stream, (grad, x, mean, rstd, weight),
                               lambda: layer_norm_grad(grad, x, mean, rstd, weight, dtype, want_x, want_params))
+    n, ldx = _rows(x, "x")
+    dim, pt, w, dtype = _norm_grad_args(grad, x, mean, rstd, weight, dtype, xt, device)
+    L = _library()
+    gx = _empty_rows(x) if want_x else None
+    gw = gb = work = None
+    need = 0
+    if want_params:
+        gw = torch.empty(dim, dtype=dtype, device=device)
+        gb = torch.empty_like(gw)
+        need = L.ersj_layer_norm_grad_work(n, dim)
+        if need:
+            work = torch.empty(need, dtype=torch.uint8, device=device)
+    _check(L.ersj_layer_norm_grad(grad.data_ptr(), _rows(grad, "grad")[1], x.data_ptr(), ldx, xt, n, dim,
+                                  mean.data_ptr(), rstd.data_ptr(), w, pt, gx.data_ptr() if want_x else None, dim,
+                                  gw.data_ptr() if want_params else None, gb.data_ptr() if want_params else None,
+                                  work.data_ptr() if need else None, need, _raw_stream(device.index)))
+    return gx, gw, gb
+
+
+def _norm_grad_args(grad, x, mean, rstd, weight, dtype, xt, device):
+    """(dim, type code and address of the weight, type of its gradient) of checked arguments."""
     shape = x.shape
     if grad.shape != shape:
         raise ValueError(f"grad has the shape {list(grad.shape)}, x {list(shape)}")
     _on(device, grad, "grad")
-    n, ldx = _rows(x if packed is None else x.codes, "x")
     dim = shape[-1]
     for what, t in (("mean", mean), ("rstd", rstd)):
         if t.dtype != torch.float32 or t.shape != shape[:-1] or not t.is_contiguous():
@@ -497,32 +517,32 @@ def layer_norm_grad(grad, x, mean, rstd, weight=None, dtype=None, want_x=True, w
             dtype = weight.dtype
         elif dtype != weight.dtype:
             raise TypeError("the gradients of weight and bias have the weight's type")
+    return dim, pt, w, dtype
+
+
+def _layer_norm_grad_packed(grad, x, mean, rstd, weight, dtype, want_x, want_params, stream):
+    xt = _TYPES[x.dtype]
+    if _type(grad, "grad") != xt:
+        raise TypeError("grad must have the type of x")
+    device = x.device
+    if _elsewhere(device, stream):
+        return _run_elsewhere(device, stream, (grad, x.codes, x.scales, mean, rstd, weight),
+                              lambda: layer_norm_grad(grad, x, mean, rstd, weight, dtype, want_x, want_params))
+    dim, pt, w, dtype = _norm_grad_args(grad, x, mean, rstd, weight, dtype, xt, device)
+    n = x.codes.numel() // dim
     L = _library()
-    gx = None
-    if want_x:
-        gx = _empty_rows(x) if packed is None else torch.empty(shape, dtype=x.dtype, device=device)
-    gw = gb = work = None
-    need = 0
+    gx = torch.empty(x.shape, dtype=x.dtype, device=device) if want_x else None
+    gw = gb = None
     if want_params:
         gw = torch.empty(dim, dtype=dtype, device=device)
         gb = torch.empty_like(gw)
-        need = L.ersj_layer_norm_grad_work(n, dim)
-    if packed is not None:
-        need = L.ersj_layer_norm_grad_packed_work(xt, n, dim)
-    if need:
-        work = torch.empty(need, dtype=torch.uint8, device=device)
-    if packed is not None:
-        _check(L.ersj_layer_norm_grad_packed(grad.data_ptr(), _rows(grad, "grad")[1], x.codes.data_ptr(),
-                                             x.scales.data_ptr(), xt, n, dim, mean.data_ptr(), rstd.data_ptr(), w, pt,
-                                             gx.data_ptr() if want_x else None, dim,
-                                             gw.data_ptr() if want_params else None,
-                                             gb.data_ptr() if want_params else None, work.data_ptr() if need else None,
-                                             need, _raw_stream(device.index)))
-        return gx, gw, gb
-    _check(L.ersj_layer_norm_grad(grad.data_ptr(), _rows(grad, "grad")[1], x.data_ptr(), ldx, xt, n, dim,
-                                  mean.data_ptr(), rstd.data_ptr(), w, pt, gx.data_ptr() if want_x else None, dim,
-                                  gw.data_ptr() if want_params else None, gb.data_ptr() if want_params else None,
-                                  work.data_ptr() if need else None, need, _raw_stream(device.index)))
+    need = L.ersj_layer_norm_grad_packed_work(xt, n, dim)
+    work = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    _check(L.ersj_layer_norm_grad_packed(grad.data_ptr(), _rows(grad, "grad")[1], x.codes.data_ptr(),
+                                         x.scales.data_ptr(), xt, n, dim, mean.data_ptr(), rstd.data_ptr(), w, pt,
+                                         gx.data_ptr() if want_x else None, dim, gw.data_ptr() if want_params else None,
+                                         gb.data_ptr() if want_params else None, work.data_ptr() if need else None,
+                                         need, _raw_stream(device.index)))
     return gx, gw, gb
 
 
