@@ -265,8 +265,8 @@ __device__ __forceinline__ float inverse(float v)
 
 // The normal distribution Phi(g) and its density phi(g).  FAST: the upper tail
 // of z = |g| is exp(-z^2/2) R(z), R as a polynomial in t = 1 / (1 + 0.32 z),
-// fitted to 1.4e-6 of the tail, which shares the density's exponential (erff:
-// 67M values of a block 374 us, 329 with this).
+// fitted to 1.4e-6 of the tail, which shares the density's exponential (65,536 x
+// 384 x 1024 bf16: forward 146 us, 181 with erff).
 template <bool FAST>
 __device__ __forceinline__ float normal(float g, float &density)
 {
