@@ -742,7 +742,7 @@ __global__ __launch_bounds__(256) void k_zero(O *out, int64_t ld, int m, int n)
 }
 
 // Sums of the parts of a product, in order, eight of them on their way at a
-// time.  (Only products of few tiles have parts: m n is below 2^23.)
+// time.  (Only products of few tiles have parts: m n is at most 2^24.)
 struct Parts {
     const float *part;
     int parts, m, n, all;  // all: of one or two results [m][n]
@@ -994,7 +994,25 @@ Tile sum_tile(int64_t m, int64_t n, int64_t slabs)
 int parts_of(int64_t m, int64_t n, int64_t slabs, Tile t)
 {
     if (t == kTile256) return 1;
-    int64_t parts = 512 / tiles_of(m, n, t);
+    const int64_t tiles = tiles_of(m, n, t);
+    if (t == kTile128 && tiles > 64 && tiles <= 1024) {
+        // the parts that come out even: turns of 512 workgroups by what each takes
+        // (900 ns a slab, three for the end), and joining (8 bytes a value and part).
+        // Both weights' gradient of 16,384 x 1280 x 3328 bf16, 520 tiles: 727 us in
+        // one part, 680 in three; of 65,536 x 768 x 2048, 192 tiles: 1051 us in the
+        // two that run at once, 1021 in five.
+        int best = 1;
+        int64_t least = 0;
+        for (int p = 1; p <= 8 && (p == 1 || p <= slabs / 4); ++p) {
+            const int64_t turns = (tiles * p + 511) / 512, ns = turns * ((slabs + p - 1) / p + 3) * 900;
+            const int64_t all = p == 1 ? ns : ns + p * m * n / 625 + 4000;
+            if (p > 1 && all * 20 > least * 19) continue;  // for less than a 20th it does not get more room
+            best = p;
+            least = all;
+        }
+        return best;
+    }
+    int64_t parts = 512 / tiles;
     if (parts > slabs / 4) parts = slabs / 4;
     return parts < 1 ? 1 : (int)parts;
 }

@@ -83,6 +83,13 @@ def test_gated_in_large_tiles(n, dim, hidden, kind):
 
 
 @pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("n,dim,hidden", [(9000, 1300, 3300), (9001, 1299, 3297), (9000, 770, 1030)])
+def test_gated_grad_in_more_parts_than_run_at_once(n, dim, hidden, kind):
+    x, wg, wu, dh = block(n, dim, hidden, TYPES[kind], 70)
+    check_gated_grad(ersj.gated_grad(dh, x, wg, wu, "silu"), dh, x, wg, wu, "silu")
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
 @pytest.mark.parametrize("dim", [1, 3, 7, 8, 15, 16, 31, 32, 33, 63, 64, 65, 100, 384, 385, 1001])
 def test_pack(dim, kind):
     for n, pad in ((1, 0), (7, 5), (300, 0), (333, 9)):
