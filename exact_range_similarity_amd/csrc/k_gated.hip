@@ -95,6 +95,10 @@ struct ProductArgs {
     int d_planes;         // of dg and du
     int n_pad;            // columns of dg and du that are written, zeros behind n
     int act;
+    // f16: parts of k_bounds, and where the factor of dg and du and its inverse go
+    const float *bounds;
+    int bound_parts;
+    float *factor;
 };
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -314,6 +318,92 @@ __device__ __forceinline__ float slope_of(int act, float g, float &value)
     return s + value * (1.f - s) * 2.f * k * (1.f + 3 * 0.044715f * g * g);
 }
 
+// The power of two by which f16 dg and du are multiplied.  As they are, a sum
+// over many rows would lose the terms below 6e-5 (1e-6 in grad_h: 4% of dW), and
+// one above 65,504 would be infinite.  |u| and |act(g)| are at most |x| |w| and
+// |act'| at most 1.13: 2^(14 - e) with 2^e the exponent of R W, R the largest of
+// max|grad_h| |x| over the rows and W of the weights' |w|, keeps all of them below
+// 1.13 * 2^15.  The bound is some sqrt(dim) above their size, which leaves twenty
+// binades of normal numbers below it.
+__device__ __forceinline__ float factor_of(float rows, float weights)
+{
+    const float bound = rows * weights;  // 2^-72 to 2^64, or 0
+    return bound > 0.f ? __uint_as_float((uint32_t)(127 + 14 + 127 - (int)(__float_as_uint(bound) >> 23)) << 23) : 1.f;
+}
+
+__device__ __forceinline__ float wave_most(float v)
+{
+#pragma unroll
+    for (int to = 32; to; to >>= 1) v = fmaxf(v, __shfl_xor(v, to));
+    return v;
+}
+
+__device__ __forceinline__ float wave_sum(float v)
+{
+#pragma unroll
+    for (int to = 32; to; to >>= 1) v += __shfl_xor(v, to);
+    return v;
+}
+
+constexpr int kBoundParts = 1024;  // most workgroups of k_bounds
+
+// R (blockIdx.y 0) and W (1) of factor_of over the rows of a workgroup's waves.
+// Rows whose bound is not finite are left out: what comes of them is not finite
+// whatever the factor.  20,000 x 384 x 1024: 57 MB, 13 us of the gradient's 159; one
+// token x 4096 x 11008, where the weights are read once more for it: 37 us of 148.
+struct BoundArgs {
+    const f16_t *gh;
+    int64_t ld_gh;
+    // as the products read them: whole pieces of 16 bytes, zeros behind dim
+    const f16_t *x, *gate, *up;
+    int64_t ld_x, ld_w;
+    int64_t n;
+    int pad, hidden;  // pad: columns of x and of the weights
+    float *part;      // [2][gridDim.x]
+};
+__global__ __launch_bounds__(256) void k_bounds(BoundArgs a)
+{
+    typedef Slot<f16_t, 8> S8;
+    __shared__ float of_wave[4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const bool weights = blockIdx.y;
+    const int64_t count = weights ? 2 * (int64_t)a.hidden : a.n;
+    float most = 0.f;
+    for (int64_t r = (int64_t)blockIdx.x * 4 + wave; r < count; r += (int64_t)gridDim.x * 4) {
+        const f16_t *row = !weights ? a.x + r * a.ld_x : r < a.hidden ? a.gate + r * a.ld_w : a.up + (r - a.hidden) * a.ld_w;
+        float square = 0.f;
+        for (int c = lane * 8; c < a.pad; c += 512) {
+            const auto v = *(const typename S8::vec *)(row + c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) square += (float)v[e] * (float)v[e];
+        }
+        float bound = sqrtf(wave_sum(square));
+        if (!weights) {
+            uint32_t top = 0;
+            const f16_t *gh = a.gh + r * a.ld_gh;
+            auto with = [&](f16_t v) {
+                const uint32_t b = bits16<f16_t>(v) & 0x7fffu;
+                top = b < 0x7c00u && b > top ? b : top;
+            };
+            for (int c = lane * 8; c < a.hidden; c += 512) {
+                if (c + 8 <= a.hidden) {
+                    const auto v = S8::load(gh + c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) with(v[e]);
+                } else {
+                    for (int e = c; e < a.hidden; ++e) with(gh[e]);
+                }
+            }
+            bound *= wave_most((float)__builtin_bit_cast(f16_t, (uint16_t)top));
+        }
+        if (bound < __builtin_inff()) most = fmaxf(most, bound);
+    }
+    if (lane == 0) of_wave[wave] = most;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        a.part[blockIdx.y * gridDim.x + blockIdx.x] = fmaxf(fmaxf(of_wave[0], of_wave[1]), fmaxf(of_wave[2], of_wave[3]));
+}
+
 // What a workgroup works on next: a tile of one of the outputs, over a part of k.
 struct Unit {
     int64_t m0;
@@ -330,6 +420,7 @@ __global__ __launch_bounds__(256, BM == 256 || kStages * BM > 256 ? 1 : 2) void 
     constexpr bool kPair = END != kStore;  // P's rows alternate between the two weights
     constexpr int CN = kPair ? BN / 2 : BN;
     constexpr bool FAST = sizeof(O) == 2;
+    constexpr bool kFactor = __is_same(O, f16_t) && END != kGate;  // dg and du come multiplied by a factor
     typedef Side<BN, PA, kPair> P;
     typedef Side<BM, QA, false> Q;
     constexpr int STAGE = P::kBytes + Q::kBytes;
@@ -363,6 +454,26 @@ __global__ __launch_bounds__(256, BM == 256 || kStages * BM > 256 ? 1 : 2) void 
         u.last = u.first + a.len < a.all ? u.first + a.len : a.all;
         return u;
     };
+
+    // of dg and du, or its inverse for what is summed of them
+    float factor = 1.f;
+    if constexpr (kFactor && END == kGateGrad) {
+        float most[2] = {0.f, 0.f};
+        for (int i = lane * 4; i < a.bound_parts; i += 256)
+#pragma unroll
+            for (int of = 0; of < 2; ++of) {
+                const f32x4 v = *(const f32x4 *)(a.bounds + of * a.bound_parts + i);
+                most[of] = fmaxf(most[of], fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])));
+            }
+        factor = factor_of(wave_most(most[0]), wave_most(most[1]));
+        if (blockIdx.x == 0 && threadIdx.x == 0) {
+            a.factor[0] = factor;
+            a.factor[1] = 1.f / factor;
+        }
+    } else if constexpr (kFactor) {
+        factor = a.factor[1];
+    }
+    if constexpr (kFactor) factor = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(factor)));
 
     // The loads run up to two slabs ahead of the products, across units: where
     // the next slab lies, how much of k it has, and how many more slabs follow it
@@ -592,7 +703,7 @@ __global__ __launch_bounds__(256, BM == 256 || kStages * BM > 256 ? 1 : 2) void 
                 for (int i = 0; i < NB; ++i)
 #pragma unroll
                     for (int j = 0; j < MB; ++j) {
-                        store32(j, i * 16, take(acc[i][j]));
+                        store32(j, i * 16, kFactor ? acc[i][j] * factor : take(acc[i][j]));
                         __builtin_amdgcn_sched_barrier(0);
                     }
             } else if constexpr (sizeof(O) == 2) {
@@ -600,8 +711,8 @@ __global__ __launch_bounds__(256, BM == 256 || kStages * BM > 256 ? 1 : 2) void 
                 for (int i = 0; i < NB; i += 2) {
 #pragma unroll
                     for (int j = 0; j < MB; ++j) {
-                        put(j, 0, acc[i][j]);
-                        put(j, 1, acc[i + 1][j]);
+                        put(j, 0, kFactor ? acc[i][j] * factor : acc[i][j]);
+                        put(j, 1, kFactor ? acc[i + 1][j] * factor : acc[i + 1][j]);
                     }
                     store((T *)a.out[u.which], a.ld_out[u.which], nw + i * 16, a.n);
                 }
@@ -648,6 +759,7 @@ __global__ __launch_bounds__(256, BM == 256 || kStages * BM > 256 ? 1 : 2) void 
                         for (int half = 0; half < 2; ++half) {
                             if constexpr (sizeof(O) == 2) {
                                 d[half] = __builtin_convertvector(*mine(j, half), f32x4);
+                                if constexpr (kFactor) d[half] *= factor;
                             } else {
                                 const int n = col + half * 16 + ln;
                                 const float *gh = (const float *)a.gh + m * a.ld_gh;
@@ -1050,6 +1162,8 @@ struct GradPlan {
     uint16_t *dg, *du;
     int64_t d_plane;
     int n_pad, outs, d_planes;
+    float *bounds, *factor;  // f16
+    int bound_parts;
     float *x_part, *w_part;
     int x_parts, w_parts;
     Tile x_tile, w_tile;
@@ -1059,7 +1173,7 @@ struct GradPlan {
 GradPlan plan(const GatedGradArgs &a)
 {
     Room room{(char *)a.work};
-    GradPlan f;
+    GradPlan f{};
     f.x = operand(room, a.x, a.type, a.n, a.dim, a.ld_x);
     weights(room, a.gate, a.ld_gate, a.up, a.ld_up, a.type, a.hidden, a.dim, f.gate, f.up);
     // dg and du as 16-bit values are a rounding more than the results' own, 1.4 times
@@ -1073,6 +1187,13 @@ GradPlan plan(const GatedGradArgs &a)
     f.d_plane = a.n * f.n_pad;
     f.dg = (uint16_t *)room.take((uint64_t)f.d_plane * 2 * planes);
     f.du = (uint16_t *)room.take((uint64_t)f.d_plane * 2 * planes);
+    if (a.type == kF16) {
+        // workgroups of k_bounds, four rows or more each, that the projections read 256 at a time
+        const int64_t most = a.n > 2 * (int64_t)a.hidden ? a.n : 2 * (int64_t)a.hidden;
+        f.bound_parts = most > 4 * (kBoundParts - 256) ? kBoundParts : (int)((most + 1023) / 1024) * 256;
+        f.bounds = (float *)room.take(2 * sizeof(float) * f.bound_parts);
+        f.factor = (float *)room.take(2 * sizeof(float));
+    }
     f.outs = (a.ggate != nullptr) + (a.gup != nullptr);
     const int64_t m = (int64_t)f.outs * a.hidden, slabs_x = (f.n_pad + kSlab - 1) / kSlab, slabs_w = (a.n + kSlab - 1) / kSlab;
     const int64_t all_x = slabs_x * 2 * (planes == 3 ? 6 : planes), all_w = slabs_w * (planes < 3 ? planes : a.x ? 6 : 3);
@@ -1181,7 +1302,16 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s)
                                a.type == kF16 ? kF16 : kBF16, f.x.ld, (int)f.x.ld};
             TRY_HIP(launch_unpack(u, s));
         }
+        if (a.type == kF16) {
+            const BoundArgs b{(const f16_t *)a.gh, a.ld_gh, (const f16_t *)f.x.p, (const f16_t *)f.gate.p,
+                              (const f16_t *)f.up.p, f.x.ld, f.gate.ld, a.n, pad8(a.dim), a.hidden, f.bounds};
+            k_bounds<<<dim3(f.bound_parts, 2), 256, 0, s>>>(b);
+            TRY_HIP(hipGetLastError());
+        }
         ProductArgs p = projections(f.gate, f.up, f.x, a.type, !a.x, a.n, a.dim, a.hidden, a.act);
+        p.bounds = f.bounds;
+        p.bound_parts = f.bound_parts;
+        p.factor = f.factor;
         p.gh = a.gh;
         p.ld_gh = a.ld_gh;
         p.dg = f.dg;
@@ -1211,6 +1341,7 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s)
         x.outs = 1;
         x.parts = f.x_parts;
         x.part = f.x_part;
+        x.factor = f.factor;
         x.m = (int)a.n;
         x.n = a.dim;
         x.n_room = pad8(a.dim);
@@ -1244,6 +1375,7 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s)
         w.outs = f.outs;
         w.parts = f.w_parts;
         w.part = f.w_part;
+        w.factor = f.factor;
         w.m = a.hidden;
         w.n = a.dim;
         w.n_room = pad8(a.dim);

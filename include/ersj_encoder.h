@@ -202,7 +202,10 @@ uint64_t ersj_gated_work(const void *d_x, int32_t type, int64_t n, int32_t dim, 
  *  d_work            : at least ersj_gated_grad_work(...) bytes, aligned to
  *                      256; want_*: whether that gradient is wanted.
  * dg and du are rounded to the 16-bit type that they are multiplied in (small
- * products: held in two parts of it, 32-bit tensors: in three).  Errors: INVALID_ARG, HIP.
+ * products: held in two parts of it, 32-bit tensors: in three).  In f16 they are
+ * held multiplied by a power of two that follows their size, so that values
+ * beyond the type's range, or below its normal numbers, only count as such in
+ * the results.  Errors: INVALID_ARG, HIP.
  */
 int ersj_gated_grad(const void *d_grad_h, int64_t ld_grad_h, const void *d_x, int64_t ld_x, const int8_t *d_codes,
                     const uint8_t *d_scales, int32_t type, int64_t n, int32_t dim, const void *d_gate, int64_t ld_gate,
