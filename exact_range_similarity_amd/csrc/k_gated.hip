@@ -315,7 +315,8 @@ __device__ __forceinline__ float slope_of(int act, float g, float &value)
     const float s = inverse<FAST>(1.f + exp_of<FAST>(act == 0 ? -g : -2.f * k * (g + 0.044715f * g * g * g)));
     value = g * s;
     if (act == 0) return s * (1.f + g * (1.f - s));
-    return s + value * (1.f - s) * 2.f * k * (1.f + 3 * 0.044715f * g * g);
+    // (beyond 64 s is 0 or 1, and g^2 may be infinite)
+    return s + value * (1.f - s) * 2.f * k * (1.f + 3 * 0.044715f * fminf(g * g, 4096.f));
 }
 
 // The power of two by which f16 dg and du are multiplied.  As they are, a sum
