@@ -267,16 +267,23 @@ __device__ __forceinline__ float inverse(float v)
     return FAST ? __builtin_amdgcn_rcpf(v) : 1.f / v;
 }
 
-// The normal distribution Phi(g) and its density phi(g).  FAST: the upper tail
-// of z = |g| is exp(-z^2/2) R(z), R as a polynomial in t = 1 / (1 + 0.32 z),
-// fitted to 1.4e-6 of the tail, which shares the density's exponential (65,536 x
-// 384 x 1024 bf16: forward 146 us, 181 with erff).
+// The normal distribution Phi(g) and its density phi(g), by the upper tail of
+// z = |g|, which keeps the bits of a small Phi.  FAST: the tail is exp(-z^2/2) R(z),
+// R as a polynomial in t = 1 / (1 + 0.32 z), fitted to 1.4e-6 of the tail, which
+// shares the density's exponential (65,536 x 384 x 1024 bf16: forward 146 us, 181
+// with erff).  Otherwise it is erfcf's, and what the rounding of z^2 leaves over
+// enters the exponential: off by some g^2 2^-24 of the tail, and not of 1.
 template <bool FAST>
 __device__ __forceinline__ float normal(float g, float &density)
 {
+    if constexpr (!FAST) {
+        const float z = fminf(fabsf(g), 64.f), square = z * z;
+        density = 0.39894228040143268f * expf(-0.5f * square) * (1.f - 0.5f * __builtin_fmaf(z, z, -square));
+        const float tail = 0.5f * erfcf(z * 0.70710678118654752f);
+        return g < 0.f ? tail : 1.f - tail;
+    }
     const float e = exp_of<FAST>(-0.5f * g * g);
     density = 0.39894228040143268f * e;
-    if constexpr (!FAST) return 0.5f * (1.f + erff(g * 0.70710678118654752f));
     const float z = fabsf(g), t = __builtin_amdgcn_rcpf(1.f + 0.32f * z);
     float r = 0.0323464572429657f;
     r = r * t + -0.11485423147678375f;

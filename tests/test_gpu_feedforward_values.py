@@ -1,10 +1,12 @@
 """The activations of the gated block and their derivatives where their parts
 overflow, underflow or cancel."""
+import math
+
 import pytest
 import torch
 
 import exact_range_similarity_amd as ersj
-from encoder_util import TYPES
+from encoder_util import F64, TYPES, U, close
 from feedforward_util import ACTIVATIONS
 from gpu_util import say
 
@@ -43,3 +45,18 @@ def test_far_out(kind, act):
         x, h, slope = through(sign * g, act, TYPES[kind])
         assert torch.equal(h.abs(), x if sign > 0 else torch.zeros_like(x))
         assert torch.equal(slope.abs(), torch.ones_like(x) if sign > 0 else torch.zeros_like(x))
+
+
+def test_gelu_keeps_the_bits_of_its_tail_in_32_bits():
+    # Phi(g) relative to itself: erfcf of a rounded argument z is off by 16 steps of its
+    # result, 32 u, and 2 z^2 = g^2 times the argument's 2 u; a few roundings follow.  The
+    # derivative Phi + g phi adds 12 u of g phi (expf, and the density's products).
+    g = torch.cat([torch.linspace(-12.5, 6, 60001, device=DEV), -torch.logspace(-6, 1, 2000, device=DEV)])
+    x, h, slope = through(g, "gelu", torch.float32)
+    x = x.to(F64)
+    phi = 0.5 * torch.erfc(-x / math.sqrt(2))
+    density = torch.exp(-0.5 * x * x) / math.sqrt(2 * math.pi)
+    rel = (36 + 2 * x * x) * U
+    close(h, x * phi, x.abs() * phi * (rel + 2 * U) + 2.0 ** -148, "gelu")
+    ref = phi + x * density
+    close(slope, ref, phi * rel + x.abs() * density * 12 * U + ref.abs() * 2 * U + 2.0 ** -148, "slope")
