@@ -989,7 +989,8 @@ struct Room {
 // In place where the loads can take it: 16-bit values, rows that begin at 16
 // bytes and hold whole pieces of 16 bytes, spaced so that a tile's offsets stay
 // below 2^31 bytes.
-Operand operand(Room &room, const void *p, int type, int64_t n, int dim, int64_t ld)
+// Otherwise laid out in `planes` of 16-bit values.
+Operand operand(Room &room, const void *p, int type, int64_t n, int dim, int64_t ld, int planes)
 {
     Operand o;
     if (p && type != kF32 && dim % 8 == 0 && ld % 8 == 0 && ((uintptr_t)p & 15) == 0 && ld < (1 << 22)) {
@@ -1001,7 +1002,7 @@ Operand operand(Room &room, const void *p, int type, int64_t n, int dim, int64_t
     o.laid = true;
     o.ld = pad;
     o.plane = n * pad;
-    o.p = (const uint16_t *)room.take((uint64_t)o.plane * 2 * (type == kF32 ? 3 : 1));
+    o.p = (const uint16_t *)room.take((uint64_t)o.plane * 2 * planes);
     return o;
 }
 
@@ -1141,12 +1142,13 @@ int parts_of(int64_t m, int64_t n, int64_t slabs, Tile t)
 void weights(Room &room, const void *gate, int64_t ld_gate, const void *up, int64_t ld_up, int type, int hidden, int dim,
              Operand &g, Operand &u)
 {
-    g = operand(room, gate, type, hidden, dim, ld_gate);
-    u = operand(room, up, type, hidden, dim, ld_up);
+    const int planes = type == kF32 ? 3 : 1;
+    g = operand(room, gate, type, hidden, dim, ld_gate, planes);
+    u = operand(room, up, type, hidden, dim, ld_up, planes);
     if (g.laid && u.laid) return;
     if (g.laid || u.laid || g.ld != u.ld) {
-        if (!g.laid) g = operand(room, nullptr, type, hidden, dim, 0);
-        if (!u.laid) u = operand(room, nullptr, type, hidden, dim, 0);
+        if (!g.laid) g = operand(room, nullptr, type, hidden, dim, 0, planes);
+        if (!u.laid) u = operand(room, nullptr, type, hidden, dim, 0, planes);
     }
 }
 
@@ -1159,7 +1161,7 @@ ForwardPlan plan(const GatedArgs &a)
 {
     Room room{(char *)a.work};
     ForwardPlan f;
-    f.x = operand(room, a.x, a.type, a.n, a.dim, a.ld_x);
+    f.x = operand(room, a.x, a.type, a.n, a.dim, a.ld_x, a.type == kF32 ? 3 : 1);
     weights(room, a.gate, a.ld_gate, a.up, a.ld_up, a.type, a.hidden, a.dim, f.gate, f.up);
     f.bytes = room.used;
     return f;
@@ -1182,7 +1184,8 @@ GradPlan plan(const GatedGradArgs &a)
 {
     Room room{(char *)a.work};
     GradPlan f{};
-    f.x = operand(room, a.x, a.type, a.n, a.dim, a.ld_x);
+    // what a code stands for is a bf16 number (in f16 rows an f16 one): one plane
+    f.x = operand(room, a.x, a.type, a.n, a.dim, a.ld_x, a.type == kF32 && a.x ? 3 : 1);
     weights(room, a.gate, a.ld_gate, a.up, a.ld_up, a.type, a.hidden, a.dim, f.gate, f.up);
     // dg and du as 16-bit values are a rounding more than the results' own, 1.4 times
     // its error; in small products, which other things bound, they have a second
@@ -1305,7 +1308,6 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s)
         layer.add(f.up, a.up, a.hidden, a.dim, a.ld_up);
         TRY_HIP(layer.run(a.type, s));
         if (!a.x) {
-            // what a code stands for is a bf16 number: 32-bit rows have one plane
             const UnpackArgs u{a.codes, a.scales, a.n, a.dim, const_cast<uint16_t *>(f.x.p),
                                a.type == kF16 ? kF16 : kBF16, f.x.ld, (int)f.x.ld};
             TRY_HIP(launch_unpack(u, s));
