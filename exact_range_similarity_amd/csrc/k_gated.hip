@@ -92,7 +92,7 @@ struct ProductArgs {
     int64_t ld_gh;
     uint16_t *dg, *du;
     int64_t d_plane, ld_d;
-    int d_planes;         // of dg and du
+    int d_planes;         // of dg and du; 16 bits: 1 or 2, 1 in tiles of 256
     int n_pad;            // columns of dg and du that are written, zeros behind n
     int act;
     // f16: parts of k_bounds, and where the factor of dg and du and its inverse go
@@ -1176,7 +1176,7 @@ struct GradPlan {
     int bound_parts;
     float *x_part, *w_part;
     int x_parts, w_parts;
-    Tile x_tile, w_tile;
+    Tile h_tile, x_tile, w_tile;
     uint64_t bytes;
 };
 
@@ -1190,9 +1190,12 @@ GradPlan plan(const GatedGradArgs &a)
     // dg and du as 16-bit values are a rounding more than the results' own, 1.4 times
     // its error; in small products, which other things bound, they have a second
     // plane for what the first leaves over (9 x 384 x 1024 bf16: 28 us either way;
-    // 1 x 4096 x 11008, where the weights are read twice for it: 117 us and 151)
-    const int64_t weight = (int64_t)a.dim * a.hidden;
-    f.d_planes = a.type == kF32 ? 3 : a.n * weight <= (int64_t)1 << 27 && weight <= 1 << 23 ? 2 : 1;
+    // 1 x 4096 x 11008, where the weights are read twice for it: 117 us and 151).  The
+    // projections' large tile writes one.
+    const int64_t weight = (int64_t)a.dim * a.hidden, slabs_h = (pad8(a.dim) + kSlab - 1) / kSlab;
+    f.h_tile = projection_tile(a.n, 2 * (int64_t)a.hidden, slabs_h * (a.type != kF32 ? 1 : a.x ? 6 : 3));
+    const bool two = f.h_tile != kTile256 && a.n * weight <= (int64_t)1 << 27 && weight <= 1 << 23;
+    f.d_planes = a.type == kF32 ? 3 : two ? 2 : 1;
     const int planes = f.d_planes;
     f.n_pad = pad8(a.hidden);
     f.d_plane = a.n * f.n_pad;
@@ -1330,7 +1333,7 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s)
         p.ld_d = f.n_pad;
         p.d_planes = f.d_planes;
         p.n_pad = f.n_pad;
-        TRY_HIP((product<false, false, kGateGrad>(p, a.type, projection_tile(a.n, 2 * (int64_t)a.hidden, (int64_t)p.products * ((p.k + kSlab - 1) / kSlab)), s)));
+        TRY_HIP((product<false, false, kGateGrad>(p, a.type, f.h_tile, s)));
     }
     Joiner joiner;
     if (a.gx && a.n) {
