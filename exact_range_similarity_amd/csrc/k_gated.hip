@@ -110,7 +110,10 @@ constexpr uint32_t kOutside = 0x80000000u;
 // 16 bytes from each lane's place in a buffer to LDS, lane by lane from `lds`.
 __device__ __forceinline__ void dma16(uint32_t lds, u32x4 buffer, uint32_t off)
 {
-    // the wait state that a write of m0 needs before it is used
+    // s_nop: the wait state that a write of m0 needs before it is used.  m0 is a
+    // reserved register: the compiler keeps nothing in it from one instruction to
+    // another and takes it in no list of clobbered ones (none of this file's code
+    // uses it but these lines).
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
                  : "s"(lds), "v"(off), "s"(buffer)
