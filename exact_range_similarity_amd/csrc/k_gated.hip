@@ -1081,31 +1081,44 @@ int64_t tiles_of(int64_t m, int64_t n, Tile t) { return ((m + edge_of(t) - 1) / 
 
 // Whether m x n results of `slabs` slabs each are formed in tiles of 256 x 256:
 // where every compute unit gets one and the sum is long enough.  They read less,
-// but two workgroups of 128 x 128 overlap one's end with the other's products
-// (65,536 x 384 x 1024 bf16, 6 slabs: 130 us with 128, 204 with 256; 8192 x 4096 x
-// 11008, 64 slabs: 1494 and 1261), and wide tiles may lie half outside (dx of the
-// former, 384 columns, 32 slabs: 121 us with 128, 132 with 256).
+// but two workgroups of 128 x 128 overlap one's end with the other's products, and
+// wide tiles may lie half outside (dx of 65,536 x 384 x 1024, 384 columns: 121 us with
+// 128, 132 with 256).  Forward of 16,384 x 64 slabs x 4096 bf16, in us with 128 and 256:
+// 6 slabs 124, 142; 12 210, 214; 16 271, 260; 24 389, 352; 32 507, 443; 64 977, 823.
+// dx of 16,384 x 4096 x (32 a slab): 24 slabs 424, 428; 32 506, 477; 64 1011, 910.
 bool large_tiles(int64_t m, int64_t n, int64_t slabs)
 {
     const int64_t large = tiles_of(m, n, kTile256);
     return slabs >= 24 && large >= 256 && large * 20 <= tiles_of(m, n, kTile128) * 6;
 }
 
-// Otherwise, for the projections, whose sums cannot be
-// cut: 128 x 128 with four slabs on their way where there is one for a compute
-// unit (1999 x 385 x 1001 f32, 42 slabs: 42 us, two slabs 48), 64 x 64 where
-// there are fewer (300 x 1000 x 1000 f32: 41 us, 63 with the larger; 9 x 4096 x
-// 11008 bf16: 34 us, 5.3 TB/s of weights, and 45).
+// Otherwise, for the projections, whose sums cannot be cut: 64 x 64 where all such
+// tiles run at once, 512 of them, else 128 x 128, with four slabs on their way
+// where there is one for a compute unit (and two slabs where there are more and
+// two share a unit).  In us, tiles of 64, of 128 with four slabs and with two:
+//   1 x 4096 x 11008 bf16, 344 of 64:      33.5  35.2  43.0   (180 MB: 5.4 TB/s)
+//   64 x 4096 x 11008, 344:                35.6  35.9  51.1
+//   128 x 4096 x 11008, 688:               45.4  36.9  53.5
+//   200 x 4096 x 4096, 512:                30.2  35.6  43.8
+//   200 x 2048 x 5632, 704:                24.4  21.0  24.9
+//   600 x 768 x 3000, 940:                 15.6  12.3  11.4
+//   1000 x 1000 x 1000 f32, 512:           65.2  67.8  86.7
+//   1100 x 1000 x 1000 f32, 576:           88.8  70.3  89.0
+//   1999 x 385 x 1001 f32, 1024:           57.5  42.6  47.0
+//   64 x 4096 x 11008 f32, 344:             424   405   529   (the other way)
+//   3000 x 768 x 1024 f32, 384 of 128:    115.6  98.2  78.2
 Tile projection_tile(int64_t m, int64_t n, int64_t slabs)
 {
     if (large_tiles(m, n, slabs)) return kTile256;
-    const int64_t tiles = tiles_of(m, n, kTile128);
-    return tiles > 256 ? kTile128 : tiles > 100 && slabs >= 16 ? kTile128Deep : kTile64;
+    if (tiles_of(m, n, kTile128) > 256) return kTile128;
+    return tiles_of(m, n, kTile64) <= 512 ? kTile64 : kTile128Deep;
 }
 
-// Other sums are cut into parts; small products do better in small tiles (dx of
-// 2000 x 384 x 1024 bf16, 1536 tiles times slabs: 18 us, 23 in tiles of 128; of
-// 1999 x 385 x 1001 f32, 12,288: 54 and 40).
+// Other sums are cut into parts; small products do better in small tiles, by
+// tiles of 128 times slabs (the gradient with dx alone, in us in tiles of 64 and of
+// 128; 768: 1000 x 384 x 1024 bf16, 22.6 and 24.5; 4096: 500 x 1024 x 4096 bf16,
+// 40.3 and 40.4; 4608: 1000 x 384 x 1024 f32, 67.4 and 63.5; 6048: 8000 x 384 x 1024
+// bf16, 53.5 and 48.9; 9216: 2000 x 384 x 1024 f32, 94.4 and 75.6).
 Tile sum_tile(int64_t m, int64_t n, int64_t slabs)
 {
     if (large_tiles(m, n, slabs)) return kTile256;
@@ -1192,9 +1205,10 @@ GradPlan plan(const GatedGradArgs &a)
     weights(room, a.gate, a.ld_gate, a.up, a.ld_up, a.type, a.hidden, a.dim, f.gate, f.up);
     // dg and du as 16-bit values are a rounding more than the results' own, 1.4 times
     // its error; in small products, which other things bound, they have a second
-    // plane for what the first leaves over (9 x 384 x 1024 bf16: 28 us either way;
-    // 1 x 4096 x 11008, where the weights are read twice for it: 117 us and 151).  The
-    // projections' large tile writes one.
+    // plane for what the first leaves over.  One plane and two, in us, bf16: 9 x 384 x
+    // 1024 28 and 28, 300 x 384 x 1024 28 and 30, 16 x 2048 x 4096 37 and 45 (the most
+    // that it costs here); beyond, 2000 x 384 x 1024 43 and 60, 1 x 4096 x 11008, where the
+    // weights are read twice for it, 109 and 143.  The projections' large tile writes one.
     const int64_t weight = (int64_t)a.dim * a.hidden, slabs_h = (pad8(a.dim) + kSlab - 1) / kSlab;
     f.h_tile = projection_tile(a.n, 2 * (int64_t)a.hidden, slabs_h * (a.type != kF32 ? 1 : a.x ? 6 : 3));
     const bool two = f.h_tile != kTile256 && a.n * weight <= (int64_t)1 << 27 && weight <= 1 << 23;
