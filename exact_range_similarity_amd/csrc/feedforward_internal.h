@@ -1,5 +1,5 @@
 // Internal declarations of the feed-forward operators
-// (include/ersj_feedforward.h): rows held in 8 bits and the gated block.
+// (include/ersj_encoder.h): rows held in 8 bits and the gated block.
 #pragma once
 
 #include "encoder_internal.h"

@@ -18,12 +18,12 @@
 // operand is the one along the results' rows in memory: a lane then holds four
 // neighbours of a row.
 //
-// 8192 x 4096 x 11008 bf16: forward 1.16 ms (1.27 PFLOP/s), gradient 3.6 ms (1.22),
-// bound by the matrix units at the clock that the power allows (2.0 GHz, half of
+// 8192 x 4096 x 11008 bf16: forward 1.13 ms (1.31 PFLOP/s), gradient 3.6 ms (1.22),
+// bound by the matrix units at the clock that the power allows (2.0 GHz, 58% of
 // their cycles busy, as in the library's product of this size, 1.25 PFLOP/s).
-// 65,536 x 384 x 1024: forward 143 us, where a tile's end (activation, 134 MB of
+// 65,536 x 384 x 1024: forward 145 us, where a tile's end (activation, 134 MB of
 // results) and the fetch of its six slabs weigh as much as its products.  Few rows
-// are bound by the weights: 1 x 4096 x 11008, 180 MB, 37 us, 4.9 TB/s.
+// are bound by the weights: 1 x 4096 x 11008, 180 MB, 33 us, 5.4 TB/s.
 //
 // 32-bit tensors are split into three bf16 parts, x = x1 + x2 + x3, each the
 // rounded rest of those before (8 bits each: nothing is left of 24), and the six
@@ -74,7 +74,9 @@ struct ProductArgs {
     // P: along the results' rows (n), Q: across them (m); planes of 16-bit values
     const uint16_t *p[2], *q[2];
     int64_t p_plane, q_plane, ld_p, ld_q;
-    int k;                // of one product, a multiple of 8 where an operand lies along it
+    // of one product.  Of an operand along k whole pieces of 8 values are read: behind
+    // k its rows go on to the next multiple of 8, with zeros or values that meet zeros
+    int k;
     int products;         // of planes
     uint32_t p_planes, q_planes;
     int sources;          // pairs (p[i], q[i]) summed, 1 or 2
@@ -991,8 +993,8 @@ struct Room {
 
 // In place where the loads can take it: 16-bit values, rows that begin at 16
 // bytes and hold whole pieces of 16 bytes, spaced so that a tile's offsets stay
-// below 2^31 bytes.
-// Otherwise laid out in `planes` of 16-bit values.
+// below 2^31 bytes.  Otherwise laid out in `planes` of 16-bit values, with zeros
+// behind dim to the next multiple of 8.
 Operand operand(Room &room, const void *p, int type, int64_t n, int dim, int64_t ld, int planes)
 {
     Operand o;
@@ -1363,7 +1365,7 @@ hipError_t launch_gated_grad(const GatedGradArgs &a, hipStream_t s)
         x.ld_q = f.n_pad;
         x.p_plane = f.gate.plane;
         x.q_plane = f.d_plane;
-        x.k = a.hidden;
+        x.k = a.hidden;  // dg and du have zeros behind it, to n_pad; the weights' rows end with it
         x.products = a.type == kF32 ? 6 : f.d_planes;
         x.p_planes = a.type == kF32 ? kPlanes6P : 0;
         x.q_planes = a.type == kF32 ? kPlanes6Q : f.d_planes == 2 ? kPlanes2 : 0;

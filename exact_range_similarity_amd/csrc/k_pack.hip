@@ -3,10 +3,13 @@
 // number of them nearest to it.  A power of two makes every step exact (scaling,
 // the value that a code stands for, also as a 16-bit number), so nothing but
 // the one rounding to a whole number is lost: at most half of 2^e, less than
-// 1/127 of the largest.  Both kernels are bound by memory: 1M x 384 bf16, 1.16 GB
-// each way, 217 to 250 us to codes and 220 to 234 us back, 4.7 to 5.3 TB/s where
-// a large copy has 5.2.  Hence items of 16 values, which make the codes' accesses
-// 16 bytes wide, and four of them on their way in every thread.
+// 1/127 of the largest (but for the ends of the scales: with a type's largest,
+// 64 steps are held as 63, up to a whole 2^e off, 1/64 of the largest; with the
+// least, 2^-126, runs whose largest is below 63.5 steps are off by half a step).
+// Both kernels are bound by memory: 1M x 384 bf16, 1.16 GB each way, 217 to 250
+// us to codes and 220 to 234 us back, 4.7 to 5.3 TB/s where a large copy has
+// 5.2.  Hence items of 16 values, which make the codes' accesses 16 bytes wide,
+// and four of them on their way in every thread.
 #include "feedforward_internal.h"
 
 namespace ersj {

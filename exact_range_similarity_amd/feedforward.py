@@ -41,7 +41,8 @@ def gated(x, w_gate, w_up, activation="silu", pack=False, out=None, stream=None)
     ``w_gate``, ``w_up``: [hidden, dim], of x's type.  ``activation``: "silu",
     "gelu" (with the normal distribution itself) or "gelu_tanh".  Differentiable
     with respect to x and both weights (``gated_grad``); the backward pass keeps
-    x alone, with ``pack`` in 8 bits (``PackedRows``)."""
+    x alone, with ``pack`` in 8 bits (``PackedRows``).  In float32 an infinity
+    among the inputs counts as NaN."""
     if (x.requires_grad or w_gate.requires_grad or w_up.requires_grad) and torch.is_grad_enabled():
         if out is not None:
             raise ValueError("out cannot be given where a gradient is wanted")
@@ -79,7 +80,10 @@ def _gated(x, w_gate, w_up, activation, out, stream):
 def gated_grad(grad, x, w_gate, w_up, activation="silu", want_x=True, want_gate=True, want_up=True, stream=None):
     """``ersj_gated_grad``: (grad of x, of w_gate, of w_up) from ``grad``, the
     gradient of ``gated``'s result.  ``x``: the rows, or ``PackedRows`` of them.
-    What is not wanted comes back as None."""
+    What is not wanted comes back as None.  The gradients of both projections are
+    rounded to the 16-bit type that they are multiplied in (in small products held
+    to twice its bits, in float32 to all): 16-bit results of large products are off
+    by 1.4 times what their own rounding makes."""
     packed = type(x) is PackedRows
     xt = _TYPES[x.dtype] if packed else _type(x, "x")
     if _type(grad, "grad") != xt:

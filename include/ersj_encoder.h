@@ -27,8 +27,9 @@
  *    looked for among the tensors of a set of gradients alone.
  *  - The same inputs give the same bits on every call: sums are taken in a
  *    fixed order.  It depends on the sizes and element types; for the gradient
- *    of a table on the ids as well; for the global norm on where each tensor
- *    lies, modulo 128 bytes.
+ *    of a table on the ids as well; for the gradient of the gated block on which
+ *    results are wanted; for the global norm on where each tensor lies, modulo
+ *    128 bytes.
  */
 #ifndef ERSJ_ENCODER_H
 #define ERSJ_ENCODER_H
@@ -139,7 +140,9 @@ uint64_t ersj_layer_norm_grad_work(int64_t n, int32_t dim);
  *  d_scales : device [n][(dim + ERSJ_PACK_BLOCK - 1) / ERSJ_PACK_BLOCK],
  *             e + 127, and 255 for a block that stands for NaN.
  * Codes and scales are to be unpacked with the type that they were packed
- * with.  Errors: INVALID_ARG, HIP.
+ * with.  A value is off by at most 2^(e - 1), less than 1/127 of its block's
+ * largest; but by up to 2^e where a code of 64 was made 63, and where e is -126
+ * the largest may itself be a few steps or none.  Errors: INVALID_ARG, HIP.
  */
 #define ERSJ_PACK_BLOCK 32
 int ersj_pack_rows(const void *d_x, int32_t type, int64_t n, int32_t dim, int64_t ld_x, int8_t *d_codes,
@@ -201,8 +204,10 @@ uint64_t ersj_gated_work(const void *d_x, int32_t type, int64_t n, int32_t dim, 
  *                      The three's spacings are below 2^21.
  *  d_work            : at least ersj_gated_grad_work(...) bytes, aligned to
  *                      256; want_*: whether that gradient is wanted.
- * dg and du are rounded to the 16-bit type that they are multiplied in (small
- * products: held in two parts of it, 32-bit tensors: in three).  In f16 they are
+ * dg and du are rounded to the 16-bit type that they are multiplied in, which
+ * makes the error of 16-bit results 1.4 times that of their own rounding (with
+ * n * dim * hidden <= 2^27 and dim * hidden <= 2^23 they are held in two parts
+ * of it, in 32-bit tensors in three: no such error).  In f16 they are
  * held multiplied by a power of two that follows their size, so that values
  * beyond the type's range, or below its normal numbers, only count as such in
  * the results.  Errors: INVALID_ARG, HIP.
