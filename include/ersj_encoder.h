@@ -207,10 +207,11 @@ uint64_t ersj_gated_work(const void *d_x, int32_t type, int64_t n, int32_t dim, 
  * dg and du are rounded to the 16-bit type that they are multiplied in, which
  * makes the error of 16-bit results 1.4 times that of their own rounding (with
  * n * dim * hidden <= 2^27 and dim * hidden <= 2^23 they are held in two parts
- * of it, in 32-bit tensors in three: no such error).  In f16 they are
- * held multiplied by a power of two that follows their size, so that values
- * beyond the type's range, or below its normal numbers, only count as such in
- * the results.  Errors: INVALID_ARG, HIP.
+ * of it, in 32-bit tensors in three: no such error).  In f16 they are held
+ * multiplied by a power of two, so that none is beyond the type's range and, where
+ * they are below its normal numbers, off by at most 2^-39 of B, the largest of
+ * max|grad_h| |x| over the rows times the largest |w| over both weights' rows
+ * (euclidean; what is not finite is left out).  Errors: INVALID_ARG, HIP.
  */
 int ersj_gated_grad(const void *d_grad_h, int64_t ld_grad_h, const void *d_x, int64_t ld_x, const int8_t *d_codes,
                     const uint8_t *d_scales, int32_t type, int64_t n, int32_t dim, const void *d_gate, int64_t ld_gate,
